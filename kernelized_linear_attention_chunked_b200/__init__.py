@@ -37,3 +37,10 @@ from ._binding import (  # noqa: F401
     test_bounds_check,
     test_forced_timeout,
 )
+from ._delta import (  # noqa: F401
+    delta_backward,
+    delta_backward_workspace_bytes,
+    delta_decode_step,
+    delta_prefill,
+    delta_prefill_workspace_bytes,
+)

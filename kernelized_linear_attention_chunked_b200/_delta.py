@@ -1,0 +1,165 @@
+"""ctypes binding of the gated delta rule (include/kata_delta.h).
+
+Argument marshalling only, like _binding.py. Tensors are checked for type,
+shape, device and contiguity here, because the C ABI sees plain pointers.
+Outputs and workspaces that are not given are allocated on the call's stream.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes as C
+
+import torch
+
+from . import _binding as kb
+from ._binding import KataError, _check, _dt, _ptr, _workspace
+
+_vp, _i, _f, _sz = C.c_void_p, C.c_int, C.c_float, C.c_size_t
+
+# name -> (restype, argtypes), mirroring include/kata_delta.h
+SIGNATURES = {
+    "kata_delta_prefill_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
+    "kata_delta_prefill": (_i, [_vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _f, _vp, _vp, _vp,
+                                _vp, _sz, _vp]),
+    "kata_delta_decode_step": (_i, [_vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _f, _vp, _vp, _vp]),
+    "kata_delta_backward_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
+    "kata_delta_backward": (_i, [_vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _f, _vp, _vp, _vp,
+                                 _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+}
+
+_bound = None
+
+
+def lib() -> C.CDLL:
+    """libkata.so with this header's entry points; raises if it has not been built."""
+    global _bound
+    if _bound is None:
+        handle = kb.lib()
+        for name, (res, args) in SIGNATURES.items():
+            fn = getattr(handle, name)
+            fn.restype = res
+            fn.argtypes = args
+        _bound = handle
+    return _bound
+
+
+def want(name: str, t, shape, dtype, like: torch.Tensor) -> None:
+    """Raise unless t (None passes) is a contiguous tensor of this shape and
+    type on like's device."""
+    if t is None:
+        return
+    if not t.is_cuda or not t.is_contiguous():
+        raise KataError("tensors must be contiguous CUDA tensors")
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != like.device:
+        raise KataError(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device}, expected "
+                        f"{tuple(shape)} {dtype} on {like.device}")
+
+
+@contextlib.contextmanager
+def on_stream(t: torch.Tensor, stream):
+    """Runs a call on t's device and on `stream` (default: that device's current
+    one), and gives the stream's handle."""
+    with contextlib.ExitStack() as stack:
+        if t.device.index != torch.cuda.current_device():
+            stack.enter_context(torch.cuda.device(t.device))
+        if stream is not None:
+            if stream.device != t.device:
+                raise KataError(f"stream of {stream.device}, tensors on {t.device}")
+            stack.enter_context(torch.cuda.stream(stream))
+        yield torch.cuda.current_stream().cuda_stream
+
+
+def _inputs(q, k, v, g, beta, ndim):
+    if q.dim() != ndim:
+        raise KataError(f"q has {q.dim()} dimensions, expected {ndim}")
+    dt = _dt(q)
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        want(name, t, q.shape, q.dtype, q)
+    for name, t in (("g", g), ("beta", beta)):
+        want(name, t, q.shape[:-1], torch.float32, q)
+    return dt
+
+
+def delta_prefill_workspace_bytes(B, H, T, d, dtype) -> int:
+    return int(lib().kata_delta_prefill_workspace_bytes(B, H, T, d, kb._DTYPE[dtype]))
+
+
+def delta_prefill(q, k, v, g, beta, scale: float | None = None, S_in=None, state: bool = True,
+                  output: bool = True, o=None, S_out=None, workspace=None, stream=None):
+    """The gated delta rule over q, k, v [B, H, T, d] with log decays g and
+    writing strengths beta [B, H, T] (fp32), from the state S_in [B, H, d, d]
+    (fp32, None: zero). ``scale`` defaults to d**-0.5. Returns (o, S): o in q's
+    dtype, None when ``output`` is False; the last state, None when ``state``
+    is False."""
+    dt = _inputs(q, k, v, g, beta, 4)
+    B, H, T, d = q.shape
+    st = (B, H, d, d)
+    want("S_in", S_in, st, torch.float32, q)
+    want("S_out", S_out, st, torch.float32, q)
+    want("o", o, q.shape, q.dtype, q)
+    scale = d ** -0.5 if scale is None else scale
+    L = lib()
+    with on_stream(q, stream) as s:
+        if output and o is None:
+            o = torch.empty_like(q)
+        if state and S_out is None:
+            S_out = torch.empty(st, dtype=torch.float32, device=q.device)
+        if workspace is None:
+            workspace = _workspace(L.kata_delta_prefill_workspace_bytes(B, H, T, d, dt), q.device)
+        _check("kata_delta_prefill", L.kata_delta_prefill(
+            _ptr(q), _ptr(k), _ptr(v), dt, _ptr(g), _ptr(beta), B, H, T, d, scale, _ptr(S_in),
+            _ptr(o), _ptr(S_out), _ptr(workspace), workspace.numel() * workspace.element_size(), s))
+    return o, S_out
+
+
+def delta_decode_step(q, k, v, g, beta, S, scale: float | None = None, o=None, stream=None):
+    """One token of the gated delta rule: q, k, v [B, H, d], g and beta [B, H]
+    (fp32), the state S [B, H, d, d] (fp32) updated in place. Returns o in q's
+    dtype."""
+    dt = _inputs(q, k, v, g, beta, 3)
+    B, H, d = q.shape
+    if S is None:
+        raise KataError("S must not be None")
+    want("S", S, (B, H, d, d), torch.float32, q)
+    want("o", o, q.shape, q.dtype, q)
+    scale = d ** -0.5 if scale is None else scale
+    with on_stream(q, stream) as s:
+        if o is None:
+            o = torch.empty_like(q)
+        _check("kata_delta_decode_step", lib().kata_delta_decode_step(
+            _ptr(q), _ptr(k), _ptr(v), dt, _ptr(g), _ptr(beta), B, H, d, scale, _ptr(S), _ptr(o),
+            s))
+    return o
+
+
+def delta_backward_workspace_bytes(B, H, T, d, dtype) -> int:
+    return int(lib().kata_delta_backward_workspace_bytes(B, H, T, d, kb._DTYPE[dtype]))
+
+
+def delta_backward(q, k, v, g, beta, do, scale: float | None = None, S_in=None, dS=None,
+                   state_grad: bool = False, workspace=None, stream=None):
+    """Gradients of delta_prefill for the gradient ``do`` of its output and
+    ``dS`` [B, H, d, d] (fp32, None: zero) of its last state. Returns (dq, dk,
+    dv, dg, dbeta, dS_in): the first three in q's dtype, the rest fp32; dS_in,
+    the gradient of the first state, is None unless ``state_grad``."""
+    dt = _inputs(q, k, v, g, beta, 4)
+    B, H, T, d = q.shape
+    st = (B, H, d, d)
+    if do is None:
+        raise KataError("do must not be None")
+    want("do", do, q.shape, q.dtype, q)
+    want("S_in", S_in, st, torch.float32, q)
+    want("dS", dS, st, torch.float32, q)
+    scale = d ** -0.5 if scale is None else scale
+    L = lib()
+    with on_stream(q, stream) as s:
+        dq, dk, dv = (torch.empty_like(q) for _ in range(3))
+        dg, db = torch.empty_like(g), torch.empty_like(beta)
+        dS_in = torch.empty(st, dtype=torch.float32, device=q.device) if state_grad else None
+        if workspace is None:
+            workspace = _workspace(L.kata_delta_backward_workspace_bytes(B, H, T, d, dt), q.device)
+        _check("kata_delta_backward", L.kata_delta_backward(
+            _ptr(q), _ptr(k), _ptr(v), dt, _ptr(g), _ptr(beta), B, H, T, d, scale, _ptr(S_in),
+            _ptr(do), _ptr(dS), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), _ptr(db), _ptr(dS_in),
+            _ptr(workspace), workspace.numel() * workspace.element_size(), s))
+    return dq, dk, dv, dg, db, dS_in

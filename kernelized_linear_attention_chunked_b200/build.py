@@ -40,7 +40,7 @@ def sources() -> list[Path]:
 
 def _compile(src: Path, extra: list[str], build_dir: Path) -> Path:
     obj = build_dir / (src.stem + ".o")
-    deps = [src] + list(CSRC.glob("*.cuh")) + list(CSRC.glob("*.h")) + [ROOT / "include" / "kata.h"]
+    deps = [src] + list(CSRC.glob("*.cuh")) + list(CSRC.glob("*.h")) + list((ROOT / "include").glob("*.h"))
     if obj.exists() and obj.stat().st_mtime > max(p.stat().st_mtime for p in deps):
         return obj
     cmd = [nvcc()] + NVCC_FLAGS + extra + ["-c", str(src), "-o", str(obj)]

@@ -1,0 +1,670 @@
+// The chunked form of the gated delta rule, shared by the prefill (delta.cu)
+// and the gradients (delta_backward.cu).
+//
+// Per (batch, head), with the state S [d, d] (key rows, value columns):
+//     e_t = v_t - exp(g_t) S_{t-1}^T k_t,
+//     S_t = exp(g_t) S_{t-1} + beta_t k_t e_t^T,      o_t = scale S_t^T q_t.
+// Over a chunk of C = 64 tokens, with G_i = g_1 + .. + g_i, a_i = exp(G_i),
+// D_ij = exp(G_i - G_j) and the chunk's first state S0:
+//     E = V - diag(a) K S0 - N diag(beta) E,  N = tril(K K^T, -1) * D
+//       = X V - X diag(a) K S0,               X = (1 + N diag(beta))^-1
+//     O = scale (diag(a) Q S0 + M diag(beta) E),          M = tril(Q K^T) * D
+//     S_C = a_C S0 + K^T diag(beta c) E,                  c_j = exp(G_C - G_j).
+// Every exponent is a sum of log decays from an earlier token to a later one,
+// so nothing overflows where g <= 0. G is summed and subtracted in 64 bits (a
+// difference of two large sums keeps its digits after a strong decay), and a
+// g below -200 counts as -200: exp of it is 0 in fp32 either way, and a g of
+// minus infinity (the state starts anew) does not make inf - inf.
+//
+// Two launches. delta_prep: one CTA per (chunk, head), everything that needs
+// no state (W = X diag(a) K, XV, M). delta_chain: one CTA per (head, slice of
+// value columns) walks the chunks; columns of the state are independent, so
+// the slices never meet. Its two products per chunk, E = XV - W S0 and
+// S_C = .. + K^T (..E), are the serial part, so the inverse is applied to K
+// and V beforehand: that leaves one product between a state and its error
+// instead of two.
+//
+// The gradients run the same chain backwards (REV below): with dS the gradient
+// of the chunk's last state,
+//     Z = X^T diag(beta) (scale M^T dO + diag(c) K dS)
+//     dS0 = a_C dS + scale Q^T diag(a) dO - K^T diag(a) Z,
+// which has the same shape: Z = Z0 + W' dS with W' = X^T diag(beta c) K and
+// Z0 = scale X^T diag(beta) M^T dO.
+//
+// All products keep fp32 accuracy by split tf32 operands (mma_tf32.cuh): the
+// state, its gradient, dg and dbeta are fp32 results. Only o of bf16 inputs,
+// rounded to bf16 at the end, takes the one-part form.
+#pragma once
+
+#include <atomic>
+
+#include "kata_common.cuh"
+#include "kata_internal.h"
+#include "mma_tf32.cuh"
+
+namespace kata {
+namespace delta {
+
+constexpr int kC = 64;    // tokens per chunk
+constexpr int kTS = 72;   // row stride of a 64 x 64 fp32 tile in shared memory
+constexpr int kCoef = 256;  // floats of coefficients per chunk: a' [64], c' [64], a_C
+constexpr float kMinLog = -200.f;
+
+// Row stride of a [64, D] tile in shared memory: rows start four 32-bit banks
+// apart (eight for fp32), so a K-major fragment load has no bank conflict.
+template <int D>
+constexpr int row_stride() {
+    return D + 8;
+}
+
+// Per-chunk scratch. "Fragment order" of a [64, n] matrix: the 16 x 8
+// accumulator tiles row block by row block, each as 32 lanes x float4, so that
+// a tile moves with one coalesced 128-bit access per lane.
+struct Scratch {
+    float *W;     // [chunks][64 D], fragment order
+    float *Y;     // [chunks][64 D], fragment order: XV, or Z0
+    float *M;     // [chunks][64 * 64], fragment order: scale M diag(beta)
+    float *coef;  // [chunks][kCoef]
+};
+
+struct Args {
+    const void *q, *k, *v, *d_o;
+    const float *g, *beta;
+    const float *S_in;  // first state (REV: gradient of the last one); NULL = zero
+    float *S_out;       // last state (REV: gradient of the first one); NULL: not written
+    void *o;
+    float *keepY;       // [chunks][64][D]: E (REV: Z)
+    float *keepS;       // [chunks][D][D]: each chunk's first state (REV: gradient of its last)
+    int T, nc;
+    float scale;
+};
+
+__device__ __forceinline__ void cp16(void *dst, const void *src, bool have) {
+    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+    const int n = have ? 16 : 0;  // 0: sixteen zero bytes, nothing is read
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(n)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Rows [t0, t0 + ROWS) of the [nrows, D] matrix that starts at row `row0`, columns [c0, c0 + N), to
+// a tile with row stride `stride`; rows from nrows on become zero.
+template <typename T, int N, int ROWS = kC>
+__device__ __forceinline__ void load_tile(T *dst, int stride, const T *src, size_t row0, int t0,
+                                          int nrows, int D, int c0, int tid, int nthreads) {
+    constexpr int PER = 16 / sizeof(T);
+    constexpr int CH = N / PER;
+    for (int i = tid; i < ROWS * CH; i += nthreads) {
+        const int r = i / CH, c = (i % CH) * PER;
+        const bool have = t0 + r < nrows;
+        const T *s = src + (row0 + (have ? t0 + r : 0)) * (size_t)D + c0 + c;
+        cp16(dst + r * stride + c, s, have);
+    }
+}
+
+// The running sums of one chunk's log decays, by one warp: G[64] (64 bits).
+__device__ __forceinline__ void cumulate(const float *g, size_t row0, int t0, int T, double *G) {
+    const int lane = threadIdx.x & 31;
+    double x[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int t = t0 + 2 * lane + i;
+        float v = t < T ? g[row0 + t] : 0.f;
+        v = v < kMinLog ? kMinLog : v;
+        x[i] = v;
+    }
+    x[1] += x[0];
+    double sum = x[1];
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const double up = __shfl_up_sync(0xffffffffu, sum, off);
+        if (lane >= off) sum += up;
+    }
+    G[2 * lane] = sum - x[1] + x[0];
+    G[2 * lane + 1] = sum;
+}
+
+// sX = (1 + A)^-1 for the strictly lower triangular A (64 x 64, both with row
+// stride kTS), by four warps. Diagonal 16 x 16 blocks by forward substitution,
+// one column per lane; then the blocks below them, 16 to 32 to 64 rows, by
+//     X21 = -X22 (A21 X11),
+// where a warp's own columns need no other warp's. The blocks above the
+// diagonal hold the intermediate products and are not part of the result.
+__device__ __forceinline__ void invert(const float *sA, float *sX, int warp, int lane) {
+    using namespace tf;
+    const int g = lane >> 2, t2 = 2 * (lane & 3);
+    {
+        const int j = lane & 15;
+        const float *A = sA + 16 * warp * kTS + 16 * warp;
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float s = i == j ? 1.f : 0.f;
+#pragma unroll
+            for (int m = 0; m < i; ++m) s = fmaf(-A[i * kTS + m], x[m], s);
+            x[i] = s;
+        }
+        if (lane < 16) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sX[(16 * warp + i) * kTS + 16 * warp + j] = x[i];
+        }
+    }
+    __syncthreads();
+    {  // blocks (1, 0) and (3, 2): warp w takes eight columns of pair w / 2
+        const int r0 = 32 * (warp >> 1), c = r0 + 8 * (warp & 1);
+        float acc[1][4];
+        clear(acc);
+        gemm<2, 2, 1>(
+            acc, 0, 2, [&](int m, int k) { return pair<true>(sA + (r0 + 16) * kTS + r0, kTS, m, k); },
+            [&](int n, int k) { return pair<false>(sX + r0 * kTS + c, kTS, n, k); });
+        float *P = sX + r0 * kTS + c + 16;
+        *reinterpret_cast<float2 *>(P + g * kTS + t2) = make_float2(acc[0][0], acc[0][1]);
+        *reinterpret_cast<float2 *>(P + (g + 8) * kTS + t2) = make_float2(acc[0][2], acc[0][3]);
+        __syncwarp();
+        clear(acc);
+        gemm<2, 2, 1>(
+            acc, 0, 2,
+            [&](int m, int k) { return pair<true>(sX + (r0 + 16) * kTS + r0 + 16, kTS, m, k); },
+            [&](int n, int k) { return pair<false>(P, kTS, n, k); });
+        float *O = sX + (r0 + 16) * kTS + c;
+        *reinterpret_cast<float2 *>(O + g * kTS + t2) = make_float2(-acc[0][0], -acc[0][1]);
+        *reinterpret_cast<float2 *>(O + (g + 8) * kTS + t2) = make_float2(-acc[0][2], -acc[0][3]);
+    }
+    __syncthreads();
+    {  // the lower left 32 x 32 block: warp w takes its columns 8 w .. 8 w + 7
+        const int c = 8 * warp;
+        float *P = sX + 32 + c;
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+            float acc[1][4];
+            clear(acc);
+            gemm<2, 2, 1>(  // X11's rows above its diagonal blocks hold no values
+                acc, warp >= 2 ? 2 : 0, 4,
+                [&](int m, int k) { return pair<true>(sA + (32 + 16 * mt) * kTS, kTS, m, k); },
+                [&](int n, int k) { return pair<false>(sX + c, kTS, n, k); });
+            *reinterpret_cast<float2 *>(P + (16 * mt + g) * kTS + t2) =
+                make_float2(acc[0][0], acc[0][1]);
+            *reinterpret_cast<float2 *>(P + (16 * mt + g + 8) * kTS + t2) =
+                make_float2(acc[0][2], acc[0][3]);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+            float acc[1][4];
+            clear(acc);
+            gemm<2, 2, 1>(
+                acc, 0, 2 * (mt + 1),
+                [&](int m, int k) { return pair<true>(sX + (32 + 16 * mt) * kTS + 32, kTS, m, k); },
+                [&](int n, int k) { return pair<false>(P, kTS, n, k); });
+            float *O = sX + (32 + 16 * mt) * kTS + c;
+            *reinterpret_cast<float2 *>(O + g * kTS + t2) = make_float2(-acc[0][0], -acc[0][1]);
+            *reinterpret_cast<float2 *>(O + (g + 8) * kTS + t2) =
+                make_float2(-acc[0][2], -acc[0][3]);
+        }
+    }
+    __syncthreads();
+}
+
+template <typename Tin, int D, bool BACK>
+struct PrepSmem {
+    static constexpr int KS = row_stride<D>();
+    static constexpr int IN = kC * KS * (int)sizeof(Tin);
+    static constexpr int P = kC * KS * 4;  // BACK: diag(beta) M^T dO, over V
+    static constexpr int K = 0, Q = IN, V = 2 * IN, DO = V + (BACK ? P : IN);
+    static constexpr int A = DO + (BACK ? IN : 0);
+    static constexpr int X = A + kC * kTS * 4, M = X + kC * kTS * 4;
+    static constexpr int G = M + (BACK ? kC * kTS * 4 : 0);
+    static constexpr int COEF = G + kC * 8;  // beta, a, c
+    static constexpr int BYTES = COEF + 3 * kC * 4;
+};
+
+template <int D>
+__device__ __forceinline__ void store_frags(float *dst, const float (&acc)[D / 8][4], int warp,
+                                            int lane) {
+    float4 *d = reinterpret_cast<float4 *>(dst) + (size_t)warp * (D / 8) * 32 + lane;
+#pragma unroll
+    for (int nt = 0; nt < D / 8; ++nt)
+        d[nt * 32] = make_float4(acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]);
+}
+
+// What each chunk needs of itself alone; 4 warps, warp w = rows 16 w .. 16 w + 15.
+// f: the forward chain's operands; r: the reverse chain's (BACK only).
+template <typename Tin, int D, bool BACK>
+__global__ void __launch_bounds__(128) delta_prep(Args p, Scratch f, Scratch r) {
+    using namespace tf;
+    using L = PrepSmem<Tin, D, BACK>;
+    constexpr int KS = L::KS, TI = Parts<Tin>::N;
+    extern __shared__ __align__(16) uint8_t sm[];
+    Tin *sK = reinterpret_cast<Tin *>(sm + L::K), *sQ = reinterpret_cast<Tin *>(sm + L::Q);
+    Tin *sV = reinterpret_cast<Tin *>(sm + L::V), *sO = reinterpret_cast<Tin *>(sm + L::DO);
+    float *sA = reinterpret_cast<float *>(sm + L::A), *sX = reinterpret_cast<float *>(sm + L::X);
+    float *sM = reinterpret_cast<float *>(sm + L::M), *sP = reinterpret_cast<float *>(sm + L::V);
+    double *G = reinterpret_cast<double *>(sm + L::G);
+    float *beta = reinterpret_cast<float *>(sm + L::COEF), *ca = beta + kC, *cc = ca + kC;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int gr = lane >> 2, t2 = 2 * (lane & 3);
+    const size_t ch = blockIdx.x;  // head * nc + chunk
+    const size_t head = ch / p.nc;
+    const int t0 = (int)(ch % p.nc) * kC;
+    const size_t row0 = head * (size_t)p.T;
+
+    load_tile<Tin, D>(sK, KS, static_cast<const Tin *>(p.k), row0, t0, p.T, D, 0, tid, 128);
+    if (BACK || p.o)
+        load_tile<Tin, D>(sQ, KS, static_cast<const Tin *>(p.q), row0, t0, p.T, D, 0, tid, 128);
+    load_tile<Tin, D>(sV, KS, static_cast<const Tin *>(p.v), row0, t0, p.T, D, 0, tid, 128);
+    if (BACK)
+        load_tile<Tin, D>(sO, KS, static_cast<const Tin *>(p.d_o), row0, t0, p.T, D, 0, tid, 128);
+    cp_commit();
+    if (warp == 0) cumulate(p.g, row0, t0, p.T, G);
+    if (tid >= 64) {
+        const int t = t0 + tid - 64;
+        beta[tid - 64] = t < p.T ? p.beta[row0 + t] : 0.f;
+    }
+    cp_wait_all();
+    __syncthreads();
+    if (tid < kC) {
+        const float a = expf((float)G[tid]), c = expf((float)(G[kC - 1] - G[tid]));
+        ca[tid] = a;
+        cc[tid] = c;
+        float *cf = f.coef + ch * kCoef;
+        cf[tid] = p.scale * a;
+        cf[kC + tid] = beta[tid] * c;
+        if (tid == kC - 1) cf[2 * kC] = a;
+        if (BACK) {
+            float *cr = r.coef + ch * kCoef;
+            cr[tid] = p.scale * a;
+            cr[kC + tid] = -a;
+            if (tid == kC - 1) cr[2 * kC] = a;
+        }
+    }
+    __syncthreads();
+
+    const int m0 = 16 * warp, nt_end = 2 * (warp + 1);  // column tiles up to the diagonal block
+    float kk[8][4], qk[8][4];
+    clear(kk);
+    clear(qk);
+    gemm<TI, TI, 8>(
+        kk, 0, D / 8, [&](int m, int k) { return pair<true>(sK + m0 * KS, KS, m, k); },
+        [&](int n, int k) { return pair<true>(sK, KS, n, k); }, nt_end);
+    if (BACK || p.o)
+        gemm<TI, TI, 8>(
+            qk, 0, D / 8, [&](int m, int k) { return pair<true>(sQ + m0 * KS, KS, m, k); },
+            [&](int n, int k) { return pair<true>(sK, KS, n, k); }, nt_end);
+#pragma unroll
+    for (int nt = 0; nt < 8; ++nt) {
+        if (nt >= nt_end) continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int i = m0 + gr + (e & 2 ? 8 : 0), j = 8 * nt + t2 + (e & 1);
+            const float dec = i >= j ? expf((float)(G[i] - G[j])) : 0.f;
+            sA[i * kTS + j] = i > j ? kk[nt][e] * dec * beta[j] : 0.f;
+            qk[nt][e] = i >= j ? qk[nt][e] * dec : 0.f;
+            if (BACK)
+                sM[i * kTS + j] = qk[nt][e];
+            else
+                qk[nt][e] *= p.scale * beta[j];
+        }
+    }
+    if (!BACK && p.o) {
+        float4 *d = reinterpret_cast<float4 *>(f.M + ch * (kC * kC)) + (size_t)warp * 8 * 32 + lane;
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt)
+            if (nt < nt_end) d[nt * 32] = make_float4(qk[nt][0], qk[nt][1], qk[nt][2], qk[nt][3]);
+    }
+    __syncthreads();
+    invert(sA, sX, warp, lane);
+
+    float acc[D / 8][4];
+    clear(acc);
+    gemm<2, TI, D / 8>(  // X V
+        acc, 0, nt_end, [&](int m, int k) { return pair<true>(sX + m0 * kTS, kTS, m, k); },
+        [&](int n, int k) { return pair<false>(sV, KS, n, k); });
+    store_frags<D>(f.Y + ch * (kC * D), acc, warp, lane);
+    clear(acc);
+    gemm<2, TI, D / 8>(  // X diag(a) K
+        acc, 0, nt_end,
+        [&](int m, int k) {
+            const float2 x = pair<true>(sX + m0 * kTS, kTS, m, k);
+            return make_float2(x.x * ca[k], x.y * ca[k + 1]);
+        },
+        [&](int n, int k) { return pair<false>(sK, KS, n, k); });
+    store_frags<D>(f.W + ch * (kC * D), acc, warp, lane);
+    if (!BACK) return;
+
+    // Z0 = X^T (scale diag(beta) M^T dO), W' = X^T diag(beta c) K: the
+    // transposed factors reach from a row's own block to the last one
+    clear(acc);
+    gemm<2, TI, D / 8>(
+        acc, 2 * warp, 8, [&](int m, int k) { return pair<false>(sM + m0, kTS, m, k); },
+        [&](int n, int k) { return pair<false>(sO, KS, n, k); });
+    __syncthreads();  // every warp has read V
+    {
+        const float s0 = p.scale * beta[m0 + gr], s1 = p.scale * beta[m0 + gr + 8];
+#pragma unroll
+        for (int nt = 0; nt < D / 8; ++nt) {
+            *reinterpret_cast<float2 *>(sP + (m0 + gr) * KS + 8 * nt + t2) =
+                make_float2(s0 * acc[nt][0], s0 * acc[nt][1]);
+            *reinterpret_cast<float2 *>(sP + (m0 + gr + 8) * KS + 8 * nt + t2) =
+                make_float2(s1 * acc[nt][2], s1 * acc[nt][3]);
+        }
+    }
+    __syncthreads();
+    clear(acc);
+    gemm<2, 2, D / 8>(
+        acc, 2 * warp, 8, [&](int m, int k) { return pair<false>(sX + m0, kTS, m, k); },
+        [&](int n, int k) { return pair<false>(sP, KS, n, k); });
+    store_frags<D>(r.Y + ch * (kC * D), acc, warp, lane);
+    clear(acc);
+    gemm<2, TI, D / 8>(
+        acc, 2 * warp, 8,
+        [&](int m, int k) {
+            const float2 x = pair<false>(sX + m0, kTS, m, k);
+            return make_float2(x.x * (beta[k] * cc[k]), x.y * (beta[k + 1] * cc[k + 1]));
+        },
+        [&](int n, int k) { return pair<false>(sK, KS, n, k); });
+    store_frags<D>(r.W + ch * (kC * D), acc, warp, lane);
+}
+
+template <typename Tin, int D, int NS, bool REV>
+struct ChainSmem {
+    static constexpr int KS = row_stride<D>();
+    static constexpr int ST = NS + 4;  // B operands' row stride: rows 2t start 8 t (24 t) banks on
+    static constexpr int DS = NS + 8;  // row stride of the dO slice
+    static constexpr int IN = kC * KS * (int)sizeof(Tin);
+    static constexpr int S = 0, Y = S + D * ST * 4, YC = Y + kC * ST * 4;
+    static constexpr int GQ = YC + kC * ST * 4;  // REV: Q^T diag(scale a) dO
+    static constexpr int STAGE = GQ + (REV ? D * ST * 4 : 0);
+    // one stage: K, Q, coefficients, (REV) the dO slice
+    static constexpr int K = 0, Q = IN, COEF = 2 * IN, DO = COEF + kCoef * 4;
+    static constexpr int STAGE_BYTES = DO + (REV ? kC * DS * (int)sizeof(Tin) : 0);
+    static constexpr int BYTES = STAGE + 2 * STAGE_BYTES;
+};
+
+// The walk over the chunks, one CTA per (head, NS value columns). Warps 0-3
+// carry the chain: they hold the state in registers (fp32, D / 4 rows each)
+// and take two dependent products per chunk. Warps 4-7 take the products that
+// hang off it: the outputs (forward) or Q^T dO (REV). K and Q arrive by
+// asynchronous copies one chunk ahead; W, XV and M come straight from global
+// memory into the fragments that use them, also ahead.
+template <typename Tin, int D, int NS, bool REV, bool KEEP>
+__global__ void __launch_bounds__(256) delta_chain(Args p, Scratch w) {
+    using namespace tf;
+    using L = ChainSmem<Tin, D, NS, REV>;
+    constexpr int KS = L::KS, ST = L::ST, NT = NS / 8, TI = Parts<Tin>::N;
+    constexpr int MT = D >= 64 ? D / 64 : 1;  // 16-row tiles of the state per chain warp
+    extern __shared__ __align__(16) uint8_t sm[];
+    float *sS = reinterpret_cast<float *>(sm + L::S), *sY = reinterpret_cast<float *>(sm + L::Y);
+    float *sYc = reinterpret_cast<float *>(sm + L::YC), *sG = reinterpret_cast<float *>(sm + L::GQ);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int gr = lane >> 2, t2 = 2 * (lane & 3);
+    const size_t head = blockIdx.x / (D / NS);
+    const int slice = blockIdx.x % (D / NS), c0 = slice * NS;
+    const size_t row0 = head * (size_t)p.T;
+    const bool chain = warp < 4;
+    const int m0 = 16 * (warp & 3);
+    const bool wantO = !REV && p.o != nullptr;
+
+    auto stage = [&](int i) { return sm + L::STAGE + (i & 1) * L::STAGE_BYTES; };
+    auto chunk_of = [&](int i) { return REV ? p.nc - 1 - i : i; };
+    auto prefetch = [&](int i) {
+        uint8_t *s = stage(i);
+        const int c = chunk_of(i);
+        load_tile<Tin, D>(reinterpret_cast<Tin *>(s + L::K), KS, static_cast<const Tin *>(p.k), row0,
+                          c * kC, p.T, D, 0, tid, 256);
+        if (REV || wantO)
+            load_tile<Tin, D>(reinterpret_cast<Tin *>(s + L::Q), KS, static_cast<const Tin *>(p.q),
+                              row0, c * kC, p.T, D, 0, tid, 256);
+        if (REV)
+            load_tile<Tin, NS>(reinterpret_cast<Tin *>(s + L::DO), L::DS,
+                               static_cast<const Tin *>(p.d_o), row0, c * kC, p.T, D, c0, tid, 256);
+        const float *cf = w.coef + (head * p.nc + c) * kCoef;
+        if (tid < kCoef / 4) cp16(s + L::COEF + tid * 16, cf + tid * 4, true);
+        cp_commit();
+    };
+
+    // the state in accumulator layout: rows 16 (MT warp + mt) + gr (+ 8), columns 8 nt + t2 (+ 1)
+    float S[MT][NT][4];
+    const bool owns = chain && (D >= 64 || warp < D / 16);
+    auto srow = [&](int mt) { return 16 * (MT * warp + mt) + gr; };
+    if (owns) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float2 x = make_float2(0.f, 0.f);
+                    const int r = srow(mt) + 8 * h;
+                    if (p.S_in)
+                        x = *reinterpret_cast<const float2 *>(p.S_in + (head * D + r) * D + c0 +
+                                                              8 * nt + t2);
+                    S[mt][nt][2 * h] = x.x;
+                    S[mt][nt][2 * h + 1] = x.y;
+                    *reinterpret_cast<float2 *>(sS + r * ST + 8 * nt + t2) = x;
+                }
+    }
+    float4 W[D / 8], Y0[NT];
+    auto load_w = [&](int i) {
+        const size_t ch = head * p.nc + chunk_of(i);
+        const float4 *s = reinterpret_cast<const float4 *>(w.W + ch * (kC * D)) +
+                          (size_t)(warp & 3) * (D / 8) * 32 + lane;
+        const float4 *y = reinterpret_cast<const float4 *>(w.Y + ch * (kC * D)) +
+                          (size_t)((warp & 3) * (D / 8) + slice * NT) * 32 + lane;
+#pragma unroll
+        for (int kt = 0; kt < D / 8; ++kt) W[kt] = s[kt * 32];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) Y0[nt] = y[nt * 32];
+    };
+    prefetch(0);
+    if (chain) load_w(0);
+    cp_wait_all();
+    __syncthreads();
+
+    for (int i = 0; i < p.nc; ++i) {
+        const int c = chunk_of(i);
+        const size_t ch = head * p.nc + c;
+        const uint8_t *st = stage(i);
+        const Tin *sK = reinterpret_cast<const Tin *>(st + L::K);
+        const Tin *sQ = reinterpret_cast<const Tin *>(st + L::Q);
+        const Tin *sO = reinterpret_cast<const Tin *>(st + L::DO);
+        const float *coef = reinterpret_cast<const float *>(st + L::COEF);
+        if (i + 1 < p.nc) prefetch(i + 1);
+        float o[NT][4];
+        float4 M[8];
+        if (chain) {
+            // E = XV - W S0 (REV: Z = Z0 + W' dS)
+            float acc[NT][4];
+            clear(acc);
+#pragma unroll
+            for (int kt = 0; kt < D / 8; ++kt) {
+                FragA<2> a;
+                a.set(make_float2(W[kt].x, W[kt].y), make_float2(W[kt].z, W[kt].w));
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    mma_step<2, 2>(acc[nt], a, pair<false>(sS, ST, 8 * nt + gr, 8 * kt + t2));
+            }
+            const float k0 = coef[kC + m0 + gr], k1 = coef[kC + m0 + gr + 8];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float sg = REV ? 1.f : -1.f;
+                const float2 y0 = make_float2(fmaf(sg, acc[nt][0], Y0[nt].x),
+                                              fmaf(sg, acc[nt][1], Y0[nt].y));
+                const float2 y1 = make_float2(fmaf(sg, acc[nt][2], Y0[nt].z),
+                                              fmaf(sg, acc[nt][3], Y0[nt].w));
+                const int n = 8 * nt + t2;
+                if (wantO) {
+                    *reinterpret_cast<float2 *>(sY + (m0 + gr) * ST + n) = y0;
+                    *reinterpret_cast<float2 *>(sY + (m0 + gr + 8) * ST + n) = y1;
+                }
+                *reinterpret_cast<float2 *>(sYc + (m0 + gr) * ST + n) =
+                    make_float2(k0 * y0.x, k0 * y0.y);
+                *reinterpret_cast<float2 *>(sYc + (m0 + gr + 8) * ST + n) =
+                    make_float2(k1 * y1.x, k1 * y1.y);
+                if (KEEP) {
+                    float *d = p.keepY + (ch * kC + m0 + gr) * D + c0 + n;
+                    *reinterpret_cast<float2 *>(d) = y0;
+                    *reinterpret_cast<float2 *>(d + 8 * D) = y1;
+                }
+            }
+            if (KEEP && owns) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float *d = p.keepS + (ch * D + srow(mt)) * D + c0 + 8 * nt + t2;
+                        *reinterpret_cast<float2 *>(d) = make_float2(S[mt][nt][0], S[mt][nt][1]);
+                        *reinterpret_cast<float2 *>(d + 8 * D) =
+                            make_float2(S[mt][nt][2], S[mt][nt][3]);
+                    }
+            }
+            if (i + 1 < p.nc) load_w(i + 1);
+        } else if (wantO) {
+            const float4 *s = reinterpret_cast<const float4 *>(w.M + ch * (kC * kC)) +
+                              (size_t)(warp & 3) * 8 * 32 + lane;
+#pragma unroll
+            for (int kt = 0; kt < 8; ++kt)
+                if (kt < 2 * ((warp & 3) + 1)) M[kt] = s[kt * 32];
+            clear(o);
+            gemm<TI, TI, NT>(
+                o, 0, D / 8, [&](int m, int k) { return pair<true>(sQ + m0 * KS, KS, m, k); },
+                [&](int n, int k) { return pair<false>(sS, ST, n, k); });
+            const float s0 = coef[m0 + gr], s1 = coef[m0 + gr + 8];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                o[nt][0] *= s0;
+                o[nt][1] *= s0;
+                o[nt][2] *= s1;
+                o[nt][3] *= s1;
+            }
+        } else if (REV) {
+            for (int mt = warp & 3; mt < D / 16; mt += 4) {
+                float acc[NT][4];
+                clear(acc);
+                gemm<TI, 2, NT>(
+                    acc, 0, kC / 8, [&](int m, int k) { return pair<false>(sQ + 16 * mt, KS, m, k); },
+                    [&](int n, int k) {
+                        const float2 x = pair<false>(sO, L::DS, n, k);
+                        return make_float2(x.x * coef[k], x.y * coef[k + 1]);
+                    });
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float *d = sG + (16 * mt + gr) * ST + 8 * nt + t2;
+                    *reinterpret_cast<float2 *>(d) = make_float2(acc[nt][0], acc[nt][1]);
+                    *reinterpret_cast<float2 *>(d + 8 * ST) = make_float2(acc[nt][2], acc[nt][3]);
+                }
+            }
+        }
+        __syncthreads();
+        if (owns) {
+            // S = a_C S + K^T (c' Y) (REV: + Q^T dO): the chunk's share is summed
+            // by itself, then added, so that rounding does not grow with the chunks
+            const float aC = coef[2 * kC];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                float acc[NT][4];
+                clear(acc);
+                const int r0 = 16 * (MT * warp + mt);
+                gemm<TI, 2, NT>(
+                    acc, 0, kC / 8, [&](int m, int k) { return pair<false>(sK + r0, KS, m, k); },
+                    [&](int n, int k) { return pair<false>(sYc, ST, n, k); });
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float *d = sS + srow(mt) * ST + 8 * nt + t2;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float x = fmaf(aC, S[mt][nt][e], acc[nt][e]);
+                        if (REV) x += sG[(srow(mt) + (e & 2 ? 8 : 0)) * ST + 8 * nt + t2 + (e & 1)];
+                        S[mt][nt][e] = x;
+                    }
+                    *reinterpret_cast<float2 *>(d) = make_float2(S[mt][nt][0], S[mt][nt][1]);
+                    *reinterpret_cast<float2 *>(d + 8 * ST) = make_float2(S[mt][nt][2], S[mt][nt][3]);
+                }
+            }
+        } else if (!chain && wantO) {
+#pragma unroll
+            for (int kt = 0; kt < 8; ++kt) {
+                if (kt >= 2 * ((warp & 3) + 1)) continue;
+                FragA<TI> a;
+                a.set(make_float2(M[kt].x, M[kt].y), make_float2(M[kt].z, M[kt].w));
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    mma_step<TI, TI>(o[nt], a, pair<false>(sY, ST, 8 * nt + gr, 8 * kt + t2));
+            }
+            Tin *od = static_cast<Tin *>(p.o);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int t = c * kC + m0 + gr + 8 * h;
+                if (t >= p.T) continue;
+                Tin *d = od + (row0 + t) * (size_t)D + c0 + t2;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    if constexpr (sizeof(Tin) == 2)
+                        *reinterpret_cast<__nv_bfloat162 *>(d + 8 * nt) =
+                            __floats2bfloat162_rn(o[nt][2 * h], o[nt][2 * h + 1]);
+                    else
+                        *reinterpret_cast<float2 *>(d + 8 * nt) =
+                            make_float2(o[nt][2 * h], o[nt][2 * h + 1]);
+                }
+            }
+        }
+        cp_wait_all();
+        __syncthreads();
+    }
+    if (owns && p.S_out) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float *d = p.S_out + (head * D + srow(mt)) * D + c0 + 8 * nt + t2;
+                *reinterpret_cast<float2 *>(d) = make_float2(S[mt][nt][0], S[mt][nt][1]);
+                *reinterpret_cast<float2 *>(d + 8 * D) = make_float2(S[mt][nt][2], S[mt][nt][3]);
+            }
+    }
+}
+
+// Kernels with over 48 KB of dynamic shared memory need their limit raised,
+// once per device (the attribute is the current device's).
+template <auto Kern>
+inline cudaError_t raise_smem(int bytes) {
+    static std::atomic<unsigned long long> done{0};  // one bit per device ordinal < 64
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+    if (bit && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && bit) done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
+
+template <typename Tin, int D, bool BACK>
+cudaError_t launch_prep(const Args &p, const Scratch &f, const Scratch &r, long heads,
+                        cudaStream_t stream) {
+    constexpr int bytes = PrepSmem<Tin, D, BACK>::BYTES;
+    static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
+    cudaError_t e = raise_smem<delta_prep<Tin, D, BACK>>(bytes);
+    if (e != cudaSuccess) return e;
+    delta_prep<Tin, D, BACK><<<(unsigned)(heads * p.nc), 128, bytes, stream>>>(p, f, r);
+    return after_launch();
+}
+
+template <typename Tin, int D, int NS, bool REV, bool KEEP>
+cudaError_t launch_chain_ns(const Args &p, const Scratch &w, long heads, cudaStream_t stream) {
+    constexpr int bytes = ChainSmem<Tin, D, NS, REV>::BYTES;
+    static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
+    cudaError_t e = raise_smem<delta_chain<Tin, D, NS, REV, KEEP>>(bytes);
+    if (e != cudaSuccess) return e;
+    delta_chain<Tin, D, NS, REV, KEEP><<<(unsigned)(heads * (D / NS)), 256, bytes, stream>>>(p, w);
+    return after_launch();
+}
+
+template <typename Tin, int D, bool REV, bool KEEP>
+cudaError_t launch_chain(const Args &p, const Scratch &w, long heads, cudaStream_t stream) {
+    return launch_chain_ns<Tin, D, 16, REV, KEEP>(p, w, heads, stream);
+}
+
+inline int chunks_of(int T) { return (T + kC - 1) / kC; }
+
+}  // namespace delta
+}  // namespace kata

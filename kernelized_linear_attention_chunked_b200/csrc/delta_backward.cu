@@ -1,0 +1,369 @@
+// Gradients of the gated delta rule's chunked prefill.
+//
+// With the chunk's quantities as in delta.cuh, U = diag(beta) E, dO the
+// gradient of O and dS that of the chunk's last state:
+//     dU = scale M^T dO + diag(c) K dS,    Z = X^T diag(beta) dU,
+//     F  = dU - N^T Z  (so that Z = diag(beta) F)
+//     dV = Z,   dbeta_i = E_i . F_i,
+//     PM = scale tril(dO U^T) * D,   PN = -tril(Z U^T, -1) * D
+//     dQ = PM K + scale diag(a) dO S0^T
+//     dK = R + L,  R = PN K - diag(a) Z S0^T              (k_i as the reader)
+//                  L = PM^T Q + PN^T K + diag(c) U dS^T   (k_j as the written key)
+// and for the running sums G of the log decays, since each term carries
+// exp(G_i - G_j) with i the reading and j the written token,
+//     dG_i = q_i . dQ_i + k_i . R_i - k_i . L_i,
+//     dg_t = sum_{i >= t in the chunk} dG_i + (a_C <S0, dS> + sum_j k_j . (c_j U_j dS^T)).
+//
+// Four launches: delta_prep (the operands of both walks), the two walks (the
+// states and errors forwards, their gradients backwards; neither needs the
+// other), and delta_grad, one CTA per (chunk, head), for everything above. The
+// states and errors of every chunk are kept in the workspace in fp32.
+//
+// delta_grad takes the value columns in slices of 32, so that d = 128 fits a
+// CTA's shared memory, and sums the products over the columns in registers.
+// 8 warps: row block warp % 4, and one half of the columns (of a 64 x 64
+// product: every other 8 columns, so that the two halves of a triangular one
+// have equal work). All products are split tf32 (mma_tf32.cuh): dg is a
+// difference of large terms and comes out in fp32.
+#include "delta.cuh"
+
+namespace kata {
+namespace {
+
+using namespace delta;
+
+struct Grads {
+    void *dq, *dk, *dv;
+    float *dg, *dbeta;
+    const float *E, *Z;   // [chunks][64][D]
+    const float *S0, *dS; // [chunks][D][D]
+};
+
+template <typename Tin, int D>
+struct GradSmem {
+    static constexpr int SL = D < 32 ? D : 32;  // value columns per slice
+    static constexpr int KS = row_stride<D>(), SS = SL + 8;
+    static constexpr int IN = kC * KS * (int)sizeof(Tin);
+    static constexpr int K = 0, Q = IN, DO = 2 * IN;
+    static constexpr int E = DO + kC * SS * (int)sizeof(Tin), Z = E + kC * SS * 4;
+    static constexpr int S0 = Z + kC * SS * 4, DS = S0 + D * SS * 4;
+    static constexpr int M = DS + D * SS * 4, N = M + kC * kTS * 4;
+    static constexpr int G = N + kC * kTS * 4;
+    static constexpr int VEC = G + kC * 8;  // beta, a, c, dbeta [2], dG [2], end [8]
+    static constexpr int BYTES = VEC + (7 * kC + 8) * 4;
+};
+
+template <typename Tin>
+__device__ __forceinline__ void store2(Tin *d, float x, float y) {
+    if constexpr (sizeof(Tin) == 2)
+        *reinterpret_cast<__nv_bfloat162 *>(d) = __floats2bfloat162_rn(x, y);
+    else
+        *reinterpret_cast<float2 *>(d) = make_float2(x, y);
+}
+
+template <typename Tin, int D>
+__global__ void __launch_bounds__(256, D <= 64 ? 2 : 1) delta_grad(Args p, Grads gr_) {
+    using namespace tf;
+    using L = GradSmem<Tin, D>;
+    constexpr int KS = L::KS, SS = L::SS, SL = L::SL, TI = Parts<Tin>::N;
+    constexpr int NF = SL / 16;  // 8-column tiles of a slice per warp
+    constexpr int ND = D / 16;   // 8-column tiles of d per warp
+    extern __shared__ __align__(16) uint8_t sm[];
+    Tin *sK = reinterpret_cast<Tin *>(sm + L::K), *sQ = reinterpret_cast<Tin *>(sm + L::Q);
+    Tin *sO = reinterpret_cast<Tin *>(sm + L::DO);
+    float *sE = reinterpret_cast<float *>(sm + L::E), *sZ = reinterpret_cast<float *>(sm + L::Z);
+    float *sS0 = reinterpret_cast<float *>(sm + L::S0), *sDS = reinterpret_cast<float *>(sm + L::DS);
+    float *sM = reinterpret_cast<float *>(sm + L::M), *sN = reinterpret_cast<float *>(sm + L::N);
+    double *G = reinterpret_cast<double *>(sm + L::G);
+    float *beta = reinterpret_cast<float *>(sm + L::VEC), *ca = beta + kC, *cc = ca + kC;
+    float *sdb = cc + kC, *sdG = sdb + 2 * kC, *send = sdG + 2 * kC;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int gr = lane >> 2, t2 = 2 * (lane & 3);
+    const int rb = warp & 3, hf = warp >> 2, m0 = 16 * rb;
+    const size_t ch = blockIdx.x, head = ch / p.nc;
+    const int t0 = (int)(ch % p.nc) * kC;
+    const size_t row0 = head * (size_t)p.T;
+
+    auto load_slice = [&](int c0) {
+        load_tile<Tin, SL>(sO, SS, static_cast<const Tin *>(p.d_o), row0, t0, p.T, D, c0, tid, 256);
+        load_tile<float, SL>(sE, SS, gr_.E, ch * kC, 0, kC, D, c0, tid, 256);
+        load_tile<float, SL>(sZ, SS, gr_.Z, ch * kC, 0, kC, D, c0, tid, 256);
+        load_tile<float, SL, D>(sS0, SS, gr_.S0, ch * D, 0, D, D, c0, tid, 256);
+        load_tile<float, SL, D>(sDS, SS, gr_.dS, ch * D, 0, D, D, c0, tid, 256);
+        cp_commit();
+    };
+    load_tile<Tin, D>(sK, KS, static_cast<const Tin *>(p.k), row0, t0, p.T, D, 0, tid, 256);
+    load_tile<Tin, D>(sQ, KS, static_cast<const Tin *>(p.q), row0, t0, p.T, D, 0, tid, 256);
+    load_slice(0);
+    if (warp == 0) cumulate(p.g, row0, t0, p.T, G);
+    if (tid >= 192) {
+        const int t = t0 + tid - 192;
+        beta[tid - 192] = t < p.T ? p.beta[row0 + t] : 0.f;
+    }
+    cp_wait_all();
+    __syncthreads();
+    if (tid < kC) {
+        ca[tid] = expf((float)G[tid]);
+        cc[tid] = expf((float)(G[kC - 1] - G[tid]));
+    }
+    // this warp's tiles of a 64 x 64 product: columns 8 (2 nt + hf), up to the diagonal block
+    const int nt_end = rb + 1;
+    auto col = [&](int nt, int e) { return 8 * (2 * nt + hf) + t2 + (e & 1); };
+    auto row = [&](int e) { return m0 + gr + (e & 2 ? 8 : 0); };
+    {
+        float kk[4][4], qk[4][4];
+        clear(kk);
+        clear(qk);
+        // column 8 nt + g of the warp's tiles is column 16 nt + 8 hf + g of the product
+        auto kcol = [&](int n, int k) {
+            return pair<true>(sK, KS, 2 * (n & ~7) + 8 * hf + (n & 7), k);
+        };
+        gemm<TI, TI, 4>(
+            kk, 0, D / 8, [&](int m, int k) { return pair<true>(sK + m0 * KS, KS, m, k); }, kcol,
+            nt_end);
+        gemm<TI, TI, 4>(
+            qk, 0, D / 8, [&](int m, int k) { return pair<true>(sQ + m0 * KS, KS, m, k); }, kcol,
+            nt_end);
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) {
+            if (nt >= nt_end) continue;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = row(e), j = col(nt, e);
+                const float dec = i >= j ? expf((float)(G[i] - G[j])) : 0.f;
+                sN[i * kTS + j] = i > j ? kk[nt][e] * dec : 0.f;
+                sM[i * kTS + j] = i >= j ? qk[nt][e] * dec : 0.f;
+            }
+        }
+    }
+    __syncthreads();
+
+    float pm[4][4], pn[4][4], dq[ND][4], dr[ND][4], dl[ND][4];
+    clear(pm);
+    clear(pn);
+    clear(dq);
+    clear(dr);
+    clear(dl);
+    float db[2] = {0.f, 0.f}, end = 0.f;
+    const float aC = ca[kC - 1];
+    const int d0 = hf * (D / 2);  // this warp's columns of a [64, D] product
+    for (int c0 = 0; c0 < D; c0 += SL) {
+        if (c0 > 0) {
+            __syncthreads();
+            load_slice(c0);
+            cp_wait_all();
+            __syncthreads();
+        }
+        {  // F, and what it gives: dbeta, and the written keys' share of the decay
+            const int f0 = hf * (SL / 2);
+            float md[NF][4], kd[NF][4];
+            clear(md);
+            clear(kd);
+            gemm<2, TI, NF>(
+                md, 2 * rb, 8, [&](int m, int k) { return pair<false>(sM + m0, kTS, m, k); },
+                [&](int n, int k) { return pair<false>(sO + f0, SS, n, k); });
+#pragma unroll
+            for (int nt = 0; nt < NF; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) md[nt][e] *= -p.scale;
+            gemm<2, 2, NF>(
+                md, 2 * rb, 8, [&](int m, int k) { return pair<false>(sN + m0, kTS, m, k); },
+                [&](int n, int k) { return pair<false>(sZ + f0, SS, n, k); });
+            gemm<TI, 2, NF>(
+                kd, 0, D / 8, [&](int m, int k) { return pair<true>(sK + m0 * KS, KS, m, k); },
+                [&](int n, int k) { return pair<false>(sDS + f0, SS, n, k); });
+#pragma unroll
+            for (int nt = 0; nt < NF; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = row(e);
+                    const float E = sE[i * SS + f0 + 8 * nt + t2 + (e & 1)];
+                    const float ckd = cc[i] * kd[nt][e];
+                    db[e >> 1] = fmaf(E, ckd - md[nt][e], db[e >> 1]);
+                    end = fmaf(beta[i] * E, ckd, end);
+                }
+        }
+        for (int i = tid; i < D * SL; i += 256) {
+            const int at = (i / SL) * SS + i % SL;
+            end = fmaf(aC * sS0[at], sDS[at], end);
+        }
+        auto ucol = [&](int n, int k) {  // U's row as a column of U^T
+            const int j = 2 * (n & ~7) + 8 * hf + (n & 7);
+            const float2 x = pair<true>(sE, SS, j, k);
+            return make_float2(beta[j] * x.x, beta[j] * x.y);
+        };
+        gemm<TI, 2, 4>(
+            pm, 0, SL / 8, [&](int m, int k) { return pair<true>(sO + m0 * SS, SS, m, k); }, ucol,
+            nt_end);
+        gemm<2, 2, 4>(
+            pn, 0, SL / 8, [&](int m, int k) { return pair<true>(sZ + m0 * SS, SS, m, k); }, ucol,
+            nt_end);
+        auto scol = [&](int n, int k) { return pair<true>(sS0 + d0 * SS, SS, n, k); };
+        gemm<TI, 2, ND>(
+            dq, 0, SL / 8, [&](int m, int k) { return pair<true>(sO + m0 * SS, SS, m, k); }, scol);
+        gemm<2, 2, ND>(
+            dr, 0, SL / 8, [&](int m, int k) { return pair<true>(sZ + m0 * SS, SS, m, k); }, scol);
+        gemm<2, 2, ND>(
+            dl, 0, SL / 8, [&](int m, int k) { return pair<true>(sE + m0 * SS, SS, m, k); },
+            [&](int n, int k) { return pair<true>(sDS + d0 * SS, SS, n, k); });
+        Tin *dv = static_cast<Tin *>(gr_.dv);
+        for (int i = tid; i < kC * SL / 2; i += 256) {
+            const int r = i / (SL / 2), c = 2 * (i % (SL / 2));
+            if (t0 + r < p.T)
+                store2(dv + (row0 + t0 + r) * (size_t)D + c0 + c, sZ[r * SS + c], sZ[r * SS + c + 1]);
+        }
+    }
+    __syncthreads();  // M and N are read; PM and PN take their places
+#pragma unroll
+    for (int nt = 0; nt < 4; ++nt) {
+        if (nt >= nt_end) continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int i = row(e), j = col(nt, e);
+            const float dec = i >= j ? expf((float)(G[i] - G[j])) : 0.f;
+            sM[i * kTS + j] = i >= j ? p.scale * pm[nt][e] * dec : 0.f;
+            sN[i * kTS + j] = i > j ? -pn[nt][e] * dec : 0.f;
+        }
+    }
+#pragma unroll
+    for (int nt = 0; nt < ND; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int i = row(e);
+            dq[nt][e] *= p.scale * ca[i];
+            dr[nt][e] *= -ca[i];
+            dl[nt][e] *= beta[i] * cc[i];
+        }
+    __syncthreads();
+    auto kc = [&](int n, int k) { return pair<false>(sK + d0, KS, n, k); };
+    gemm<2, TI, ND>(
+        dq, 0, 2 * nt_end, [&](int m, int k) { return pair<true>(sM + m0 * kTS, kTS, m, k); }, kc);
+    gemm<2, TI, ND>(
+        dr, 0, 2 * nt_end, [&](int m, int k) { return pair<true>(sN + m0 * kTS, kTS, m, k); }, kc);
+    gemm<2, TI, ND>(
+        dl, 2 * rb, 8, [&](int m, int k) { return pair<false>(sM + m0, kTS, m, k); },
+        [&](int n, int k) { return pair<false>(sQ + d0, KS, n, k); });
+    gemm<2, TI, ND>(
+        dl, 2 * rb, 8, [&](int m, int k) { return pair<false>(sN + m0, kTS, m, k); }, kc);
+
+    float dG[2] = {0.f, 0.f};
+#pragma unroll
+    for (int nt = 0; nt < ND; ++nt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int i = m0 + gr + 8 * h, n = d0 + 8 * nt + t2;
+            const float2 kx = pair<true>(sK, KS, i, n), qx = pair<true>(sQ, KS, i, n);
+            const float q0 = dq[nt][2 * h], q1 = dq[nt][2 * h + 1];
+            const float r0 = dr[nt][2 * h], r1 = dr[nt][2 * h + 1];
+            const float l0 = dl[nt][2 * h], l1 = dl[nt][2 * h + 1];
+            dG[h] = fmaf(qx.x, q0, fmaf(kx.x, r0 - l0, dG[h]));
+            dG[h] = fmaf(qx.y, q1, fmaf(kx.y, r1 - l1, dG[h]));
+            if (t0 + i < p.T) {
+                const size_t at = (row0 + t0 + i) * (size_t)D + n;
+                store2(static_cast<Tin *>(gr_.dq) + at, q0, q1);
+                store2(static_cast<Tin *>(gr_.dk) + at, r0 + l0, r1 + l1);
+            }
+        }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int off = 1; off < 4; off <<= 1) {
+            dG[h] += __shfl_xor_sync(0xffffffffu, dG[h], off);
+            db[h] += __shfl_xor_sync(0xffffffffu, db[h], off);
+        }
+        if ((lane & 3) == 0) {
+            sdG[hf * kC + m0 + gr + 8 * h] = dG[h];
+            sdb[hf * kC + m0 + gr + 8 * h] = db[h];
+        }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) end += __shfl_xor_sync(0xffffffffu, end, off);
+    if (lane == 0) send[warp] = end;
+    __syncthreads();
+    if (warp == 0) {  // dg: sums from each token to the chunk's end, two tokens per lane
+        double tail = 0.0;
+        for (int w = 0; w < 8; ++w) tail += send[w];
+        const int i = 2 * lane;
+        const double x0 = (double)sdG[i] + sdG[kC + i], x1 = (double)sdG[i + 1] + sdG[kC + i + 1];
+        double sum = x0 + x1;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const double up = __shfl_down_sync(0xffffffffu, sum, off);
+            if (lane + off < 32) sum += up;
+        }
+        if (t0 + i < p.T) gr_.dg[row0 + t0 + i] = (float)(sum + tail);
+        if (t0 + i + 1 < p.T) gr_.dg[row0 + t0 + i + 1] = (float)(sum - x0 + tail);
+    } else if (tid >= 64 && tid < 128) {
+        const int i = tid - 64;
+        if (t0 + i < p.T) gr_.dbeta[row0 + t0 + i] = sdb[i] + sdb[kC + i];
+    }
+}
+
+// floats of scratch per chunk: the two walks' operands, what they keep
+constexpr size_t chunk_floats(int d) {
+    return 6 * (size_t)kC * d + 2 * (size_t)d * d + 2 * kCoef;
+}
+
+template <typename Tin, int D>
+cudaError_t backward_d(const DeltaArgs &a, const DeltaGrads &g, cudaStream_t stream) {
+    const int nc = chunks_of(a.T);
+    const size_t chunks = (size_t)a.heads * nc, mat = chunks * kC * D, st = chunks * D * D;
+    float *ws = static_cast<float *>(a.ws);
+    const Scratch f{ws, ws + mat, nullptr, ws + 6 * mat + 2 * st};
+    const Scratch r{ws + 2 * mat, ws + 3 * mat, nullptr, ws + 6 * mat + 2 * st + chunks * kCoef};
+    float *E = ws + 4 * mat, *Z = ws + 5 * mat, *S0 = ws + 6 * mat, *dS = S0 + st;
+
+    Args p{};
+    p.q = a.q;
+    p.k = a.k;
+    p.v = a.v;
+    p.d_o = g.d_o;
+    p.g = a.g;
+    p.beta = a.beta;
+    p.T = a.T;
+    p.nc = nc;
+    p.scale = a.scale;
+    cudaError_t e = launch_prep<Tin, D, true>(p, f, r, a.heads, stream);
+    if (e != cudaSuccess) return e;
+    Args fw = p;
+    fw.S_in = a.S_in;
+    fw.keepY = E;
+    fw.keepS = S0;
+    if ((e = launch_chain<Tin, D, false, true>(fw, f, a.heads, stream)) != cudaSuccess) return e;
+    Args bw = p;
+    bw.S_in = g.dS_out;
+    bw.S_out = g.dS_in;
+    bw.keepY = Z;
+    bw.keepS = dS;
+    if ((e = launch_chain<Tin, D, true, true>(bw, r, a.heads, stream)) != cudaSuccess) return e;
+
+    constexpr int bytes = GradSmem<Tin, D>::BYTES;
+    static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
+    if ((e = raise_smem<delta_grad<Tin, D>>(bytes)) != cudaSuccess) return e;
+    delta_grad<Tin, D><<<(unsigned)chunks, 256, bytes, stream>>>(
+        p, Grads{g.dq, g.dk, g.dv, g.dg, g.dbeta, E, Z, S0, dS});
+    return after_launch();
+}
+
+template <typename Tin>
+cudaError_t backward_t(const DeltaArgs &a, const DeltaGrads &g, cudaStream_t stream) {
+    switch (a.d) {
+        case 16: return backward_d<Tin, 16>(a, g, stream);
+        case 32: return backward_d<Tin, 32>(a, g, stream);
+        case 64: return backward_d<Tin, 64>(a, g, stream);
+        case 128: return backward_d<Tin, 128>(a, g, stream);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace
+
+size_t delta_backward_workspace_bytes(long heads, int T, int d) {
+    return (size_t)heads * delta::chunks_of(T) * chunk_floats(d) * sizeof(float);
+}
+
+cudaError_t delta_backward(const DeltaArgs &a, const DeltaGrads &g, cudaStream_t stream) {
+    return a.dtype == 0 ? backward_t<float>(a, g, stream) : backward_t<__nv_bfloat16>(a, g, stream);
+}
+
+}  // namespace kata

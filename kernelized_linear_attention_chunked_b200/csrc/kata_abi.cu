@@ -8,6 +8,7 @@
 #include <string.h>
 
 #include "../../include/kata.h"
+#include "../../include/kata_delta.h"
 #include "kata_common.cuh"
 #include "kata_internal.h"
 
@@ -818,6 +819,132 @@ int lola_prefill_ex(const void *q, const void *k, const void *v, int dtype, int 
               : kata::lola_run(q, k, v, dtype, B, H, T, d, window, cache, eps, tau, o, Hst, s,
                                kept_pos, workspace, ws_bytes, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "lola_prefill launch");
+    return KATA_OK;
+}
+
+/* ------------------------------------------------------ gated delta rule -- */
+
+static int check_delta(int dtype, int B, int H, int d, float scale) {
+    if (dtype != KATA_F32 && dtype != KATA_BF16)
+        return fail(KATA_ERR_UNSUPPORTED, "dtype %d is not KATA_F32 or KATA_BF16", dtype);
+    if (B <= 0 || H <= 0) return fail(KATA_ERR_INVALID_ARG, "B=%d H=%d must be positive", B, H);
+    if (d != 16 && d != 32 && d != 64 && d != 128)
+        return fail(KATA_ERR_UNSUPPORTED, "d=%d: only 16, 32, 64 and 128 are built", d);
+    if ((long)B * H > (1L << 20)) return fail(KATA_ERR_INVALID_ARG, "B*H=%ld too large", (long)B * H);
+    if (!(scale - scale == 0.f)) return fail(KATA_ERR_INVALID_ARG, "scale must be finite");
+    return KATA_OK;
+}
+
+static int check_delta_seq(int dtype, int B, int H, int T, int d, float scale) {
+    int st = check_delta(dtype, B, H, d, scale);
+    if (st) return st;
+    if (T <= 0) return fail(KATA_ERR_INVALID_ARG, "T=%d must be positive", T);
+    // one CTA per 64-token chunk and head
+    if (T > (1 << 24) || (long)B * H * (((long)T + 63) / 64) > 0x7FFFFFFFL)
+        return fail(KATA_ERR_INVALID_ARG, "T=%d with B*H=%ld is too large", T, (long)B * H);
+    return KATA_OK;
+}
+
+// An output that starts where an input does would be read by one CTA after
+// another has written it.
+#define KATA_NO_ALIAS(out, in)                                                     \
+    do {                                                                           \
+        if ((out) && (const void *)(out) == (const void *)(in))                    \
+            return fail(KATA_ERR_INVALID_ARG, "%s must not overwrite %s", #out, #in); \
+    } while (0)
+
+size_t kata_delta_prefill_workspace_bytes(int B, int H, int T, int d, int dtype) {
+    if (check_delta_seq(dtype, B, H, T, d, 1.f)) return 0;
+    return kata::delta_prefill_workspace_bytes((long)B * H, T, d);
+}
+
+int kata_delta_prefill(const void *q, const void *k, const void *v, int dtype, const float *g,
+                       const float *beta, int B, int H, int T, int d, float scale,
+                       const float *S_in, void *o, float *S_out, void *workspace,
+                       size_t ws_bytes, void *stream) {
+    g_last_error[0] = 0;
+    int st = check_delta_seq(dtype, B, H, T, d, scale);
+    if (st) return st;
+    KATA_REQUIRE_PTR(q);
+    KATA_REQUIRE_PTR(k);
+    KATA_REQUIRE_PTR(v);
+    KATA_REQUIRE_PTR(g);
+    KATA_REQUIRE_PTR(beta);
+    KATA_OPTIONAL_PTR(S_in);
+    KATA_OPTIONAL_PTR(o);
+    KATA_OPTIONAL_PTR(S_out);
+    if (!o && !S_out) return fail(KATA_ERR_INVALID_ARG, "o and S_out: at least one");
+    KATA_NO_ALIAS(o, q);
+    KATA_NO_ALIAS(o, k);
+    KATA_NO_ALIAS(o, v);
+    const size_t need = kata::delta_prefill_workspace_bytes((long)B * H, T, d);
+    if (ws_bytes < need || !workspace)
+        return fail(KATA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, need);
+    KATA_REQUIRE_PTR(workspace);
+    kata::DeltaArgs a{q, k, v, dtype, g, beta, (long)B * H, T, d, scale, S_in, o, S_out, workspace};
+    cudaError_t e = kata::delta_prefill(a, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "kata_delta_prefill launch");
+    return KATA_OK;
+}
+
+int kata_delta_decode_step(const void *q, const void *k, const void *v, int dtype, const float *g,
+                           const float *beta, int B, int H, int d, float scale, float *S, void *o,
+                           void *stream) {
+    g_last_error[0] = 0;
+    int st = check_delta(dtype, B, H, d, scale);
+    if (st) return st;
+    KATA_REQUIRE_PTR(q);
+    KATA_REQUIRE_PTR(k);
+    KATA_REQUIRE_PTR(v);
+    KATA_REQUIRE_PTR(g);
+    KATA_REQUIRE_PTR(beta);
+    KATA_REQUIRE_PTR(S);
+    KATA_REQUIRE_PTR(o);
+    KATA_NO_ALIAS(o, q);
+    KATA_NO_ALIAS(o, k);
+    KATA_NO_ALIAS(o, v);
+    cudaError_t e = kata::delta_decode_step(q, k, v, dtype, g, beta, (long)B * H, d, scale, S, o,
+                                            static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "kata_delta_decode_step launch");
+    return KATA_OK;
+}
+
+size_t kata_delta_backward_workspace_bytes(int B, int H, int T, int d, int dtype) {
+    if (check_delta_seq(dtype, B, H, T, d, 1.f)) return 0;
+    return kata::delta_backward_workspace_bytes((long)B * H, T, d);
+}
+
+int kata_delta_backward(const void *q, const void *k, const void *v, int dtype, const float *g,
+                        const float *beta, int B, int H, int T, int d, float scale,
+                        const float *S_in, const void *d_o, const float *dS_out, void *dq,
+                        void *dk, void *dv, float *dg, float *dbeta, float *dS_in,
+                        void *workspace, size_t ws_bytes, void *stream) {
+    g_last_error[0] = 0;
+    int st = check_delta_seq(dtype, B, H, T, d, scale);
+    if (st) return st;
+    KATA_REQUIRE_PTR(q);
+    KATA_REQUIRE_PTR(k);
+    KATA_REQUIRE_PTR(v);
+    KATA_REQUIRE_PTR(g);
+    KATA_REQUIRE_PTR(beta);
+    KATA_OPTIONAL_PTR(S_in);
+    KATA_REQUIRE_PTR(d_o);
+    KATA_OPTIONAL_PTR(dS_out);
+    KATA_REQUIRE_PTR(dq);
+    KATA_REQUIRE_PTR(dk);
+    KATA_REQUIRE_PTR(dv);
+    KATA_REQUIRE_PTR(dg);
+    KATA_REQUIRE_PTR(dbeta);
+    KATA_OPTIONAL_PTR(dS_in);
+    const size_t need = kata::delta_backward_workspace_bytes((long)B * H, T, d);
+    if (ws_bytes < need || !workspace)
+        return fail(KATA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, need);
+    KATA_REQUIRE_PTR(workspace);
+    kata::DeltaArgs a{q, k, v, dtype, g, beta, (long)B * H, T, d, scale, S_in, nullptr, nullptr,
+                      workspace};
+    kata::DeltaGrads gr{d_o, dS_out, dq, dk, dv, dg, dbeta, dS_in};
+    cudaError_t e = kata::delta_backward(a, gr, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "kata_delta_backward launch");
     return KATA_OK;
 }
 

@@ -95,6 +95,33 @@ cudaError_t lola_fused(const void *q, const void *k, const void *v, int dtype, i
 cudaError_t exclusive_prefix(const float *in, int nparts, size_t n, float *out,
                              cudaStream_t stream);
 
+// The gated delta rule (delta.cu, delta_backward.cu). heads = B * H.
+struct DeltaArgs {
+    const void *q, *k, *v;
+    int dtype;
+    const float *g, *beta;
+    long heads;
+    int T, d;
+    float scale;
+    const float *S_in;
+    void *o;
+    float *S_out;
+    void *ws;
+};
+struct DeltaGrads {
+    const void *d_o;
+    const float *dS_out;
+    void *dq, *dk, *dv;
+    float *dg, *dbeta, *dS_in;
+};
+size_t delta_prefill_workspace_bytes(long heads, int T, int d);
+cudaError_t delta_prefill(const DeltaArgs &a, cudaStream_t stream);
+cudaError_t delta_decode_step(const void *q, const void *k, const void *v, int dtype,
+                              const float *g, const float *beta, long heads, int d, float scale,
+                              float *S, void *o, cudaStream_t stream);
+size_t delta_backward_workspace_bytes(long heads, int T, int d);
+cudaError_t delta_backward(const DeltaArgs &a, const DeltaGrads &g, cudaStream_t stream);
+
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // Called right after every kernel launch: counts it (kata_launch_count) and
