@@ -1,0 +1,42 @@
+/*
+ * kata_backward.h -- gradients of kata_prefill in libkata.so, on NVIDIA B200
+ * (sm_100a). The conventions are those of kata.h.
+ */
+#ifndef KATA_BACKWARD_H
+#define KATA_BACKWARD_H
+
+#include "kata.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Device workspace bytes kata_prefill_backward needs (0: invalid sizes). */
+KATA_API size_t kata_prefill_backward_workspace_bytes(int B, int H, int T, int d, int dtype);
+
+/*
+ * Gradients of the output of kata_prefill from a zero state,
+ *   o_i = sum_{j<=i} (q_i.k_j)^2 v_j / (sum_{j<=i} (q_i.k_j)^2 + eps),
+ * with respect to q, k and v. The weights are recomputed from q and k; nothing
+ * of the forward call is needed, o included. Work is quadratic in T.
+ *   q, k, v      [B, H, T, d], dtype KATA_F32 or KATA_BF16; d 16, 32 or 64;
+ *                T any positive number (no multiple is asked for).
+ *   d_o          [B, H, T, d] gradient of o, in the dtype of q.
+ *   dq, dk, dv   [B, H, T, d], dtype of q; must not overlap the inputs.
+ *   workspace    device scratch of at least
+ *                kata_prefill_backward_workspace_bytes(); calls that may run
+ *                at the same time need one each.
+ * Deterministic. Inputs are expected finite, up to the last token: a NaN or an
+ * infinity reaches the whole 64- or 128-token tile it lies in. A row whose denominator is zero (eps = 0 and every score 0)
+ * has no defined output; its gradients are taken as 0.
+ */
+KATA_API int kata_prefill_backward(const void *q, const void *k, const void *v, int dtype, int B,
+                                   int H, int T, int d, float eps, const void *d_o, void *dq,
+                                   void *dk, void *dv, void *workspace, size_t ws_bytes,
+                                   void *stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* KATA_BACKWARD_H */

@@ -5,12 +5,13 @@
  * The conventions are those of kata.h (row-major, 16-byte aligned device
  * pointers, caller-owned buffers, asynchronous on `stream`, arguments
  * validated on the host before any launch, kata_status returned and
- * kata_last_error() set), with three differences of this family:
+ * kata_last_error() set), with these differences of this family:
  *   - the state is S [B, H, d, d] fp32, key rows and value columns (no packed
  *     feature, no normaliser);
  *   - o and the gradients of q, k, v have the dtype of q, k, v: what the next
  *     layer's product reads. g, beta, their gradients and the states are fp32;
- *   - d may be 16, 32, 64 or 128, and T any positive number.
+ *   - d may be 16, 32, 64 or 128, and T any positive number;
+ *   - g, beta, dg and dbeta need 4-byte alignment only.
  *
  * Per (b, h), token by token:
  *   e_t = v_t - exp(g_t) S_{t-1}^T k_t
@@ -20,7 +21,9 @@
  * exp of either is 0 in fp32; minus infinity starts the state anew); beta_t is
  * the writing strength. Keys are used as given: callers that want unit keys
  * normalise them. A token with beta = 0 and g = 0 leaves the state as it is,
- * so shorter sequences of a padded batch are padded with such tokens.
+ * so shorter sequences of a padded batch are padded with such tokens (with
+ * finite q, k and v: a NaN or an infinity reaches the whole 64-token chunk it
+ * lies in, and the state).
  */
 #ifndef KATA_DELTA_H
 #define KATA_DELTA_H

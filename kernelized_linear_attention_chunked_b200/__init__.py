@@ -37,6 +37,10 @@ from ._binding import (  # noqa: F401
     test_bounds_check,
     test_forced_timeout,
 )
+from ._backward import (  # noqa: F401
+    prefill_backward,
+    prefill_backward_workspace_bytes,
+)
 from ._delta import (  # noqa: F401
     delta_backward,
     delta_backward_workspace_bytes,

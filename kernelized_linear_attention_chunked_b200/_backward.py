@@ -1,0 +1,55 @@
+"""ctypes binding of the prefill's gradients (include/kata_backward.h).
+
+Argument marshalling only, like _binding.py; tensors are checked here, because
+the C ABI sees plain pointers.
+"""
+from __future__ import annotations
+
+import ctypes as C
+
+import torch
+
+from . import _binding as kb
+from ._binding import KataError, _check, _dt, _ptr, _workspace
+from ._calls import bind, on_stream, want
+
+_vp, _i, _f, _sz = C.c_void_p, C.c_int, C.c_float, C.c_size_t
+
+# name -> (restype, argtypes), mirroring include/kata_backward.h
+SIGNATURES = {
+    "kata_prefill_backward_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
+    "kata_prefill_backward": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _f, _vp, _vp, _vp, _vp, _vp,
+                                   _sz, _vp]),
+}
+
+
+def lib() -> C.CDLL:
+    """libkata.so with this header's entry points; raises if it has not been built."""
+    return bind(SIGNATURES)
+
+
+def prefill_backward_workspace_bytes(B, H, T, d, dtype) -> int:
+    return int(lib().kata_prefill_backward_workspace_bytes(B, H, T, d, kb._DTYPE[dtype]))
+
+
+def prefill_backward(q, k, v, do, eps: float = 1e-6, workspace=None, stream=None):
+    """Gradients (dq, dk, dv) of prefill's output from a zero state, for the
+    output's gradient ``do``. All [B, H, T, d] in q's dtype; any T."""
+    if q.dim() != 4:
+        raise KataError(f"q has {q.dim()} dimensions, expected 4")
+    dt = _dt(q)
+    for name, t in (("q", q), ("k", k), ("v", v), ("do", do)):
+        if t is None:
+            raise KataError(f"{name} must not be None")
+        want(name, t, q.shape, q.dtype, q)
+    want("workspace", workspace, None, None, q)
+    B, H, T, d = q.shape
+    L = lib()
+    with on_stream(q, stream) as s:
+        dq, dk, dv = (torch.empty_like(q) for _ in range(3))
+        if workspace is None:
+            workspace = _workspace(L.kata_prefill_backward_workspace_bytes(B, H, T, d, dt), q.device)
+        _check("kata_prefill_backward", L.kata_prefill_backward(
+            _ptr(q), _ptr(k), _ptr(v), dt, B, H, T, d, eps, _ptr(do), _ptr(dq), _ptr(dk), _ptr(dv),
+            _ptr(workspace), workspace.numel() * workspace.element_size(), s))
+    return dq, dk, dv

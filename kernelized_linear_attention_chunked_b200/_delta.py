@@ -6,13 +6,13 @@ Outputs and workspaces that are not given are allocated on the call's stream.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes as C
 
 import torch
 
 from . import _binding as kb
 from ._binding import KataError, _check, _dt, _ptr, _workspace
+from ._calls import bind, on_stream, want
 
 _vp, _i, _f, _sz = C.c_void_p, C.c_int, C.c_float, C.c_size_t
 
@@ -27,56 +27,23 @@ SIGNATURES = {
                                  _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
 }
 
-_bound = None
-
-
 def lib() -> C.CDLL:
     """libkata.so with this header's entry points; raises if it has not been built."""
-    global _bound
-    if _bound is None:
-        handle = kb.lib()
-        for name, (res, args) in SIGNATURES.items():
-            fn = getattr(handle, name)
-            fn.restype = res
-            fn.argtypes = args
-        _bound = handle
-    return _bound
-
-
-def want(name: str, t, shape, dtype, like: torch.Tensor) -> None:
-    """Raise unless t (None passes) is a contiguous tensor of this shape and
-    type on like's device."""
-    if t is None:
-        return
-    if not t.is_cuda or not t.is_contiguous():
-        raise KataError("tensors must be contiguous CUDA tensors")
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != like.device:
-        raise KataError(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device}, expected "
-                        f"{tuple(shape)} {dtype} on {like.device}")
-
-
-@contextlib.contextmanager
-def on_stream(t: torch.Tensor, stream):
-    """Runs a call on t's device and on `stream` (default: that device's current
-    one), and gives the stream's handle."""
-    with contextlib.ExitStack() as stack:
-        if t.device.index != torch.cuda.current_device():
-            stack.enter_context(torch.cuda.device(t.device))
-        if stream is not None:
-            if stream.device != t.device:
-                raise KataError(f"stream of {stream.device}, tensors on {t.device}")
-            stack.enter_context(torch.cuda.stream(stream))
-        yield torch.cuda.current_stream().cuda_stream
+    return bind(SIGNATURES)
 
 
 def _inputs(q, k, v, g, beta, ndim):
     if q.dim() != ndim:
         raise KataError(f"q has {q.dim()} dimensions, expected {ndim}")
     dt = _dt(q)
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        want(name, t, q.shape, q.dtype, q)
-    for name, t in (("g", g), ("beta", beta)):
-        want(name, t, q.shape[:-1], torch.float32, q)
+    for name, t in (("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta)):
+        if t is None:
+            raise KataError(f"{name} must not be None")
+    want("q", q, None, None, q)
+    want("k", k, q.shape, q.dtype, q)
+    want("v", v, q.shape, q.dtype, q)
+    want("g", g, q.shape[:-1], torch.float32, q)
+    want("beta", beta, q.shape[:-1], torch.float32, q)
     return dt
 
 
@@ -97,6 +64,7 @@ def delta_prefill(q, k, v, g, beta, scale: float | None = None, S_in=None, state
     want("S_in", S_in, st, torch.float32, q)
     want("S_out", S_out, st, torch.float32, q)
     want("o", o, q.shape, q.dtype, q)
+    want("workspace", workspace, None, None, q)
     scale = d ** -0.5 if scale is None else scale
     L = lib()
     with on_stream(q, stream) as s:
@@ -150,6 +118,7 @@ def delta_backward(q, k, v, g, beta, do, scale: float | None = None, S_in=None, 
     want("do", do, q.shape, q.dtype, q)
     want("S_in", S_in, st, torch.float32, q)
     want("dS", dS, st, torch.float32, q)
+    want("workspace", workspace, None, None, q)
     scale = d ** -0.5 if scale is None else scale
     L = lib()
     with on_stream(q, stream) as s:

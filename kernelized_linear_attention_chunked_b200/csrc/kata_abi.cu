@@ -8,6 +8,7 @@
 #include <string.h>
 
 #include "../../include/kata.h"
+#include "../../include/kata_backward.h"
 #include "../../include/kata_delta.h"
 #include "kata_common.cuh"
 #include "kata_internal.h"
@@ -845,6 +846,14 @@ static int check_delta_seq(int dtype, int B, int H, int T, int d, float scale) {
     return KATA_OK;
 }
 
+// Per-token scalars are read and written one by one: their own alignment is enough.
+#define KATA_REQUIRE_F32(p)                                                        \
+    do {                                                                           \
+        if (!(p)) return fail(KATA_ERR_INVALID_ARG, "%s must not be NULL", #p);    \
+        if (reinterpret_cast<uintptr_t>(p) & 3u)                                   \
+            return fail(KATA_ERR_INVALID_ARG, "%s is not 4-byte aligned", #p);     \
+    } while (0)
+
 // An output that starts where an input does would be read by one CTA after
 // another has written it.
 #define KATA_NO_ALIAS(out, in)                                                     \
@@ -868,8 +877,8 @@ int kata_delta_prefill(const void *q, const void *k, const void *v, int dtype, c
     KATA_REQUIRE_PTR(q);
     KATA_REQUIRE_PTR(k);
     KATA_REQUIRE_PTR(v);
-    KATA_REQUIRE_PTR(g);
-    KATA_REQUIRE_PTR(beta);
+    KATA_REQUIRE_F32(g);
+    KATA_REQUIRE_F32(beta);
     KATA_OPTIONAL_PTR(S_in);
     KATA_OPTIONAL_PTR(o);
     KATA_OPTIONAL_PTR(S_out);
@@ -896,8 +905,8 @@ int kata_delta_decode_step(const void *q, const void *k, const void *v, int dtyp
     KATA_REQUIRE_PTR(q);
     KATA_REQUIRE_PTR(k);
     KATA_REQUIRE_PTR(v);
-    KATA_REQUIRE_PTR(g);
-    KATA_REQUIRE_PTR(beta);
+    KATA_REQUIRE_F32(g);
+    KATA_REQUIRE_F32(beta);
     KATA_REQUIRE_PTR(S);
     KATA_REQUIRE_PTR(o);
     KATA_NO_ALIAS(o, q);
@@ -925,16 +934,16 @@ int kata_delta_backward(const void *q, const void *k, const void *v, int dtype, 
     KATA_REQUIRE_PTR(q);
     KATA_REQUIRE_PTR(k);
     KATA_REQUIRE_PTR(v);
-    KATA_REQUIRE_PTR(g);
-    KATA_REQUIRE_PTR(beta);
+    KATA_REQUIRE_F32(g);
+    KATA_REQUIRE_F32(beta);
     KATA_OPTIONAL_PTR(S_in);
     KATA_REQUIRE_PTR(d_o);
     KATA_OPTIONAL_PTR(dS_out);
     KATA_REQUIRE_PTR(dq);
     KATA_REQUIRE_PTR(dk);
     KATA_REQUIRE_PTR(dv);
-    KATA_REQUIRE_PTR(dg);
-    KATA_REQUIRE_PTR(dbeta);
+    KATA_REQUIRE_F32(dg);
+    KATA_REQUIRE_F32(dbeta);
     KATA_OPTIONAL_PTR(dS_in);
     const size_t need = kata::delta_backward_workspace_bytes((long)B * H, T, d);
     if (ws_bytes < need || !workspace)
@@ -945,6 +954,46 @@ int kata_delta_backward(const void *q, const void *k, const void *v, int dtype, 
     kata::DeltaGrads gr{d_o, dS_out, dq, dk, dv, dg, dbeta, dS_in};
     cudaError_t e = kata::delta_backward(a, gr, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "kata_delta_backward launch");
+    return KATA_OK;
+}
+
+/* ---------------------------------------------------- prefill gradients -- */
+
+static int check_prefill_backward(int dtype, int B, int H, int T, int d) {
+    int st = check_common(dtype, B, H, d);
+    if (st) return st;
+    // one CTA per 64 rows and head
+    if (T <= 0 || T > (1 << 24) || (long)B * H * (((long)T + 63) / 64) > 0x7FFFFFFFL)
+        return fail(KATA_ERR_INVALID_ARG, "T=%d must be positive, and B*H*T smaller", T);
+    return KATA_OK;
+}
+
+size_t kata_prefill_backward_workspace_bytes(int B, int H, int T, int d, int dtype) {
+    if (check_prefill_backward(dtype, B, H, T, d)) return 0;
+    return kata::prefill_backward_workspace_bytes((long)B * H, T);
+}
+
+int kata_prefill_backward(const void *q, const void *k, const void *v, int dtype, int B, int H,
+                          int T, int d, float eps, const void *d_o, void *dq, void *dk, void *dv,
+                          void *workspace, size_t ws_bytes, void *stream) {
+    g_last_error[0] = 0;
+    int st = check_prefill_backward(dtype, B, H, T, d);
+    if (st) return st;
+    if (!(eps >= 0.f)) return fail(KATA_ERR_INVALID_ARG, "eps must be >= 0");
+    KATA_REQUIRE_PTR(q);
+    KATA_REQUIRE_PTR(k);
+    KATA_REQUIRE_PTR(v);
+    KATA_REQUIRE_PTR(d_o);
+    KATA_REQUIRE_PTR(dq);
+    KATA_REQUIRE_PTR(dk);
+    KATA_REQUIRE_PTR(dv);
+    const size_t need = kata::prefill_backward_workspace_bytes((long)B * H, T);
+    if (ws_bytes < need || !workspace)
+        return fail(KATA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, need);
+    KATA_REQUIRE_PTR(workspace);
+    kata::PrefillBackwardArgs a{q, k, v, d_o, dtype, (long)B * H, T, d, eps, dq, dk, dv, workspace};
+    cudaError_t e = kata::prefill_backward(a, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "kata_prefill_backward launch");
     return KATA_OK;
 }
 

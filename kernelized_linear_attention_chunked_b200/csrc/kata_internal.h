@@ -122,6 +122,18 @@ cudaError_t delta_decode_step(const void *q, const void *k, const void *v, int d
 size_t delta_backward_workspace_bytes(long heads, int T, int d);
 cudaError_t delta_backward(const DeltaArgs &a, const DeltaGrads &g, cudaStream_t stream);
 
+// Gradients of the output-only prefill from a zero state (prefill_backward.cu).
+struct PrefillBackwardArgs {
+    const void *q, *k, *v, *d_o;
+    int dtype;
+    long heads;
+    int T, d;
+    float eps;
+    void *dq, *dk, *dv, *ws;
+};
+size_t prefill_backward_workspace_bytes(long heads, int T);
+cudaError_t prefill_backward(const PrefillBackwardArgs &a, cudaStream_t stream);
+
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // Called right after every kernel launch: counts it (kata_launch_count) and
