@@ -970,7 +970,7 @@ static int check_prefill_backward(int dtype, int B, int H, int T, int d) {
 
 size_t kata_prefill_backward_workspace_bytes(int B, int H, int T, int d, int dtype) {
     if (check_prefill_backward(dtype, B, H, T, d)) return 0;
-    return kata::prefill_backward_workspace_bytes((long)B * H, T);
+    return kata::prefill_backward_workspace_bytes(dtype, (long)B * H, T, d);
 }
 
 int kata_prefill_backward(const void *q, const void *k, const void *v, int dtype, int B, int H,
@@ -987,11 +987,14 @@ int kata_prefill_backward(const void *q, const void *k, const void *v, int dtype
     KATA_REQUIRE_PTR(dq);
     KATA_REQUIRE_PTR(dk);
     KATA_REQUIRE_PTR(dv);
-    const size_t need = kata::prefill_backward_workspace_bytes((long)B * H, T);
+    const size_t need = kata::prefill_backward_workspace_bytes(dtype, (long)B * H, T, d);
     if (ws_bytes < need || !workspace)
         return fail(KATA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, need);
     KATA_REQUIRE_PTR(workspace);
-    kata::PrefillBackwardArgs a{q, k, v, d_o, dtype, (long)B * H, T, d, eps, dq, dk, dv, workspace};
+    unsigned int *err = error_word();
+    if (!err) return fail(KATA_ERR_CUDA, "error word unavailable");
+    kata::PrefillBackwardArgs a{q,   k,  v,  d_o, dtype,     (long)B * H, T,
+                                d,   eps, dq, dk,  dv,        workspace,   err};
     cudaError_t e = kata::prefill_backward(a, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "kata_prefill_backward launch");
     return KATA_OK;

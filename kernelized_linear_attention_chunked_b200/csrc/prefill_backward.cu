@@ -363,11 +363,13 @@ cudaError_t run_d(const Args &p, long heads, int d, cudaStream_t stream) {
 
 }  // namespace
 
-size_t prefill_backward_workspace_bytes(long heads, int T) {
-    return (size_t)heads * T * sizeof(float4);
+size_t prefill_backward_workspace_bytes(int dtype, long heads, int T, int d) {
+    return prefill_backward_tc_applies(dtype, T, d) ? prefill_backward_tc_workspace_bytes(heads, T)
+                                                    : (size_t)heads * T * sizeof(float4);
 }
 
 cudaError_t prefill_backward(const PrefillBackwardArgs &a, cudaStream_t stream) {
+    if (prefill_backward_tc_applies(a.dtype, a.T, a.d)) return prefill_backward_tc(a, stream);
     const Args p{a.q, a.k, a.v, a.d_o, a.dq, a.dk, a.dv, static_cast<float4 *>(a.ws), a.T,
                  (a.T + kB - 1) / kB, a.eps};
     return a.dtype == 0 ? run_d<float>(p, a.heads, a.d, stream)

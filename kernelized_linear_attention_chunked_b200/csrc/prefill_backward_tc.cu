@@ -1,0 +1,504 @@
+// Gradients of the causal kernelized prefill on the tcgen05 tensor cores, for
+// bf16 inputs with d = 32 or 64 and any T. The formulas are in
+// prefill_backward.cu; this file is about how the products are fed.
+//
+// One kernel in two modes, two launches:
+//   queries  one CTA per (head, 128 queries). Walks the 64-key steps up to the
+//            diagonal twice: first S = Q K^T and dP = dO V^T for the rows' den
+//            and delta, then the same again for dS and dQ += dS K.
+//   keys     one CTA per (head, 128 keys). Walks the 64-query steps from the
+//            diagonal on: S^T = K Q^T, dP^T = V dO^T, dV += P^T dO,
+//            dK += dS^T Q, with each query's 1 / den and delta from the first.
+// In both the CTA's own 128 rows are the A operands of the score products
+// (tensor-memory lane = row) and the other side's 64 rows stream by TMA.
+//
+// Tensor memory (512 columns, one CTA per SM): two buffers of S (64 fp32
+// columns) and dP (64), then the accumulators. The workers overwrite S with P
+// and dP with dS as bf16 pairs, in place, and the output products take them
+// from there as A operands. A streamed tile serves both products it is needed
+// in: [64 rows, d] in rows of 2 d bytes, swizzled by that width, is a K-major
+// operand for the scores and an MN-major one for the outputs.
+//
+// Warp roles: two worker groups of four warps, a buffer each (step s goes to
+// s % 2; thread = row), a score issuer, an output issuer, a TMA producer. Every wait
+// is bounded.
+//
+// Rounding: scores, dP, den and delta are fp32 or wider; P and dS are rounded
+// to bf16 as operands (2^-9 of each term), the same size as the rounding of the
+// results. The rows of the first 128 queries sum den and delta in 64 bits, and
+// delta is two floats: with few keys dP - delta is a small difference. It
+// stays exact because S and dP come out of the same products with the same
+// bits in both modes and both walks.
+#include "kata_internal.h"
+#include "tc_tiles.cuh"
+
+namespace kata {
+namespace {
+
+using namespace tc;
+
+constexpr int kStep = 64;    // streamed rows per step
+constexpr int kBufs = 2;     // S | dP buffers, one per worker group
+constexpr int kStages = 5;   // streamed tiles in flight
+constexpr int kWorkerWarps = 4 * kBufs;
+constexpr int kThreads = 32 * (kWorkerWarps + 3);
+
+struct BwdParams {
+    int T, tiles, steps;  // tokens; 128-row tiles and 64-row steps per head
+    long pitch;           // rows per head of the statistics: 128 * tiles
+    float eps;
+    float *inv, *dhi, *dlo;  // [heads][pitch]: 1 / den, delta as two floats
+    __nv_bfloat16 *out0, *out1;  // queries: dQ; keys: dV, dK
+    unsigned int *err;
+};
+
+enum BwdBar {
+    kOwn = 0,                     // the CTA's own tiles landed
+    kTileFull = 1,                // stages: a step's tiles (and statistics) landed
+    kTileFree = kTileFull + kStages,
+    kSFull = kTileFree + kStages,  // buffers: S and dP are in tensor memory
+    kSRead = kSFull + kBufs,       // buffers: the first walk's workers read them (4 arrivals)
+    kPFull = kSRead + kBufs,       // buffers: P and dS are written (4 arrivals)
+    kPFree = kPFull + kBufs,       // buffers: the products that read them completed
+    kOutDone = kPFree + kBufs,
+    kSDrain,
+    kODrain,
+    kBars
+};
+
+template <int DH, bool KEYS>
+struct BwdCfg {
+    static constexpr int ROW = 2 * DH;                       // bytes per row, one swizzle atom
+    static constexpr uint32_t SW = DH == 64 ? kSwizzle128 : kSwizzle64;
+    static constexpr int OWN = 128 * ROW;                    // one own tile
+    static constexpr int TILE = kStep * ROW;                 // one streamed tile
+    static constexpr int STATS = 2 * TILE;                   // keys: inv, dhi, dlo of a step
+    static constexpr int STAGE = 2 * TILE + 1024;
+    static constexpr int STREAM = 2 * OWN;
+    static constexpr int RED = STREAM + kStages * STAGE;     // queries: row sums of the two groups
+    static constexpr int BAR = RED + kBufs * 2 * 128 * 8;
+    static constexpr int SLOT = BAR + kBars * 8;
+    static constexpr int NEED = SLOT + 16 + 1024;
+    // over half an SM's shared memory: a second CTA could not have tensor memory
+    static constexpr int BYTES = NEED > 118 * 1024 ? NEED : 118 * 1024;
+    static constexpr uint32_t ACC = 128 * kBufs;             // first accumulator column
+    static_assert(ACC + 2 * DH <= 512, "tensor-memory budget");
+    static constexpr int S_WARP = kWorkerWarps, O_WARP = S_WARP + 1, TMA_WARP = O_WARP + 1;
+};
+
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int x, int y, int z,
+                                            uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// Two fp32 values per instruction.
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float x, float y) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ F2 f2(uint32_t x, uint32_t y) {
+    return f2(__uint_as_float(x), __uint_as_float(y));
+}
+__device__ __forceinline__ float2 un(F2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 add(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+
+template <int DH, bool KEYS>
+__global__ void __launch_bounds__(kThreads, 1)
+    backward_kernel(const __grid_constant__ CUtensorMap own0, const __grid_constant__ CUtensorMap own1,
+                    const __grid_constant__ CUtensorMap str0, const __grid_constant__ CUtensorMap str1,
+                    BwdParams p) {
+    using L = BwdCfg<DH, KEYS>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::BAR);
+    uint32_t *slot = reinterpret_cast<uint32_t *>(sm + L::SLOT);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int head = blockIdx.x;
+    // the longest walks launch first: the last queries, the first keys
+    const int tile = KEYS ? (int)blockIdx.y : p.tiles - 1 - (int)blockIdx.y;
+    // steps of one walk: keys up to the diagonal, or queries from it on
+    const int first = KEYS ? 2 * tile : 0;
+    const int walk = KEYS ? p.steps - first : min(2 * tile + 2, p.steps);
+    const int n1 = KEYS ? 0 : walk;  // steps of the first (statistics) walk
+    const int n = n1 + walk;
+    auto step_of = [&](int s) { return first + (s < n1 ? s : s - n1); };
+    // how often buffer s % kBufs was filled before step s, in the second walk alone
+    auto second_use = [&](int s) {
+        const int f = n1 + (s % kBufs - n1 % kBufs + kBufs) % kBufs;
+        return (s - f) / kBufs;
+    };
+    const ErrCtx err{p.err};
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kBars; ++i) {
+            const bool four = (i >= kSRead && i < kSRead + kBufs) || (i >= kPFull && i < kPFull + kBufs);
+            mbar_init(&bar[i], four ? 4 : 1);
+        }
+        cta_abort_clear();
+        fence_barrier_init();
+    }
+    if (warp == L::S_WARP) {
+        tmem_alloc(slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *slot;
+
+    if (warp == L::TMA_WARP) {
+        if (lane == 0) {
+            prefetch_tensormap(&own0);
+            prefetch_tensormap(&own1);
+            prefetch_tensormap(&str0);
+            prefetch_tensormap(&str1);
+            mbar_arrive_expect_tx(&bar[kOwn], 2 * L::OWN);
+            for (int h = 0; h < 2; ++h) {  // boxes are 64 rows high
+                tma_load_3d(sm + h * L::TILE, &own0, 0, tile * 128 + h * kStep, head, &bar[kOwn]);
+                tma_load_3d(sm + L::OWN + h * L::TILE, &own1, 0, tile * 128 + h * kStep, head,
+                            &bar[kOwn]);
+            }
+            int issued = 0;
+            for (int s = 0; s < n; ++s) {
+                const int st = s % kStages;
+                if (s >= kStages &&
+                    !mbar_wait(&bar[kTileFree + st], (s / kStages - 1) & 1, err, 0x801))
+                    break;
+                uint8_t *d = sm + L::STREAM + st * L::STAGE;
+                const int y = step_of(s) * kStep;
+                mbar_arrive_expect_tx(&bar[kTileFull + st], 2 * L::TILE + (KEYS ? 3 * 4 * kStep : 0));
+                tma_load_3d(d, &str0, 0, y, head, &bar[kTileFull + st]);
+                tma_load_3d(d + L::TILE, &str1, 0, y, head, &bar[kTileFull + st]);
+                if (KEYS) {
+                    const size_t at = (size_t)head * p.pitch + y;
+                    bulk_load(d + L::STATS, p.inv + at, 4 * kStep, &bar[kTileFull + st]);
+                    bulk_load(d + L::STATS + 4 * kStep, p.dhi + at, 4 * kStep, &bar[kTileFull + st]);
+                    bulk_load(d + L::STATS + 8 * kStep, p.dlo + at, 4 * kStep, &bar[kTileFull + st]);
+                }
+                ++issued;
+            }
+            // no copy may be in flight when the CTA exits: the last one on each barrier
+            mbar_drain(&bar[kOwn], 0, err, 0x802);
+            for (int s = issued - kStages < 0 ? 0 : issued - kStages; s < issued; ++s)
+                mbar_drain(&bar[kTileFull + s % kStages], (s / kStages) & 1, err, 0x803);
+        }
+    } else if (warp == L::S_WARP) {
+        if (lane == 0) {
+            // S = own0 str0^T, dP = own1 str1^T into buffer s % kBufs
+            const uint32_t id = idesc_bf16(128, kStep, 0, 0);
+            const uint32_t a0 = smem_u32(sm), a1 = a0 + L::OWN, str = a0 + L::STREAM;
+            auto desc = [&](uint32_t base, int kk) {
+                return smem_desc(base + 32 * kk, 16, 8 * L::ROW, L::SW);
+            };
+            bool ok = mbar_wait(&bar[kOwn], 0, err, 0x810);
+            for (int s = 0; ok && s < n; ++s) {
+                const int b = s % kBufs, st = s % kStages;
+                if (s >= kBufs) {  // what used this buffer last has been read
+                    const int u = s - kBufs;
+                    ok = u < n1 ? mbar_wait(&bar[kSRead + b], (u / kBufs) & 1, err, 0x811)
+                                : mbar_wait(&bar[kPFree + b], second_use(u) & 1, err, 0x812);
+                }
+                ok = ok && mbar_wait(&bar[kTileFull + st], (s / kStages) & 1, err, 0x813);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t t0 = str + st * L::STAGE;
+#pragma unroll
+                for (int kk = 0; kk < DH / 16; ++kk)
+                    mma_ss(tmem + 128 * b, desc(a0, kk), desc(t0, kk), id, kk > 0);
+#pragma unroll
+                for (int kk = 0; kk < DH / 16; ++kk)
+                    mma_ss(tmem + 128 * b + 64, desc(a1, kk), desc(t0 + L::TILE, kk), id, kk > 0);
+                mma_commit(&bar[kSFull + b]);
+                if (s < n1) mma_commit(&bar[kTileFree + st]);
+            }
+            mma_commit(&bar[kSDrain]);
+            mbar_drain(&bar[kSDrain], 0, err, 0x814);
+        }
+    } else if (warp == L::O_WARP) {
+        if (lane == 0) {
+            // queries: dQ += dS K;  keys: dV += P^T dO, dK += dS^T Q
+            const uint32_t id = idesc_bf16(128, DH, 0, 1);
+            const uint32_t str = smem_u32(sm) + L::STREAM;
+            auto desc = [&](uint32_t base, int kk) {  // rows 16 kk ..
+                return smem_desc(base + 16 * kk * L::ROW, 16, 8 * L::ROW, L::SW);
+            };
+            bool ok = true;
+            for (int s = n1; s < n; ++s) {
+                const int b = s % kBufs, st = s % kStages;
+                ok = mbar_wait(&bar[kPFull + b], second_use(s) & 1, err, 0x820);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t t0 = str + st * L::STAGE;
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                    if (KEYS)
+                        mma_ts(tmem + L::ACC + DH, tmem + 128 * b + 8 * kk, desc(t0 + L::TILE, kk), id,
+                               s > n1 || kk > 0);
+                    mma_ts(tmem + L::ACC, tmem + 128 * b + 64 + 8 * kk, desc(t0, kk), id,
+                           s > n1 || kk > 0);
+                }
+                mma_commit(&bar[kPFree + b]);
+                mma_commit(&bar[kTileFree + st]);
+            }
+            if (ok) mma_commit(&bar[kOutDone]);
+            mma_commit(&bar[kODrain]);
+            mbar_drain(&bar[kODrain], 0, err, 0x821);
+        }
+    } else {
+        // ---------------- workers: thread = own row = tensor-memory lane ----------------
+        const int group = warp >> 2, i = threadIdx.x & 127, row = tile * 128 + i;
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        bool ok = true;
+        float inv = 0.f, dhi = 0.f, dlo = 0.f;
+
+        // columns c .. c + 31 of S and dP
+        auto load = [&](int b, int c, uint32_t (&s)[32], uint32_t (&dp)[32]) {
+            uint32_t(*s2)[16] = reinterpret_cast<uint32_t(*)[16]>(s);
+            uint32_t(*d2)[16] = reinterpret_cast<uint32_t(*)[16]>(dp);
+            tmem_ld16(lanes + 128 * b + c, s2[0]);
+            tmem_ld16(lanes + 128 * b + c + 16, s2[1]);
+            tmem_ld16(lanes + 128 * b + 64 + c, d2[0]);
+            tmem_ld16(lanes + 128 * b + 64 + c + 16, d2[1]);
+            tmem_ld_wait();
+        };
+        // columns a row does not see count as a score of zero
+        auto mask = [&](int col0, uint32_t (&s)[32]) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                if (KEYS ? col0 + e < row : col0 + e > row) s[e] = 0u;
+        };
+        auto on_diagonal = [&](int step) {
+            return KEYS ? step < 2 * tile + 2 : step >= 2 * tile;
+        };
+
+        if (!KEYS) {
+            double den = 0.0, num = 0.0;
+            for (int s = group; s < n1; s += kBufs) {
+                const int b = group, step = step_of(s);
+                if (!(ok = warp_wait(&bar[kSFull + b], (s / kBufs) & 1, err, 0x830))) break;
+                tc_fence_after();
+                F2 d2 = f2(0.f, 0.f), n2 = d2;
+#pragma unroll
+                for (int c = 0; c < 64; c += 32) {
+                    uint32_t sv[32], dv[32];
+                    load(b, c, sv, dv);
+                    if (on_diagonal(step)) mask(step * kStep + c, sv);
+                    if (tile == 0) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const double x = __uint_as_float(sv[e]), w = x * x;
+                            den += w;
+                            num = ::fma(w, (double)__uint_as_float(dv[e]), num);
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            const F2 x = f2(sv[e], sv[e + 1]), w = mul(x, x);
+                            d2 = add(d2, w);
+                            n2 = fma(w, f2(dv[e], dv[e + 1]), n2);
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[kSRead + b]);
+                const float2 a = un(d2), c = un(n2);
+                den += (double)a.x + (double)a.y;
+                num += (double)c.x + (double)c.y;
+            }
+            // join the two groups' sums
+            double *red = reinterpret_cast<double *>(sm + L::RED);
+            red[group * 256 + i] = den;
+            red[group * 256 + 128 + i] = num;
+            ok = bar_sync_and(1, 32 * kWorkerWarps, ok);
+            den = (double)p.eps;
+            num = 0.0;
+            for (int g = 0; g < kBufs; ++g) {
+                den += red[g * 256 + i];
+                num += red[g * 256 + 128 + i];
+            }
+            if (den != 0.0) {
+                const double delta = num / den;
+                inv = (float)(1.0 / den);
+                dhi = (float)delta;
+                dlo = (float)(delta - (double)dhi);
+            }
+            if (ok && group == 0) {  // rows from T on: zeros, which make their keys' terms zero
+                const size_t at = (size_t)head * p.pitch + row;
+                const bool have = row < p.T;
+                p.inv[at] = have ? inv : 0.f;
+                p.dhi[at] = have ? dhi : 0.f;
+                p.dlo[at] = have ? dlo : 0.f;
+            }
+        }
+        // dS / 2 = (s / den) (dP - delta), P = s (s / den); the factor 2 comes at the end
+        for (int s = n1 + (group - n1 % kBufs + kBufs) % kBufs; ok && s < n; s += kBufs) {
+            const int b = group, step = step_of(s);
+            if (!(ok = warp_wait(&bar[kSFull + b], (s / kBufs) & 1, err, 0x831))) break;
+            tc_fence_after();
+            // the statistics arrived with the step's tiles, before its products
+            if (KEYS && !(ok = warp_wait(&bar[kTileFull + s % kStages], (s / kStages) & 1, err, 0x832)))
+                break;
+            const float *st = reinterpret_cast<const float *>(sm + L::STREAM + (s % kStages) * L::STAGE +
+                                                              L::STATS);
+            const bool few = KEYS ? step < 2 : tile == 0;  // rows that may see few keys
+#pragma unroll
+            for (int c = 0; c < 64; c += 32) {
+                uint32_t sv[32], dv[32];
+                load(b, c, sv, dv);
+                if (on_diagonal(step)) mask(step * kStep + c, sv);
+                uint32_t pk[16], dk[16];
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    float4 iv = make_float4(inv, inv, inv, inv), dh = make_float4(dhi, dhi, dhi, dhi);
+                    float4 dl = make_float4(dlo, dlo, dlo, dlo);
+                    if (KEYS) {
+                        iv = *reinterpret_cast<const float4 *>(st + c + e);
+                        dh = *reinterpret_cast<const float4 *>(st + kStep + c + e);
+                        if (few) dl = *reinterpret_cast<const float4 *>(st + 2 * kStep + c + e);
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const F2 x = f2(sv[e + 2 * h], sv[e + 2 * h + 1]);
+                        const F2 w = mul(x, h ? f2(iv.z, iv.w) : f2(iv.x, iv.y));
+                        F2 t = add(f2(dv[e + 2 * h], dv[e + 2 * h + 1]),
+                                   h ? f2(-dh.z, -dh.w) : f2(-dh.x, -dh.y));
+                        if (few) t = add(t, h ? f2(-dl.z, -dl.w) : f2(-dl.x, -dl.y));
+                        const float2 ds = un(mul(w, t));
+                        dk[e / 2 + h] = pack_bf16x2(ds.x, ds.y);
+                        if (KEYS) {
+                            const float2 pp = un(mul(x, w));
+                            pk[e / 2 + h] = pack_bf16x2(pp.x, pp.y);
+                        }
+                    }
+                }
+                if (KEYS) tmem_st16(lanes + 128 * b + c / 2, pk);
+                tmem_st16(lanes + 128 * b + 64 + c / 2, dk);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[kPFull + b]);
+        }
+        // queries: both groups take half of dQ's columns; keys: group 0 dK, group 1 dV
+        if (ok) ok = warp_wait(&bar[kOutDone], 0, err, 0x833);
+        tc_fence_after();
+        constexpr int COLS = KEYS ? DH : DH / 2;
+        const uint32_t col0 = L::ACC + group * COLS;
+        const float scale = KEYS && group == 1 ? 1.f : 2.f;
+        __nv_bfloat16 *out = KEYS && group == 1 ? p.out1 : p.out0;
+        uint4 *dst = reinterpret_cast<uint4 *>(out + ((size_t)head * p.T + row) * DH +
+                                               (KEYS ? 0 : group * COLS));
+#pragma unroll
+        for (int c = 0; c < COLS; c += 16) {
+            uint32_t r[16];
+            tmem_ld16(lanes + col0 + c, r);
+            tmem_ld_wait();
+            uint32_t o[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                o[e] = pack_bf16x2(scale * __uint_as_float(r[2 * e]),
+                                   scale * __uint_as_float(r[2 * e + 1]));
+            if (ok && row < p.T) {
+                dst[c / 8] = make_uint4(o[0], o[1], o[2], o[3]);
+                dst[c / 8 + 1] = make_uint4(o[4], o[5], o[6], o[7]);
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == L::S_WARP) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// [heads, T, d] in boxes of 64 rows x d columns; rows past T are zero-filled.
+bool map_rows(CUtensorMap *m, const void *base, int d, int T, long heads) {
+    auto enc = get_encode();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)T, (cuuint64_t)heads};
+    cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)T * d * 2};
+    cuuint32_t box[3] = {(cuuint32_t)d, (cuuint32_t)kStep, 1};
+    cuuint32_t es[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
+               es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               d == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DH>
+cudaError_t launch(const PrefillBackwardArgs &a, cudaStream_t stream) {
+    CUtensorMap mq, mk, mv, mo;
+    if (!map_rows(&mq, a.q, DH, a.T, a.heads) || !map_rows(&mk, a.k, DH, a.T, a.heads) ||
+        !map_rows(&mv, a.v, DH, a.T, a.heads) || !map_rows(&mo, a.d_o, DH, a.T, a.heads))
+        return cudaErrorInvalidValue;
+    BwdParams p;
+    p.T = a.T;
+    p.tiles = (a.T + 127) / 128;
+    p.steps = (a.T + kStep - 1) / kStep;
+    p.pitch = 128L * p.tiles;
+    p.eps = a.eps;
+    p.inv = static_cast<float *>(a.ws);
+    p.dhi = p.inv + a.heads * p.pitch;
+    p.dlo = p.dhi + a.heads * p.pitch;
+    p.err = a.err;
+    const dim3 grid((unsigned)a.heads, (unsigned)p.tiles);
+    cudaError_t e;
+    using Q = BwdCfg<DH, false>;
+    using K = BwdCfg<DH, true>;
+    if ((e = set_smem_once<backward_kernel<DH, false>>(Q::BYTES)) != cudaSuccess) return e;
+    if ((e = set_smem_once<backward_kernel<DH, true>>(K::BYTES)) != cudaSuccess) return e;
+    p.out0 = static_cast<__nv_bfloat16 *>(a.dq);
+    p.out1 = nullptr;
+    backward_kernel<DH, false><<<grid, kThreads, Q::BYTES, stream>>>(mq, mo, mk, mv, p);
+    if ((e = after_launch()) != cudaSuccess) return e;
+    p.out0 = static_cast<__nv_bfloat16 *>(a.dk);
+    p.out1 = static_cast<__nv_bfloat16 *>(a.dv);
+    backward_kernel<DH, true><<<grid, kThreads, K::BYTES, stream>>>(mk, mv, mq, mo, p);
+    return after_launch();
+}
+
+}  // namespace
+
+bool prefill_backward_tc_applies(int dtype, int T, int d) {
+    return dtype == 1 && (d == 32 || d == 64) && (T + 127) / 128 <= 65535;
+}
+
+size_t prefill_backward_tc_workspace_bytes(long heads, int T) {
+    return (size_t)heads * ((T + 127) / 128) * 128 * 3 * sizeof(float);
+}
+
+cudaError_t prefill_backward_tc(const PrefillBackwardArgs &a, cudaStream_t stream) {
+    return a.d == 64 ? launch<64>(a, stream) : launch<32>(a, stream);
+}
+
+}  // namespace kata
