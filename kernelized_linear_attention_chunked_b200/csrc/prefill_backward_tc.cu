@@ -12,16 +12,17 @@
 // In both the CTA's own 128 rows are the A operands of the score products
 // (tensor-memory lane = row) and the other side's 64 rows stream by TMA.
 //
-// Tensor memory (512 columns, one CTA per SM): two buffers of S (64 fp32
+// Tensor memory (512 columns, one CTA per SM): three buffers of S (64 fp32
 // columns) and dP (64), then the accumulators. The workers overwrite S with P
 // and dP with dS as bf16 pairs, in place, and the output products take them
 // from there as A operands. A streamed tile serves both products it is needed
 // in: [64 rows, d] in rows of 2 d bytes, swizzled by that width, is a K-major
 // operand for the scores and an MN-major one for the outputs.
 //
-// Warp roles: two worker groups of four warps, a buffer each (step s goes to
-// s % 2; thread = row), a score issuer, an output issuer, a TMA producer. Every wait
-// is bounded.
+// Warp roles: two sets of workers on alternate steps, each two groups of four
+// warps with half the step's columns (thread = row), an issuer of the score products, one of the output
+// products, a TMA producer. Every wait is bounded. A step takes two commits: each
+// costs the tensor pipe about as much as two MMAs.
 //
 // Rounding: scores, dP, den and delta are fp32 or wider; P and dS are rounded
 // to bf16 as operands (2^-9 of each term), the same size as the rounding of the
@@ -38,29 +39,34 @@ namespace {
 using namespace tc;
 
 constexpr int kStep = 64;    // streamed rows per step
-constexpr int kBufs = 2;     // S | dP buffers, one per worker group
-constexpr int kStages = 5;   // streamed tiles in flight
-constexpr int kWorkerWarps = 4 * kBufs;
+constexpr int kBufs = 3;     // S | dP buffers
+constexpr int kStages = 6;   // streamed tiles in flight
+constexpr int kSets = 2;     // sets of workers, on alternate steps
+constexpr int kGroups = 2 * kSets;  // a set is two groups of four warps, half the columns each
+constexpr int kWorkerWarps = 4 * kGroups;
+constexpr int kFulls = kBufs * kSets;  // a barrier per (buffer, set): each is awaited in every phase
 constexpr int kThreads = 32 * (kWorkerWarps + 3);
 
 struct BwdParams {
     int T, tiles, steps;  // tokens; 128-row tiles and 64-row steps per head
     long pitch;           // rows per head of the statistics: 128 * tiles
     float eps;
-    float *inv, *dhi, *dlo;  // [heads][pitch]: 1 / den, delta as two floats
+    float *inv, *dhi, *dlo;  // [heads][pitch]: 1 / den, -delta as two floats
     __nv_bfloat16 *out0, *out1;  // queries: dQ; keys: dV, dK
     unsigned int *err;
 };
 
 enum BwdBar {
     kOwn = 0,                     // the CTA's own tiles landed
-    kTileFull = 1,                // stages: a step's tiles (and statistics) landed
-    kTileFree = kTileFull + kStages,
-    kSFull = kTileFree + kStages,  // buffers: S and dP are in tensor memory
-    kSRead = kSFull + kBufs,       // buffers: the first walk's workers read them (4 arrivals)
-    kPFull = kSRead + kBufs,       // buffers: P and dS are written (4 arrivals)
-    kPFree = kPFull + kBufs,       // buffers: the products that read them completed
-    kOutDone = kPFree + kBufs,
+    kTileFull = 1,                 // stages: a step's tiles (and statistics) landed
+    kSFull = kTileFull + kStages,  // (buffer, set): S and dP are in tensor memory
+    kPFull = kSFull + kFulls,      // buffers: P and dS are written (8 arrivals)
+    // stages: a step is over, its tiles and its buffer free: in the first walk when
+    // the workers have read S and dP (8 arrivals), in the second when the output
+    // products completed
+    kRead = kPFull + kBufs,
+    kDone = kRead + kStages,
+    kOutDone = kDone + kStages,
     kSDrain,
     kODrain,
     kBars
@@ -76,13 +82,14 @@ struct BwdCfg {
     static constexpr int STAGE = 2 * TILE + 1024;
     static constexpr int STREAM = 2 * OWN;
     static constexpr int RED = STREAM + kStages * STAGE;     // queries: row sums of the two groups
-    static constexpr int BAR = RED + kBufs * 2 * 128 * 8;
+    static constexpr int BAR = RED + kGroups * 2 * 128 * 8;
     static constexpr int SLOT = BAR + kBars * 8;
     static constexpr int NEED = SLOT + 16 + 1024;
     // over half an SM's shared memory: a second CTA could not have tensor memory
     static constexpr int BYTES = NEED > 118 * 1024 ? NEED : 118 * 1024;
     static constexpr uint32_t ACC = 128 * kBufs;             // first accumulator column
     static_assert(ACC + 2 * DH <= 512, "tensor-memory budget");
+    static_assert(SLOT % 8 == 0 && BAR % 8 == 0, "barriers");
     static constexpr int S_WARP = kWorkerWarps, O_WARP = S_WARP + 1, TMA_WARP = O_WARP + 1;
 };
 
@@ -143,23 +150,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int head = blockIdx.x;
     // the longest walks launch first: the last queries, the first keys
     const int tile = KEYS ? (int)blockIdx.y : p.tiles - 1 - (int)blockIdx.y;
+    const ErrCtx err{p.err};
     // steps of one walk: keys up to the diagonal, or queries from it on
     const int first = KEYS ? 2 * tile : 0;
     const int walk = KEYS ? p.steps - first : min(2 * tile + 2, p.steps);
     const int n1 = KEYS ? 0 : walk;  // steps of the first (statistics) walk
     const int n = n1 + walk;
     auto step_of = [&](int s) { return first + (s < n1 ? s : s - n1); };
-    // how often buffer s % kBufs was filled before step s, in the second walk alone
-    auto second_use = [&](int s) {
-        const int f = n1 + (s % kBufs - n1 % kBufs + kBufs) % kBufs;
-        return (s - f) / kBufs;
+    // which use of its kind step s makes of slot s % m, counted in the second walk alone
+    auto second_use = [&](int s, int m) { return (s - n1 - (s % m - n1 % m + m) % m) / m; };
+    auto wait_over = [&](int u, unsigned int code) {  // step u is over
+        return u < n1 ? mbar_wait(&bar[kRead + u % kStages], (u / kStages) & 1, err, code)
+                      : mbar_wait(&bar[kDone + u % kStages], second_use(u, kStages) & 1, err, code);
     };
-    const ErrCtx err{p.err};
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kBars; ++i) {
-            const bool four = (i >= kSRead && i < kSRead + kBufs) || (i >= kPFull && i < kPFull + kBufs);
-            mbar_init(&bar[i], four ? 4 : 1);
+            const bool workers = (i >= kPFull && i < kPFull + kBufs) || (i >= kRead && i < kRead + kStages);
+            mbar_init(&bar[i], workers ? 8 : 1);
         }
         cta_abort_clear();
         fence_barrier_init();
@@ -188,9 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int issued = 0;
             for (int s = 0; s < n; ++s) {
                 const int st = s % kStages;
-                if (s >= kStages &&
-                    !mbar_wait(&bar[kTileFree + st], (s / kStages - 1) & 1, err, 0x801))
-                    break;
+                if (s >= kStages && !wait_over(s - kStages, 0x801)) break;
                 uint8_t *d = sm + L::STREAM + st * L::STAGE;
                 const int y = step_of(s) * kStep;
                 mbar_arrive_expect_tx(&bar[kTileFull + st], 2 * L::TILE + (KEYS ? 3 * 4 * kStep : 0));
@@ -211,87 +217,83 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == L::S_WARP) {
         if (lane == 0) {
-            // S = own0 str0^T, dP = own1 str1^T into buffer s % kBufs
+            // S = own0 str0^T and dP = own1 str1^T into buffer s % kBufs
             const uint32_t id = idesc_bf16(128, kStep, 0, 0);
-            const uint32_t a0 = smem_u32(sm), a1 = a0 + L::OWN, str = a0 + L::STREAM;
-            auto desc = [&](uint32_t base, int kk) {
-                return smem_desc(base + 32 * kk, 16, 8 * L::ROW, L::SW);
-            };
+            const uint32_t own = smem_u32(sm), str = own + L::STREAM;
+            const uint64_t a0 = smem_desc(own, 16, 8 * L::ROW, L::SW);
+            const uint64_t a1 = smem_desc(own + L::OWN, 16, 8 * L::ROW, L::SW);
+            const uint64_t db = smem_desc(str, 16, 8 * L::ROW, L::SW);
             bool ok = mbar_wait(&bar[kOwn], 0, err, 0x810);
             for (int s = 0; ok && s < n; ++s) {
                 const int b = s % kBufs, st = s % kStages;
-                if (s >= kBufs) {  // what used this buffer last has been read
-                    const int u = s - kBufs;
-                    ok = u < n1 ? mbar_wait(&bar[kSRead + b], (u / kBufs) & 1, err, 0x811)
-                                : mbar_wait(&bar[kPFree + b], second_use(u) & 1, err, 0x812);
-                }
-                ok = ok && mbar_wait(&bar[kTileFull + st], (s / kStages) & 1, err, 0x813);
+                ok = (s < kBufs || wait_over(s - kBufs, 0x811)) &&
+                     mbar_wait(&bar[kTileFull + st], (s / kStages) & 1, err, 0x812);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t t0 = str + st * L::STAGE;
+                const uint32_t d = tmem + 128 * b;
+                const uint64_t t0 = db + (uint32_t)(st * (L::STAGE >> 4)), t1 = t0 + (L::TILE >> 4);
+#pragma unroll
+                for (int kk = 0; kk < DH / 16; ++kk)  // 16 columns = 32 bytes on
+                    mma_ss(d, a0 + 2 * kk, t0 + 2 * kk, id, kk > 0);
 #pragma unroll
                 for (int kk = 0; kk < DH / 16; ++kk)
-                    mma_ss(tmem + 128 * b, desc(a0, kk), desc(t0, kk), id, kk > 0);
-#pragma unroll
-                for (int kk = 0; kk < DH / 16; ++kk)
-                    mma_ss(tmem + 128 * b + 64, desc(a1, kk), desc(t0 + L::TILE, kk), id, kk > 0);
-                mma_commit(&bar[kSFull + b]);
-                if (s < n1) mma_commit(&bar[kTileFree + st]);
+                    mma_ss(d + 64, a1 + 2 * kk, t1 + 2 * kk, id, kk > 0);
+                mma_commit(&bar[kSFull + s % kFulls]);
             }
             mma_commit(&bar[kSDrain]);
             mbar_drain(&bar[kSDrain], 0, err, 0x814);
         }
     } else if (warp == L::O_WARP) {
         if (lane == 0) {
-            // queries: dQ += dS K;  keys: dV += P^T dO, dK += dS^T Q
+            // queries: dQ += dS K;  keys: dK += dS^T Q and dV += P^T dO
             const uint32_t id = idesc_bf16(128, DH, 0, 1);
-            const uint32_t str = smem_u32(sm) + L::STREAM;
-            auto desc = [&](uint32_t base, int kk) {  // rows 16 kk ..
-                return smem_desc(base + 16 * kk * L::ROW, 16, 8 * L::ROW, L::SW);
-            };
+            const uint64_t db = smem_desc(smem_u32(sm) + L::STREAM, 16, 8 * L::ROW, L::SW);
             bool ok = true;
             for (int s = n1; s < n; ++s) {
                 const int b = s % kBufs, st = s % kStages;
-                ok = mbar_wait(&bar[kPFull + b], second_use(s) & 1, err, 0x820);
+                ok = mbar_wait(&bar[kPFull + b], second_use(s, kBufs) & 1, err, 0x820);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t t0 = str + st * L::STAGE;
+                const uint64_t t0 = db + (uint32_t)(st * (L::STAGE >> 4)), t1 = t0 + (L::TILE >> 4);
+                // 16 rows on; a group's columns lie in its own half
+                auto a = [&](int kk) { return tmem + 128 * b + 8 * kk + (kk < 2 ? 0 : 16); };
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                    if (KEYS)
-                        mma_ts(tmem + L::ACC + DH, tmem + 128 * b + 8 * kk, desc(t0 + L::TILE, kk), id,
-                               s > n1 || kk > 0);
-                    mma_ts(tmem + L::ACC, tmem + 128 * b + 64 + 8 * kk, desc(t0, kk), id,
-                           s > n1 || kk > 0);
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_ts(tmem + L::ACC, a(kk) + 64, t0 + kk * L::ROW, id, s > n1 || kk > 0);
+                if (KEYS) {
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_ts(tmem + L::ACC + DH, a(kk), t1 + kk * L::ROW, id, s > n1 || kk > 0);
                 }
-                mma_commit(&bar[kPFree + b]);
-                mma_commit(&bar[kTileFree + st]);
+                mma_commit(&bar[kDone + st]);
             }
             if (ok) mma_commit(&bar[kOutDone]);
             mma_commit(&bar[kODrain]);
             mbar_drain(&bar[kODrain], 0, err, 0x821);
         }
-    } else {
+    } else if (warp < kWorkerWarps) {
         // ---------------- workers: thread = own row = tensor-memory lane ----------------
         const int group = warp >> 2, i = threadIdx.x & 127, row = tile * 128 + i;
+        const int set = group >> 1, half = 32 * (group & 1);  // this group's columns
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         bool ok = true;
         float inv = 0.f, dhi = 0.f, dlo = 0.f;
 
-        // columns c .. c + 31 of S and dP
-        auto load = [&](int b, int c, uint32_t (&s)[32], uint32_t (&dp)[32]) {
-            uint32_t(*s2)[16] = reinterpret_cast<uint32_t(*)[16]>(s);
-            uint32_t(*d2)[16] = reinterpret_cast<uint32_t(*)[16]>(dp);
-            tmem_ld16(lanes + 128 * b + c, s2[0]);
-            tmem_ld16(lanes + 128 * b + c + 16, s2[1]);
-            tmem_ld16(lanes + 128 * b + 64 + c, d2[0]);
-            tmem_ld16(lanes + 128 * b + 64 + c + 16, d2[1]);
+        // columns c .. c + 15 of S and dP (complete after tmem_ld_wait)
+        auto load = [&](int b, int c, uint32_t (&s)[16], uint32_t (&dp)[16]) {
+            tmem_ld16(lanes + 128 * b + c, s);
+            tmem_ld16(lanes + 128 * b + 64 + c, dp);
+        };
+        // waits for the loads; ties the values to the wait, so that nothing that uses them moves above it
+        auto arrived = [&](uint32_t (&s)[16], uint32_t (&dp)[16]) {
             tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) asm volatile("" : "+r"(s[e]), "+r"(dp[e]));
         };
         // columns a row does not see count as a score of zero
-        auto mask = [&](int col0, uint32_t (&s)[32]) {
+        auto mask = [&](int col0, uint32_t (&s)[16]) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
+            for (int e = 0; e < 16; ++e)
                 if (KEYS ? col0 + e < row : col0 + e > row) s[e] = 0u;
         };
         auto on_diagonal = [&](int step) {
@@ -300,35 +302,39 @@ __global__ void __launch_bounds__(kThreads, 1)
 
         if (!KEYS) {
             double den = 0.0, num = 0.0;
-            for (int s = group; s < n1; s += kBufs) {
-                const int b = group, step = step_of(s);
-                if (!(ok = warp_wait(&bar[kSFull + b], (s / kBufs) & 1, err, 0x830))) break;
+            for (int s = set; s < n1; s += kSets) {
+                const int b = s % kBufs, step = step_of(s);
+                if (!(ok = warp_wait(&bar[kSFull + s % kFulls], (s / kFulls) & 1, err, 0x830))) break;
                 tc_fence_after();
                 F2 d2 = f2(0.f, 0.f), n2 = d2;
+                uint32_t sv[2][16], dv[2][16];
+                load(b, half, sv[0], dv[0]);
 #pragma unroll
-                for (int c = 0; c < 64; c += 32) {
-                    uint32_t sv[32], dv[32];
-                    load(b, c, sv, dv);
-                    if (on_diagonal(step)) mask(step * kStep + c, sv);
+                for (int c = 0; c < 2; ++c) {  // the next columns load while these are summed
+                    uint32_t(&x)[16] = sv[c & 1];
+                    uint32_t(&y)[16] = dv[c & 1];
+                    arrived(x, y);
+                    if (c == 0) load(b, half + 16, sv[1], dv[1]);
+                    if (on_diagonal(step)) mask(step * kStep + half + 16 * c, x);
                     if (tile == 0) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const double x = __uint_as_float(sv[e]), w = x * x;
+                        for (int e = 0; e < 16; ++e) {
+                            const double v = __uint_as_float(x[e]), w = v * v;
                             den += w;
-                            num = ::fma(w, (double)__uint_as_float(dv[e]), num);
+                            num = ::fma(w, (double)__uint_as_float(y[e]), num);
                         }
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            const F2 x = f2(sv[e], sv[e + 1]), w = mul(x, x);
+                        for (int e = 0; e < 16; e += 2) {
+                            const F2 v = f2(x[e], x[e + 1]), w = mul(v, v);
                             d2 = add(d2, w);
-                            n2 = fma(w, f2(dv[e], dv[e + 1]), n2);
+                            n2 = fma(w, f2(y[e], y[e + 1]), n2);
                         }
                     }
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar[kSRead + b]);
+                if (lane == 0) mbar_arrive(&bar[kRead + s % kStages]);
                 const float2 a = un(d2), c = un(n2);
                 den += (double)a.x + (double)a.y;
                 num += (double)c.x + (double)c.y;
@@ -340,15 +346,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = bar_sync_and(1, 32 * kWorkerWarps, ok);
             den = (double)p.eps;
             num = 0.0;
-            for (int g = 0; g < kBufs; ++g) {
+            for (int g = 0; g < kGroups; ++g) {
                 den += red[g * 256 + i];
                 num += red[g * 256 + 128 + i];
             }
             if (den != 0.0) {
-                const double delta = num / den;
+                const double minus = -num / den;
                 inv = (float)(1.0 / den);
-                dhi = (float)delta;
-                dlo = (float)(delta - (double)dhi);
+                dhi = (float)minus;
+                dlo = (float)(minus - (double)dhi);
             }
             if (ok && group == 0) {  // rows from T on: zeros, which make their keys' terms zero
                 const size_t at = (size_t)head * p.pitch + row;
@@ -359,9 +365,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         // dS / 2 = (s / den) (dP - delta), P = s (s / den); the factor 2 comes at the end
-        for (int s = n1 + (group - n1 % kBufs + kBufs) % kBufs; ok && s < n; s += kBufs) {
-            const int b = group, step = step_of(s);
-            if (!(ok = warp_wait(&bar[kSFull + b], (s / kBufs) & 1, err, 0x831))) break;
+        for (int s = n1 + ((n1 ^ set) & 1); ok && s < n; s += kSets) {
+            const int b = s % kBufs, step = step_of(s);
+            if (!(ok = warp_wait(&bar[kSFull + s % kFulls], (s / kFulls) & 1, err, 0x831))) break;
             tc_fence_after();
             // the statistics arrived with the step's tiles, before its products
             if (KEYS && !(ok = warp_wait(&bar[kTileFull + s % kStages], (s / kStages) & 1, err, 0x832)))
@@ -369,55 +375,62 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float *st = reinterpret_cast<const float *>(sm + L::STREAM + (s % kStages) * L::STAGE +
                                                               L::STATS);
             const bool few = KEYS ? step < 2 : tile == 0;  // rows that may see few keys
+            uint32_t sv[2][16], dv[2][16];
+            load(b, half, sv[0], dv[0]);
 #pragma unroll
-            for (int c = 0; c < 64; c += 32) {
-                uint32_t sv[32], dv[32];
-                load(b, c, sv, dv);
-                if (on_diagonal(step)) mask(step * kStep + c, sv);
-                uint32_t pk[16], dk[16];
+            for (int c = 0; c < 2; ++c) {
+                uint32_t(&x)[16] = sv[c & 1];
+                uint32_t(&y)[16] = dv[c & 1];
+                arrived(x, y);
+                if (c == 0) load(b, half + 16, sv[1], dv[1]);
+                if (on_diagonal(step)) mask(step * kStep + half + 16 * c, x);
+                uint32_t pk[8], dk[8];
 #pragma unroll
-                for (int e = 0; e < 32; e += 4) {
+                for (int e = 0; e < 16; e += 4) {
                     float4 iv = make_float4(inv, inv, inv, inv), dh = make_float4(dhi, dhi, dhi, dhi);
                     float4 dl = make_float4(dlo, dlo, dlo, dlo);
                     if (KEYS) {
-                        iv = *reinterpret_cast<const float4 *>(st + c + e);
-                        dh = *reinterpret_cast<const float4 *>(st + kStep + c + e);
-                        if (few) dl = *reinterpret_cast<const float4 *>(st + 2 * kStep + c + e);
+                        const float *at = st + half + 16 * c + e;
+                        iv = *reinterpret_cast<const float4 *>(at);
+                        dh = *reinterpret_cast<const float4 *>(at + kStep);
+                        if (few) dl = *reinterpret_cast<const float4 *>(at + 2 * kStep);
                     }
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const F2 x = f2(sv[e + 2 * h], sv[e + 2 * h + 1]);
-                        const F2 w = mul(x, h ? f2(iv.z, iv.w) : f2(iv.x, iv.y));
-                        F2 t = add(f2(dv[e + 2 * h], dv[e + 2 * h + 1]),
-                                   h ? f2(-dh.z, -dh.w) : f2(-dh.x, -dh.y));
-                        if (few) t = add(t, h ? f2(-dl.z, -dl.w) : f2(-dl.x, -dl.y));
+                        const F2 v = f2(x[e + 2 * h], x[e + 2 * h + 1]);
+                        const F2 w = mul(v, h ? f2(iv.z, iv.w) : f2(iv.x, iv.y));
+                        F2 t = add(f2(y[e + 2 * h], y[e + 2 * h + 1]),
+                                   h ? f2(dh.z, dh.w) : f2(dh.x, dh.y));
+                        if (few) t = add(t, h ? f2(dl.z, dl.w) : f2(dl.x, dl.y));
                         const float2 ds = un(mul(w, t));
                         dk[e / 2 + h] = pack_bf16x2(ds.x, ds.y);
                         if (KEYS) {
-                            const float2 pp = un(mul(x, w));
+                            const float2 pp = un(mul(v, w));
                             pk[e / 2 + h] = pack_bf16x2(pp.x, pp.y);
                         }
                     }
                 }
-                if (KEYS) tmem_st16(lanes + 128 * b + c / 2, pk);
-                tmem_st16(lanes + 128 * b + 64 + c / 2, dk);
+                // over columns of this group's half that have been read by now
+                if (KEYS) tmem_st8(lanes + 128 * b + half + 8 * c, pk);
+                tmem_st8(lanes + 128 * b + 64 + half + 8 * c, dk);
             }
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[kPFull + b]);
         }
-        // queries: both groups take half of dQ's columns; keys: group 0 dK, group 1 dV
-        if (ok) ok = warp_wait(&bar[kOutDone], 0, err, 0x833);
+        // half of the columns each: set 0 those of dQ or dK, set 1 (keys) those of dV
+        if (ok) ok = (KEYS || set == 0) && warp_wait(&bar[kOutDone], 0, err, 0x833);
         tc_fence_after();
-        constexpr int COLS = KEYS ? DH : DH / 2;
+        constexpr int COLS = DH / 2;
         const uint32_t col0 = L::ACC + group * COLS;
-        const float scale = KEYS && group == 1 ? 1.f : 2.f;
-        __nv_bfloat16 *out = KEYS && group == 1 ? p.out1 : p.out0;
+        const float scale = set == 0 ? 2.f : 1.f;
+        __nv_bfloat16 *out = set == 0 ? p.out0 : p.out1;
         uint4 *dst = reinterpret_cast<uint4 *>(out + ((size_t)head * p.T + row) * DH +
-                                               (KEYS ? 0 : group * COLS));
+                                               (group & 1) * COLS);
 #pragma unroll
         for (int c = 0; c < COLS; c += 16) {
+            if (!ok) break;
             uint32_t r[16];
             tmem_ld16(lanes + col0 + c, r);
             tmem_ld_wait();
@@ -426,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 8; ++e)
                 o[e] = pack_bf16x2(scale * __uint_as_float(r[2 * e]),
                                    scale * __uint_as_float(r[2 * e + 1]));
-            if (ok && row < p.T) {
+            if (row < p.T) {
                 dst[c / 8] = make_uint4(o[0], o[1], o[2], o[3]);
                 dst[c / 8 + 1] = make_uint4(o[4], o[5], o[6], o[7]);
             }
