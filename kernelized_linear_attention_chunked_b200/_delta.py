@@ -12,7 +12,7 @@ import torch
 
 from . import _binding as kb
 from ._binding import KataError, _check, _dt, _ptr, _workspace
-from ._calls import bind, on_stream, want
+from ._calls import bind, fits, on_stream, want
 
 _vp, _i, _f, _sz = C.c_void_p, C.c_int, C.c_float, C.c_size_t
 
@@ -33,17 +33,22 @@ def lib() -> C.CDLL:
 
 
 def _inputs(q, k, v, g, beta, ndim):
-    if q.dim() != ndim:
-        raise KataError(f"q has {q.dim()} dimensions, expected {ndim}")
-    dt = _dt(q)
     for name, t in (("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta)):
         if t is None:
             raise KataError(f"{name} must not be None")
-    want("q", q, None, None, q)
-    want("k", k, q.shape, q.dtype, q)
-    want("v", v, q.shape, q.dtype, q)
-    want("g", g, q.shape[:-1], torch.float32, q)
-    want("beta", beta, q.shape[:-1], torch.float32, q)
+    if q.dim() != ndim:
+        raise KataError(f"q has {q.dim()} dimensions, expected {ndim}")
+    dt = _dt(q)
+    shape, dtype, dev = q.shape, q.dtype, q.get_device()
+    rows = shape[:-1]
+    if not (dev >= 0 and fits(q, shape, dtype, dev) and fits(k, shape, dtype, dev)
+            and fits(v, shape, dtype, dev) and fits(g, rows, torch.float32, dev)
+            and fits(beta, rows, torch.float32, dev)):
+        want("q", q, None, None, q)
+        want("k", k, shape, dtype, q)
+        want("v", v, shape, dtype, q)
+        want("g", g, rows, torch.float32, q)
+        want("beta", beta, rows, torch.float32, q)
     return dt
 
 
@@ -88,7 +93,8 @@ def delta_decode_step(q, k, v, g, beta, S, scale: float | None = None, o=None, s
     B, H, d = q.shape
     if S is None:
         raise KataError("S must not be None")
-    want("S", S, (B, H, d, d), torch.float32, q)
+    if not fits(S, (B, H, d, d), torch.float32, q.get_device()):
+        want("S", S, (B, H, d, d), torch.float32, q)
     want("o", o, q.shape, q.dtype, q)
     scale = d ** -0.5 if scale is None else scale
     with on_stream(q, stream) as s:
