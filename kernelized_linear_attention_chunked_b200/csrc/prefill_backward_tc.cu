@@ -20,9 +20,9 @@
 // operand for the scores and an MN-major one for the outputs.
 //
 // Warp roles: two sets of workers on alternate steps, each two groups of four
-// warps with half the step's columns (thread = row), an issuer of the score products, one of the output
-// products, a TMA producer. Every wait is bounded. A step takes two commits: each
-// costs the tensor pipe about as much as two MMAs.
+// warps with half the step's columns (thread = row), two issuers of the score products (alternate steps: one
+// thread needs longer for a step's waits and MMAs than the tensor pipe), one of the
+// output products, a TMA producer. Every wait is bounded.
 //
 // Rounding: scores, dP, den and delta are fp32 or wider; P and dS are rounded
 // to bf16 as operands (2^-9 of each term), the same size as the rounding of the
@@ -40,12 +40,12 @@ using namespace tc;
 
 constexpr int kStep = 64;    // streamed rows per step
 constexpr int kBufs = 3;     // S | dP buffers
-constexpr int kStages = 6;   // streamed tiles in flight
+constexpr int kStages = 6;   // streamed tiles in flight, a multiple of kBufs and kSets
 constexpr int kSets = 2;     // sets of workers, on alternate steps
 constexpr int kGroups = 2 * kSets;  // a set is two groups of four warps, half the columns each
 constexpr int kWorkerWarps = 4 * kGroups;
-constexpr int kFulls = kBufs * kSets;  // a barrier per (buffer, set): each is awaited in every phase
-constexpr int kThreads = 32 * (kWorkerWarps + 3);
+static_assert(kStages == 2 * kBufs && kStages % kSets == 0, "slots of a step");
+constexpr int kThreads = 32 * (kWorkerWarps + 4);
 
 struct BwdParams {
     int T, tiles, steps;  // tokens; 128-row tiles and 64-row steps per head
@@ -58,17 +58,14 @@ struct BwdParams {
 
 enum BwdBar {
     kOwn = 0,                     // the CTA's own tiles landed
-    kTileFull = 1,                 // stages: a step's tiles (and statistics) landed
-    kSFull = kTileFull + kStages,  // (buffer, set): S and dP are in tensor memory
-    kPFull = kSFull + kFulls,      // buffers: P and dS are written (8 arrivals)
-    // stages: a step is over, its tiles and its buffer free: in the first walk when
-    // the workers have read S and dP (8 arrivals), in the second when the output
-    // products completed
-    kRead = kPFull + kBufs,
-    kDone = kRead + kStages,
-    kOutDone = kDone + kStages,
-    kSDrain,
-    kODrain,
+    // one per stage, step s using stage s % kStages in phase s / kStages:
+    kTileFull = 1,                 // its tiles (and statistics) landed
+    kSFull = kTileFull + kStages,  // S and dP are in tensor memory
+    kOver = kSFull + kStages,      // its tiles and its buffer are free (9 arrivals)
+    kPFull = kOver + kStages,      // second walk: P and dS are written (8 arrivals)
+    kOutDone = kPFull + kStages,
+    kSDrain,                   // two issuers
+    kODrain = kSDrain + kSets,
     kBars
 };
 
@@ -90,7 +87,7 @@ struct BwdCfg {
     static constexpr uint32_t ACC = 128 * kBufs;             // first accumulator column
     static_assert(ACC + 2 * DH <= 512, "tensor-memory budget");
     static_assert(SLOT % 8 == 0 && BAR % 8 == 0, "barriers");
-    static constexpr int S_WARP = kWorkerWarps, O_WARP = S_WARP + 1, TMA_WARP = O_WARP + 1;
+    static constexpr int S_WARP = kWorkerWarps, O_WARP = S_WARP + kSets, TMA_WARP = O_WARP + 1;
 };
 
 __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int x, int y, int z,
@@ -157,17 +154,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int n1 = KEYS ? 0 : walk;  // steps of the first (statistics) walk
     const int n = n1 + walk;
     auto step_of = [&](int s) { return first + (s < n1 ? s : s - n1); };
-    // which use of its kind step s makes of slot s % m, counted in the second walk alone
-    auto second_use = [&](int s, int m) { return (s - n1 - (s % m - n1 % m + m) % m) / m; };
-    auto wait_over = [&](int u, unsigned int code) {  // step u is over
-        return u < n1 ? mbar_wait(&bar[kRead + u % kStages], (u / kStages) & 1, err, code)
-                      : mbar_wait(&bar[kDone + u % kStages], second_use(u, kStages) & 1, err, code);
+    // step s is over: the workers have read its S and dP and, in the second walk,
+    // the output products have completed
+    auto wait_over = [&](int st, int par, unsigned int code) {
+        return mbar_wait(&bar[kOver + st], par, err, code);
     };
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kBars; ++i) {
-            const bool workers = (i >= kPFull && i < kPFull + kBufs) || (i >= kRead && i < kRead + kStages);
-            mbar_init(&bar[i], workers ? 8 : 1);
+            const bool over = i >= kOver && i < kOver + kStages;
+            const bool full = i >= kPFull && i < kPFull + kStages;
+            mbar_init(&bar[i], over ? 9 : full ? 8 : 1);
         }
         cta_abort_clear();
         fence_barrier_init();
@@ -194,9 +191,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             &bar[kOwn]);
             }
             int issued = 0;
-            for (int s = 0; s < n; ++s) {
-                const int st = s % kStages;
-                if (s >= kStages && !wait_over(s - kStages, 0x801)) break;
+            for (int s = 0, st = 0, par = 1; s < n; ++s) {
+                if (s >= kStages && !wait_over(st, par, 0x801)) break;
                 uint8_t *d = sm + L::STREAM + st * L::STAGE;
                 const int y = step_of(s) * kStep;
                 mbar_arrive_expect_tx(&bar[kTileFull + st], 2 * L::TILE + (KEYS ? 3 * 4 * kStep : 0));
@@ -209,28 +205,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                     bulk_load(d + L::STATS + 8 * kStep, p.dlo + at, 4 * kStep, &bar[kTileFull + st]);
                 }
                 ++issued;
+                if (++st == kStages) st = 0, par ^= 1;
             }
             // no copy may be in flight when the CTA exits: the last one on each barrier
             mbar_drain(&bar[kOwn], 0, err, 0x802);
             for (int s = issued - kStages < 0 ? 0 : issued - kStages; s < issued; ++s)
                 mbar_drain(&bar[kTileFull + s % kStages], (s / kStages) & 1, err, 0x803);
         }
-    } else if (warp == L::S_WARP) {
+    } else if (warp >= L::S_WARP && warp < L::S_WARP + kSets) {
         if (lane == 0) {
-            // S = own0 str0^T and dP = own1 str1^T into buffer s % kBufs
+            // S = own0 str0^T and dP = own1 str1^T into buffer s % kBufs, every kSets-th step
+            const int me = warp - L::S_WARP;
             const uint32_t id = idesc_bf16(128, kStep, 0, 0);
-            const uint32_t own = smem_u32(sm), str = own + L::STREAM;
+            const uint32_t own = smem_u32(sm);
             const uint64_t a0 = smem_desc(own, 16, 8 * L::ROW, L::SW);
             const uint64_t a1 = smem_desc(own + L::OWN, 16, 8 * L::ROW, L::SW);
-            const uint64_t db = smem_desc(str, 16, 8 * L::ROW, L::SW);
+            const uint64_t db = smem_desc(own + L::STREAM, 16, 8 * L::ROW, L::SW);
             bool ok = mbar_wait(&bar[kOwn], 0, err, 0x810);
-            for (int s = 0; ok && s < n; ++s) {
-                const int b = s % kBufs, st = s % kStages;
-                ok = (s < kBufs || wait_over(s - kBufs, 0x811)) &&
-                     mbar_wait(&bar[kTileFull + st], (s / kStages) & 1, err, 0x812);
+            for (int s = me, st = me, par = 0; ok && s < n; s += kSets) {
+                const bool up = st >= kBufs;  // step s - kBufs used the buffer last
+                ok = (s < kBufs || wait_over(up ? st - kBufs : st + kBufs, up ? par : par ^ 1, 0x811)) &&
+                     mbar_wait(&bar[kTileFull + st], par, err, 0x812);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t d = tmem + 128 * b;
+                const uint32_t d = tmem + 128 * (up ? st - kBufs : st);
                 const uint64_t t0 = db + (uint32_t)(st * (L::STAGE >> 4)), t1 = t0 + (L::TILE >> 4);
 #pragma unroll
                 for (int kk = 0; kk < DH / 16; ++kk)  // 16 columns = 32 bytes on
@@ -238,10 +236,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int kk = 0; kk < DH / 16; ++kk)
                     mma_ss(d + 64, a1 + 2 * kk, t1 + 2 * kk, id, kk > 0);
-                mma_commit(&bar[kSFull + s % kFulls]);
+                mma_commit(&bar[kSFull + st]);
+                if (s < n1) mbar_arrive(&bar[kOver + st]);  // in the output products' place
+                if ((st += kSets) >= kStages) st -= kStages, par ^= 1;
             }
-            mma_commit(&bar[kSDrain]);
-            mbar_drain(&bar[kSDrain], 0, err, 0x814);
+            mma_commit(&bar[kSDrain + me]);
+            mbar_drain(&bar[kSDrain + me], 0, err, 0x814);
         }
     } else if (warp == L::O_WARP) {
         if (lane == 0) {
@@ -249,14 +249,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t id = idesc_bf16(128, DH, 0, 1);
             const uint64_t db = smem_desc(smem_u32(sm) + L::STREAM, 16, 8 * L::ROW, L::SW);
             bool ok = true;
-            for (int s = n1; s < n; ++s) {
-                const int b = s % kBufs, st = s % kStages;
-                ok = mbar_wait(&bar[kPFull + b], second_use(s, kBufs) & 1, err, 0x820);
+            uint32_t phases = 0;  // a bit per stage: kPFull is used in the second walk only
+            for (int s = n1, st = n1 % kStages; s < n; ++s) {
+                ok = mbar_wait(&bar[kPFull + st], (phases >> st) & 1, err, 0x820);
                 if (!ok) break;
+                phases ^= 1u << st;
                 tc_fence_after();
                 const uint64_t t0 = db + (uint32_t)(st * (L::STAGE >> 4)), t1 = t0 + (L::TILE >> 4);
+                const uint32_t buf = tmem + 128 * (st >= kBufs ? st - kBufs : st);
                 // 16 rows on; a group's columns lie in its own half
-                auto a = [&](int kk) { return tmem + 128 * b + 8 * kk + (kk < 2 ? 0 : 16); };
+                auto a = [&](int kk) { return buf + 8 * kk + (kk < 2 ? 0 : 16); };
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
                     mma_ts(tmem + L::ACC, a(kk) + 64, t0 + kk * L::ROW, id, s > n1 || kk > 0);
@@ -265,7 +267,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int kk = 0; kk < 4; ++kk)
                         mma_ts(tmem + L::ACC + DH, a(kk), t1 + kk * L::ROW, id, s > n1 || kk > 0);
                 }
-                mma_commit(&bar[kDone + st]);
+                mma_commit(&bar[kOver + st]);
+                if (++st == kStages) st = 0;
             }
             if (ok) mma_commit(&bar[kOutDone]);
             mma_commit(&bar[kODrain]);
@@ -278,6 +281,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         bool ok = true;
         float inv = 0.f, dhi = 0.f, dlo = 0.f;
+        int s = set, st = set, par = 0;  // this set's steps
+        auto next = [&] {
+            s += kSets;
+            if ((st += kSets) >= kStages) st -= kStages, par ^= 1;
+        };
 
         // columns c .. c + 15 of S and dP (complete after tmem_ld_wait)
         auto load = [&](int b, int c, uint32_t (&s)[16], uint32_t (&dp)[16]) {
@@ -302,9 +310,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
         if (!KEYS) {
             double den = 0.0, num = 0.0;
-            for (int s = set; s < n1; s += kSets) {
-                const int b = s % kBufs, step = step_of(s);
-                if (!(ok = warp_wait(&bar[kSFull + s % kFulls], (s / kFulls) & 1, err, 0x830))) break;
+            for (; s < n1; next()) {
+                const int b = st >= kBufs ? st - kBufs : st, step = step_of(s);
+                if (!(ok = warp_wait(&bar[kSFull + st], par, err, 0x830))) break;
                 tc_fence_after();
                 F2 d2 = f2(0.f, 0.f), n2 = d2;
                 uint32_t sv[2][16], dv[2][16];
@@ -334,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar[kRead + s % kStages]);
+                if (lane == 0) mbar_arrive(&bar[kOver + st]);
                 const float2 a = un(d2), c = un(n2);
                 den += (double)a.x + (double)a.y;
                 num += (double)c.x + (double)c.y;
@@ -365,15 +373,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         // dS / 2 = (s / den) (dP - delta), P = s (s / den); the factor 2 comes at the end
-        for (int s = n1 + ((n1 ^ set) & 1); ok && s < n; s += kSets) {
-            const int b = s % kBufs, step = step_of(s);
-            if (!(ok = warp_wait(&bar[kSFull + s % kFulls], (s / kFulls) & 1, err, 0x831))) break;
+        for (; ok && s < n; next()) {
+            const int b = st >= kBufs ? st - kBufs : st, step = step_of(s);
+            if (!(ok = warp_wait(&bar[kSFull + st], par, err, 0x831))) break;
             tc_fence_after();
             // the statistics arrived with the step's tiles, before its products
-            if (KEYS && !(ok = warp_wait(&bar[kTileFull + s % kStages], (s / kStages) & 1, err, 0x832)))
-                break;
-            const float *st = reinterpret_cast<const float *>(sm + L::STREAM + (s % kStages) * L::STAGE +
-                                                              L::STATS);
+            if (KEYS && !(ok = warp_wait(&bar[kTileFull + st], par, err, 0x832))) break;
+            const float *stats = reinterpret_cast<const float *>(sm + L::STREAM + st * L::STAGE + L::STATS);
             const bool few = KEYS ? step < 2 : tile == 0;  // rows that may see few keys
             uint32_t sv[2][16], dv[2][16];
             load(b, half, sv[0], dv[0]);
@@ -390,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float4 iv = make_float4(inv, inv, inv, inv), dh = make_float4(dhi, dhi, dhi, dhi);
                     float4 dl = make_float4(dlo, dlo, dlo, dlo);
                     if (KEYS) {
-                        const float *at = st + half + 16 * c + e;
+                        const float *at = stats + half + 16 * c + e;
                         iv = *reinterpret_cast<const float4 *>(at);
                         dh = *reinterpret_cast<const float4 *>(at + kStep);
                         if (few) dl = *reinterpret_cast<const float4 *>(at + 2 * kStep);
@@ -417,7 +423,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar[kPFull + b]);
+            if (lane == 0) {
+                mbar_arrive(&bar[kPFull + st]);
+                mbar_arrive(&bar[kOver + st]);
+            }
         }
         // half of the columns each: set 0 those of dQ or dK, set 1 (keys) those of dV
         if (ok) ok = (KEYS || set == 0) && warp_wait(&bar[kOutDone], 0, err, 0x833);
