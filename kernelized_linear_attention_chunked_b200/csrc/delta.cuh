@@ -480,9 +480,10 @@ __global__ void __launch_bounds__(256) delta_chain(Args p, Scratch w) {
             for (int kt = 0; kt < D / 8; ++kt) {
                 FragA<2> a;
                 a.set(make_float2(W[kt].x, W[kt].y), make_float2(W[kt].z, W[kt].w));
+                float2 b[NT];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    mma_step<2, 2>(acc[nt], a, pair<false>(sS, ST, 8 * nt + gr, 8 * kt + t2));
+                for (int nt = 0; nt < NT; ++nt) b[nt] = pair<false>(sS, ST, 8 * nt + gr, 8 * kt + t2);
+                mma_step<2, 2, NT>(acc, a, b);
             }
             const float k0 = coef[kC + m0 + gr], k1 = coef[kC + m0 + gr + 8];
 #pragma unroll
@@ -587,9 +588,10 @@ __global__ void __launch_bounds__(256) delta_chain(Args p, Scratch w) {
                 if (kt >= 2 * ((warp & 3) + 1)) continue;
                 FragA<TI> a;
                 a.set(make_float2(M[kt].x, M[kt].y), make_float2(M[kt].z, M[kt].w));
+                float2 b[NT];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    mma_step<TI, TI>(o[nt], a, pair<false>(sY, ST, 8 * nt + gr, 8 * kt + t2));
+                for (int nt = 0; nt < NT; ++nt) b[nt] = pair<false>(sY, ST, 8 * nt + gr, 8 * kt + t2);
+                mma_step<TI, TI, NT>(o, a, b);
             }
             Tin *od = static_cast<Tin *>(p.o);
 #pragma unroll

@@ -31,7 +31,7 @@ namespace tf {
 
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                     uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -41,7 +41,7 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
 // c = A B, on a zero accumulator.
 __device__ __forceinline__ void mma0(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                      uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%10,%10,%10,%10};"
         : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
@@ -75,30 +75,43 @@ struct FragA {
 // toward zero, so a long sum kept in it drifts. The eight terms of a step are
 // summed there from zero and added to acc by an ordinary rounded addition:
 // the error of a 64-term product falls from 5e-7 to 1.5e-7 of its norm.
-template <int TA, int TB>
-__device__ __forceinline__ void mma_step(float (&acc)[4], const FragA<TA> &a, float2 b) {
-    uint32_t h0, h1, l0, l1;
-    float t[4];
-    if (TB == 2) {
-        split(b.x, h0, l0);
-        split(b.y, h1, l1);
-        mma0(t, a.hi, l0, l1);
-    } else {
-        h0 = __float_as_uint(b.x);
-        h1 = __float_as_uint(b.y);
-    }
-    if (TA == 2) {
-        if (TB == 2)
-            mma(t, a.lo, h0, h1);
-        else
-            mma0(t, a.lo, h0, h1);
-    }
-    if (TA == 2 || TB == 2)
-        mma(t, a.hi, h0, h1);
-    else
-        mma0(t, a.hi, h0, h1);
+//
+// The parts of one tile depend on each other (20.6 cycles apart), so a step goes
+// part by part over all NT tiles.
+template <int TA, int TB, int NT>
+__device__ __forceinline__ void mma_step(float (&acc)[NT][4], const FragA<TA> &a,
+                                         const float2 (&b)[NT], int nt_end = NT) {
+    float t[NT][4];
+    uint32_t h0[NT], h1[NT], l0[NT], l1[NT];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] += t[i];
+    for (int n = 0; n < NT; ++n) {
+        if (n >= nt_end) continue;
+        if (TB == 2) {
+            split(b[n].x, h0[n], l0[n]);
+            split(b[n].y, h1[n], l1[n]);
+            mma0(t[n], a.hi, l0[n], l1[n]);
+        } else {
+            h0[n] = __float_as_uint(b[n].x);
+            h1[n] = __float_as_uint(b[n].y);
+            mma0(t[n], TA == 2 ? a.lo : a.hi, h0[n], h1[n]);
+        }
+    }
+    if (TA == 2 && TB == 2) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            if (n < nt_end) mma(t[n], a.lo, h0[n], h1[n]);
+    }
+    if (TA == 2 || TB == 2) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            if (n < nt_end) mma(t[n], a.hi, h0[n], h1[n]);
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        if (n >= nt_end) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[n][i] += t[n][i];
+    }
 }
 
 // Two k neighbours of an operand in shared memory, as floats. `K` says that k
@@ -130,9 +143,15 @@ __device__ __forceinline__ void gemm(float (&acc)[NT][4], int kt0, int kt1, FA f
         const int k = 8 * kt + t2;
         FragA<TA> a;
         a.set(fa(g, k), fa(g + 8, k));
+        constexpr int G = NT % 2 == 0 ? 2 : 1;  // tiles at a time: more cost registers
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-            if (nt < nt_end) mma_step<TA, TB>(acc[nt], a, fb(8 * nt + g, k));
+        for (int n0 = 0; n0 < NT; n0 += G) {
+            float2 b[G];
+#pragma unroll
+            for (int nt = 0; nt < G; ++nt)
+                if (n0 + nt < nt_end) b[nt] = fb(8 * (n0 + nt) + g, k);
+            mma_step<TA, TB, G>(*reinterpret_cast<float(*)[G][4]>(&acc[n0]), a, b, nt_end - n0);
+        }
     }
 }
 
