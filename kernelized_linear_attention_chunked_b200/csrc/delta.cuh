@@ -86,6 +86,14 @@ __device__ __forceinline__ void cp16(void *dst, const void *src, bool have) {
                  : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// waits until at most N of this thread's groups are on their way
+template <int N>
+__device__ __forceinline__ void cp_wait_ahead() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void prefetch_l2(const void *p, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Rows [t0, t0 + ROWS) of the [nrows, D] matrix that starts at row `row0`, columns [c0, c0 + N), to
@@ -155,18 +163,18 @@ __device__ __forceinline__ void invert(const float *sA, float *sX, int warp, int
         const int r0 = 32 * (warp >> 1), c = r0 + 8 * (warp & 1);
         float acc[1][4];
         clear(acc);
-        gemm<2, 2, 1>(
-            acc, 0, 2, [&](int m, int k) { return pair<true>(sA + (r0 + 16) * kTS + r0, kTS, m, k); },
-            [&](int n, int k) { return pair<false>(sX + r0 * kTS + c, kTS, n, k); });
+        gemm<2, 2, 1, false>(
+            acc, 0, 1, [&](int m, int k) { return quad<true, false>(sA + (r0 + 16) * kTS + r0, kTS, m, k); },
+            [&](int n, int k) { return quad<false, false>(sX + r0 * kTS + c, kTS, n, k); });
         float *P = sX + r0 * kTS + c + 16;
         *reinterpret_cast<float2 *>(P + g * kTS + t2) = make_float2(acc[0][0], acc[0][1]);
         *reinterpret_cast<float2 *>(P + (g + 8) * kTS + t2) = make_float2(acc[0][2], acc[0][3]);
         __syncwarp();
         clear(acc);
-        gemm<2, 2, 1>(
-            acc, 0, 2,
-            [&](int m, int k) { return pair<true>(sX + (r0 + 16) * kTS + r0 + 16, kTS, m, k); },
-            [&](int n, int k) { return pair<false>(P, kTS, n, k); });
+        gemm<2, 2, 1, false>(
+            acc, 0, 1,
+            [&](int m, int k) { return quad<true, false>(sX + (r0 + 16) * kTS + r0 + 16, kTS, m, k); },
+            [&](int n, int k) { return quad<false, false>(P, kTS, n, k); });
         float *O = sX + (r0 + 16) * kTS + c;
         *reinterpret_cast<float2 *>(O + g * kTS + t2) = make_float2(-acc[0][0], -acc[0][1]);
         *reinterpret_cast<float2 *>(O + (g + 8) * kTS + t2) = make_float2(-acc[0][2], -acc[0][3]);
@@ -179,10 +187,10 @@ __device__ __forceinline__ void invert(const float *sA, float *sX, int warp, int
         for (int mt = 0; mt < 2; ++mt) {
             float acc[1][4];
             clear(acc);
-            gemm<2, 2, 1>(  // X11's rows above its diagonal blocks hold no values
-                acc, warp >= 2 ? 2 : 0, 4,
-                [&](int m, int k) { return pair<true>(sA + (32 + 16 * mt) * kTS, kTS, m, k); },
-                [&](int n, int k) { return pair<false>(sX + c, kTS, n, k); });
+            gemm<2, 2, 1, false>(  // X11's rows above its diagonal blocks hold no values
+                acc, warp >= 2 ? 1 : 0, 2,
+                [&](int m, int k) { return quad<true, false>(sA + (32 + 16 * mt) * kTS, kTS, m, k); },
+                [&](int n, int k) { return quad<false, false>(sX + c, kTS, n, k); });
             *reinterpret_cast<float2 *>(P + (16 * mt + g) * kTS + t2) =
                 make_float2(acc[0][0], acc[0][1]);
             *reinterpret_cast<float2 *>(P + (16 * mt + g + 8) * kTS + t2) =
@@ -193,10 +201,10 @@ __device__ __forceinline__ void invert(const float *sA, float *sX, int warp, int
         for (int mt = 0; mt < 2; ++mt) {
             float acc[1][4];
             clear(acc);
-            gemm<2, 2, 1>(
-                acc, 0, 2 * (mt + 1),
-                [&](int m, int k) { return pair<true>(sX + (32 + 16 * mt) * kTS + 32, kTS, m, k); },
-                [&](int n, int k) { return pair<false>(P, kTS, n, k); });
+            gemm<2, 2, 1, false>(
+                acc, 0, mt + 1,
+                [&](int m, int k) { return quad<true, false>(sX + (32 + 16 * mt) * kTS + 32, kTS, m, k); },
+                [&](int n, int k) { return quad<false, false>(P, kTS, n, k); });
             float *O = sX + (32 + 16 * mt) * kTS + c;
             *reinterpret_cast<float2 *>(O + g * kTS + t2) = make_float2(-acc[0][0], -acc[0][1]);
             *reinterpret_cast<float2 *>(O + (g + 8) * kTS + t2) =
@@ -215,7 +223,7 @@ struct PrepSmem {
     static constexpr int A = DO + (BACK ? IN : 0);
     static constexpr int X = A + kC * kTS * 4, M = X + kC * kTS * 4;
     static constexpr int G = M + (BACK ? kC * kTS * 4 : 0);
-    static constexpr int COEF = G + kC * 8;  // beta, a, c
+    static constexpr int COEF = G + kC * 8;  // beta, a, beta c
     static constexpr int BYTES = COEF + 3 * kC * 4;
 };
 
@@ -241,7 +249,7 @@ __global__ void __launch_bounds__(128) delta_prep(Args p, Scratch f, Scratch r) 
     float *sA = reinterpret_cast<float *>(sm + L::A), *sX = reinterpret_cast<float *>(sm + L::X);
     float *sM = reinterpret_cast<float *>(sm + L::M), *sP = reinterpret_cast<float *>(sm + L::V);
     double *G = reinterpret_cast<double *>(sm + L::G);
-    float *beta = reinterpret_cast<float *>(sm + L::COEF), *ca = beta + kC, *cc = ca + kC;
+    float *beta = reinterpret_cast<float *>(sm + L::COEF), *ca = beta + kC, *bc = ca + kC;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int gr = lane >> 2, t2 = 2 * (lane & 3);
     const size_t ch = blockIdx.x;  // head * nc + chunk
@@ -266,10 +274,10 @@ __global__ void __launch_bounds__(128) delta_prep(Args p, Scratch f, Scratch r) 
     if (tid < kC) {
         const float a = expf((float)G[tid]), c = expf((float)(G[kC - 1] - G[tid]));
         ca[tid] = a;
-        cc[tid] = c;
+        bc[tid] = beta[tid] * c;
         float *cf = f.coef + ch * kCoef;
         cf[tid] = p.scale * a;
-        cf[kC + tid] = beta[tid] * c;
+        cf[kC + tid] = bc[tid];
         if (tid == kC - 1) cf[2 * kC] = a;
         if (BACK) {
             float *cr = r.coef + ch * kCoef;
@@ -284,13 +292,13 @@ __global__ void __launch_bounds__(128) delta_prep(Args p, Scratch f, Scratch r) 
     float kk[8][4], qk[8][4];
     clear(kk);
     clear(qk);
-    gemm<TI, TI, 8>(
-        kk, 0, D / 8, [&](int m, int k) { return pair<true>(sK + m0 * KS, KS, m, k); },
-        [&](int n, int k) { return pair<true>(sK, KS, n, k); }, nt_end);
+    gemm<TI, TI, 8, true>(
+        kk, 0, D / 16, [&](int m, int k) { return quad<true, true>(sK + m0 * KS, KS, m, k); },
+        [&](int n, int k) { return quad<true, true>(sK, KS, n, k); }, nt_end);
     if (BACK || p.o)
-        gemm<TI, TI, 8>(
-            qk, 0, D / 8, [&](int m, int k) { return pair<true>(sQ + m0 * KS, KS, m, k); },
-            [&](int n, int k) { return pair<true>(sK, KS, n, k); }, nt_end);
+        gemm<TI, TI, 8, true>(
+            qk, 0, D / 16, [&](int m, int k) { return quad<true, true>(sQ + m0 * KS, KS, m, k); },
+            [&](int n, int k) { return quad<true, true>(sK, KS, n, k); }, nt_end);
 #pragma unroll
     for (int nt = 0; nt < 8; ++nt) {
         if (nt >= nt_end) continue;
@@ -317,27 +325,26 @@ __global__ void __launch_bounds__(128) delta_prep(Args p, Scratch f, Scratch r) 
 
     float acc[D / 8][4];
     clear(acc);
-    gemm<2, TI, D / 8>(  // X V
-        acc, 0, nt_end, [&](int m, int k) { return pair<true>(sX + m0 * kTS, kTS, m, k); },
-        [&](int n, int k) { return pair<false>(sV, KS, n, k); });
+    gemm<2, TI, D / 8, false>(  // X V
+        acc, 0, warp + 1, [&](int m, int k) { return quad<true, false>(sX + m0 * kTS, kTS, m, k); },
+        [&](int n, int k) { return quad<false, false>(sV, KS, n, k); });
     store_frags<D>(f.Y + ch * (kC * D), acc, warp, lane);
     clear(acc);
-    gemm<2, TI, D / 8>(  // X diag(a) K
-        acc, 0, nt_end,
+    gemm<2, TI, D / 8, false>(  // X diag(a) K
+        acc, 0, warp + 1,
         [&](int m, int k) {
-            const float2 x = pair<true>(sX + m0 * kTS, kTS, m, k);
-            return make_float2(x.x * ca[k], x.y * ca[k + 1]);
+            return scaled<false>(quad<true, false>(sX + m0 * kTS, kTS, m, k), ca, k);
         },
-        [&](int n, int k) { return pair<false>(sK, KS, n, k); });
+        [&](int n, int k) { return quad<false, false>(sK, KS, n, k); });
     store_frags<D>(f.W + ch * (kC * D), acc, warp, lane);
     if (!BACK) return;
 
     // Z0 = X^T (scale diag(beta) M^T dO), W' = X^T diag(beta c) K: the
     // transposed factors reach from a row's own block to the last one
     clear(acc);
-    gemm<2, TI, D / 8>(
-        acc, 2 * warp, 8, [&](int m, int k) { return pair<false>(sM + m0, kTS, m, k); },
-        [&](int n, int k) { return pair<false>(sO, KS, n, k); });
+    gemm<2, TI, D / 8, false>(
+        acc, warp, 4, [&](int m, int k) { return quad<false, false>(sM + m0, kTS, m, k); },
+        [&](int n, int k) { return quad<false, false>(sO, KS, n, k); });
     __syncthreads();  // every warp has read V
     {
         const float s0 = p.scale * beta[m0 + gr], s1 = p.scale * beta[m0 + gr + 8];
@@ -351,78 +358,115 @@ __global__ void __launch_bounds__(128) delta_prep(Args p, Scratch f, Scratch r) 
     }
     __syncthreads();
     clear(acc);
-    gemm<2, 2, D / 8>(
-        acc, 2 * warp, 8, [&](int m, int k) { return pair<false>(sX + m0, kTS, m, k); },
-        [&](int n, int k) { return pair<false>(sP, KS, n, k); });
+    gemm<2, 2, D / 8, false>(
+        acc, warp, 4, [&](int m, int k) { return quad<false, false>(sX + m0, kTS, m, k); },
+        [&](int n, int k) { return quad<false, false>(sP, KS, n, k); });
     store_frags<D>(r.Y + ch * (kC * D), acc, warp, lane);
     clear(acc);
-    gemm<2, TI, D / 8>(
-        acc, 2 * warp, 8,
+    gemm<2, TI, D / 8, false>(
+        acc, warp, 4,
         [&](int m, int k) {
-            const float2 x = pair<false>(sX + m0, kTS, m, k);
-            return make_float2(x.x * (beta[k] * cc[k]), x.y * (beta[k + 1] * cc[k + 1]));
+            return scaled<false>(quad<false, false>(sX + m0, kTS, m, k), bc, k);
         },
-        [&](int n, int k) { return pair<false>(sK, KS, n, k); });
+        [&](int n, int k) { return quad<false, false>(sK, KS, n, k); });
     store_frags<D>(r.W + ch * (kC * D), acc, warp, lane);
 }
 
 template <typename Tin, int D, int NS, bool REV>
 struct ChainSmem {
     static constexpr int KS = row_stride<D>();
-    static constexpr int ST = NS + 4;  // B operands' row stride: rows 2t start 8 t (24 t) banks on
+    static constexpr int SP = NS + 2;  // row stride of {hi, lo} pairs: rows 2t start 8t banks on
+    static constexpr int ST = NS + 4;  // row stride of fp32 B operands: rows 2t start 8t (24t) banks on
     static constexpr int DS = NS + 8;  // row stride of the dO slice
     static constexpr int IN = kC * KS * (int)sizeof(Tin);
-    static constexpr int S = 0, Y = S + D * ST * 4, YC = Y + kC * ST * 4;
-    static constexpr int GQ = YC + kC * ST * 4;  // REV: Q^T diag(scale a) dO
+    static constexpr int S = 0, YC = S + D * SP * 8, Y = YC + kC * SP * 8;
+    static constexpr int GQ = Y + kC * ST * 4;  // REV: Q^T diag(scale a) dO
     static constexpr int STAGE = GQ + (REV ? D * ST * 4 : 0);
     // one stage: K, Q, coefficients, (REV) the dO slice
     static constexpr int K = 0, Q = IN, COEF = 2 * IN, DO = COEF + kCoef * 4;
     static constexpr int STAGE_BYTES = DO + (REV ? kC * DS * (int)sizeof(Tin) : 0);
-    static constexpr int BYTES = STAGE + 2 * STAGE_BYTES;
+    // as many as fit, up to four: three chunks ahead
+    static constexpr int FIT = (227 * 1024 - STAGE) / STAGE_BYTES;
+    static constexpr int STAGES = FIT < 4 ? FIT : 4;
+    static_assert(STAGES >= 2, "a stage in use and one on its way");
+    static constexpr int BYTES = STAGE + STAGES * STAGE_BYTES;
 };
+
+// {hi, lo} of two neighbours, 16 bytes.
+__device__ __forceinline__ float4 cut2(float x, float y) {
+    uint32_t h0, l0, h1, l1;
+    tf::split(x, h0, l0);
+    tf::split(y, h1, l1);
+    return make_float4(__uint_as_float(h0), __uint_as_float(l0), __uint_as_float(h1),
+                       __uint_as_float(l1));
+}
 
 // The walk over the chunks, one CTA per (head, NS value columns). Warps 0-3
 // carry the chain: they hold the state in registers (fp32, D / 4 rows each)
 // and take two dependent products per chunk. Warps 4-7 take the products that
-// hang off it: the outputs (forward) or Q^T dO (REV). K and Q arrive by
-// asynchronous copies one chunk ahead; W, XV and M come straight from global
-// memory into the fragments that use them, also ahead.
+// hang off it: the outputs (forward) or Q^T dO (REV). Warp 8 brings K, Q and
+// the coefficients by asynchronous copies up to three chunks ahead, and calls
+// the next chunks' W, XV and M into L2; those come straight from there into
+// the fragments that use them, one chunk ahead. The state and the errors, B
+// operands that four warps read, are cut into their tf32 parts by the warp
+// that writes them.
 template <typename Tin, int D, int NS, bool REV, bool KEEP>
-__global__ void __launch_bounds__(256) delta_chain(Args p, Scratch w) {
+__global__ void __launch_bounds__(288, 1) delta_chain(Args p, Scratch w) {
     using namespace tf;
     using L = ChainSmem<Tin, D, NS, REV>;
-    constexpr int KS = L::KS, ST = L::ST, NT = NS / 8, TI = Parts<Tin>::N;
+    constexpr int KS = L::KS, SP = L::SP, ST = L::ST, NT = NS / 8, TI = Parts<Tin>::N;
     constexpr int MT = D >= 64 ? D / 64 : 1;  // 16-row tiles of the state per chain warp
     extern __shared__ __align__(16) uint8_t sm[];
-    float *sS = reinterpret_cast<float *>(sm + L::S), *sY = reinterpret_cast<float *>(sm + L::Y);
-    float *sYc = reinterpret_cast<float *>(sm + L::YC), *sG = reinterpret_cast<float *>(sm + L::GQ);
+    float2 *sS = reinterpret_cast<float2 *>(sm + L::S), *sYc = reinterpret_cast<float2 *>(sm + L::YC);
+    float *sY = reinterpret_cast<float *>(sm + L::Y), *sG = reinterpret_cast<float *>(sm + L::GQ);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int gr = lane >> 2, t2 = 2 * (lane & 3);
     const size_t head = blockIdx.x / (D / NS);
     const int slice = blockIdx.x % (D / NS), c0 = slice * NS;
     const size_t row0 = head * (size_t)p.T;
-    const bool chain = warp < 4;
     const int m0 = 16 * (warp & 3);
     const bool wantO = !REV && p.o != nullptr;
-
-    auto stage = [&](int i) { return sm + L::STAGE + (i & 1) * L::STAGE_BYTES; };
+    const size_t ch0 = head * p.nc;
     auto chunk_of = [&](int i) { return REV ? p.nc - 1 - i : i; };
-    auto prefetch = [&](int i) {
-        uint8_t *s = stage(i);
-        const int c = chunk_of(i);
-        load_tile<Tin, D>(reinterpret_cast<Tin *>(s + L::K), KS, static_cast<const Tin *>(p.k), row0,
-                          c * kC, p.T, D, 0, tid, 256);
-        if (REV || wantO)
-            load_tile<Tin, D>(reinterpret_cast<Tin *>(s + L::Q), KS, static_cast<const Tin *>(p.q),
-                              row0, c * kC, p.T, D, 0, tid, 256);
-        if (REV)
-            load_tile<Tin, NS>(reinterpret_cast<Tin *>(s + L::DO), L::DS,
-                               static_cast<const Tin *>(p.d_o), row0, c * kC, p.T, D, c0, tid, 256);
-        const float *cf = w.coef + (head * p.nc + c) * kCoef;
-        if (tid < kCoef / 4) cp16(s + L::COEF + tid * 16, cf + tid * 4, true);
-        cp_commit();
-    };
 
+    if (warp == 8) {
+        // ---------------- copies ----------------
+        auto fetch = [&](int i) {
+            if (i < p.nc) {
+                uint8_t *s = sm + L::STAGE + (i % L::STAGES) * L::STAGE_BYTES;
+                const int c = chunk_of(i);
+                load_tile<Tin, D>(reinterpret_cast<Tin *>(s + L::K), KS, static_cast<const Tin *>(p.k),
+                                  row0, c * kC, p.T, D, 0, lane, 32);
+                if (REV || wantO)
+                    load_tile<Tin, D>(reinterpret_cast<Tin *>(s + L::Q), KS,
+                                      static_cast<const Tin *>(p.q), row0, c * kC, p.T, D, 0, lane, 32);
+                if (REV)
+                    load_tile<Tin, NS>(reinterpret_cast<Tin *>(s + L::DO), L::DS,
+                                       static_cast<const Tin *>(p.d_o), row0, c * kC, p.T, D, c0, lane,
+                                       32);
+                const float *cf = w.coef + (ch0 + c) * kCoef;
+                for (int j = lane; j < kCoef / 4; j += 32) cp16(s + L::COEF + j * 16, cf + j * 4, true);
+                if (slice == 0 && lane == 0) {
+                    prefetch_l2(w.W + (ch0 + c) * (kC * D), kC * D * 4);
+                    prefetch_l2(w.Y + (ch0 + c) * (kC * D), kC * D * 4);
+                    if (wantO) prefetch_l2(w.M + (ch0 + c) * (kC * kC), kC * kC * 4);
+                }
+            }
+            cp_commit();  // one group per chunk, empty past the end
+        };
+        for (int i = 0; i < L::STAGES - 1; ++i) fetch(i);
+        cp_wait_ahead<L::STAGES - 2>();
+        __syncthreads();
+        for (int i = 0; i < p.nc; ++i) {
+            fetch(i + L::STAGES - 1);  // over the stage of chunk i - 1
+            __syncthreads();
+            cp_wait_ahead<L::STAGES - 2>();
+            __syncthreads();
+        }
+        return;
+    }
+
+    const bool chain = warp < 4;
     // the state in accumulator layout: rows 16 (MT warp + mt) + gr (+ 8), columns 8 nt + t2 (+ 1)
     float S[MT][NT][4];
     const bool owns = chain && (D >= 64 || warp < D / 16);
@@ -441,48 +485,65 @@ __global__ void __launch_bounds__(256) delta_chain(Args p, Scratch w) {
                                                               8 * nt + t2);
                     S[mt][nt][2 * h] = x.x;
                     S[mt][nt][2 * h + 1] = x.y;
-                    *reinterpret_cast<float2 *>(sS + r * ST + 8 * nt + t2) = x;
+                    *reinterpret_cast<float4 *>(sS + r * SP + 8 * nt + t2) = cut2(x.x, x.y);
                 }
     }
-    float4 W[D / 8], Y0[NT];
-    auto load_w = [&](int i) {
-        const size_t ch = head * p.nc + chunk_of(i);
-        const float4 *s = reinterpret_cast<const float4 *>(w.W + ch * (kC * D)) +
-                          (size_t)(warp & 3) * (D / 8) * 32 + lane;
-        const float4 *y = reinterpret_cast<const float4 *>(w.Y + ch * (kC * D)) +
-                          (size_t)((warp & 3) * (D / 8) + slice * NT) * 32 + lane;
+    // the next chunk's W and XV (chain) or M (outputs), as fragments
+    constexpr int NW = D / 8 > 8 ? D / 8 : 8;
+    float4 W[NW], Y0[NT];
+    const ptrdiff_t dir = REV ? -1 : 1;
+    const float4 *wp = reinterpret_cast<const float4 *>(w.W + (ch0 + chunk_of(0)) * (kC * D)) +
+                       (size_t)(warp & 3) * (D / 8) * 32 + lane;
+    const float4 *yp = reinterpret_cast<const float4 *>(w.Y + (ch0 + chunk_of(0)) * (kC * D)) +
+                       (size_t)((warp & 3) * (D / 8) + slice * NT) * 32 + lane;
+    const float4 *mp = reinterpret_cast<const float4 *>(w.M + (ch0 + chunk_of(0)) * (kC * kC)) +
+                       (size_t)(warp & 3) * 8 * 32 + lane;
+    const int kts = 2 * ((warp & 3) + 1);  // eights of M's columns up to the diagonal block
+    auto load_frags = [&]() {
+        if (chain) {
 #pragma unroll
-        for (int kt = 0; kt < D / 8; ++kt) W[kt] = s[kt * 32];
+            for (int kt = 0; kt < D / 8; ++kt) W[kt] = wp[kt * 32];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) Y0[nt] = y[nt * 32];
+            for (int nt = 0; nt < NT; ++nt) Y0[nt] = yp[nt * 32];
+            wp += dir * (kC * D / 4);
+            yp += dir * (kC * D / 4);
+        } else if (wantO) {
+#pragma unroll
+            for (int kt = 0; kt < 8; ++kt)
+                if (kt < kts) W[kt] = mp[kt * 32];
+            mp += kC * kC / 4;
+        }
     };
-    prefetch(0);
-    if (chain) load_w(0);
-    cp_wait_all();
+    load_frags();
     __syncthreads();
 
     for (int i = 0; i < p.nc; ++i) {
         const int c = chunk_of(i);
-        const size_t ch = head * p.nc + c;
-        const uint8_t *st = stage(i);
+        const uint8_t *st = sm + L::STAGE + (i % L::STAGES) * L::STAGE_BYTES;
         const Tin *sK = reinterpret_cast<const Tin *>(st + L::K);
         const Tin *sQ = reinterpret_cast<const Tin *>(st + L::Q);
         const Tin *sO = reinterpret_cast<const Tin *>(st + L::DO);
         const float *coef = reinterpret_cast<const float *>(st + L::COEF);
-        if (i + 1 < p.nc) prefetch(i + 1);
         float o[NT][4];
-        float4 M[8];
+        // a column's four k of the state or the errors, in parts
+        auto parts = [&](const float2 *x, int n, int k) {
+            x += k * SP + n;
+            FragB<2> b;
+            b.set(x[0], x[SP], x[8 * SP], x[9 * SP]);
+            return b;
+        };
         if (chain) {
             // E = XV - W S0 (REV: Z = Z0 + W' dS)
             float acc[NT][4];
             clear(acc);
 #pragma unroll
-            for (int kt = 0; kt < D / 8; ++kt) {
+            for (int ks = 0; ks < D / 16; ++ks) {
                 FragA<2> a;
-                a.set(make_float2(W[kt].x, W[kt].y), make_float2(W[kt].z, W[kt].w));
-                float2 b[NT];
+                const float4 w0 = W[2 * ks], w1 = W[2 * ks + 1];
+                a.set(make_float4(w0.x, w0.y, w1.x, w1.y), make_float4(w0.z, w0.w, w1.z, w1.w));
+                FragB<2> b[NT];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) b[nt] = pair<false>(sS, ST, 8 * nt + gr, 8 * kt + t2);
+                for (int nt = 0; nt < NT; ++nt) b[nt] = parts(sS, 8 * nt + gr, 16 * ks + t2);
                 mma_step<2, 2, NT>(acc, a, b);
             }
             const float k0 = coef[kC + m0 + gr], k1 = coef[kC + m0 + gr + 8];
@@ -494,42 +555,49 @@ __global__ void __launch_bounds__(256) delta_chain(Args p, Scratch w) {
                 const float2 y1 = make_float2(fmaf(sg, acc[nt][2], Y0[nt].z),
                                               fmaf(sg, acc[nt][3], Y0[nt].w));
                 const int n = 8 * nt + t2;
+                *reinterpret_cast<float4 *>(sYc + (m0 + gr) * SP + n) = cut2(k0 * y0.x, k0 * y0.y);
+                *reinterpret_cast<float4 *>(sYc + (m0 + gr + 8) * SP + n) = cut2(k1 * y1.x, k1 * y1.y);
                 if (wantO) {
                     *reinterpret_cast<float2 *>(sY + (m0 + gr) * ST + n) = y0;
                     *reinterpret_cast<float2 *>(sY + (m0 + gr + 8) * ST + n) = y1;
                 }
-                *reinterpret_cast<float2 *>(sYc + (m0 + gr) * ST + n) =
-                    make_float2(k0 * y0.x, k0 * y0.y);
-                *reinterpret_cast<float2 *>(sYc + (m0 + gr + 8) * ST + n) =
-                    make_float2(k1 * y1.x, k1 * y1.y);
                 if (KEEP) {
-                    float *d = p.keepY + (ch * kC + m0 + gr) * D + c0 + n;
+                    float *d = p.keepY + ((ch0 + c) * kC + m0 + gr) * D + c0 + n;
                     *reinterpret_cast<float2 *>(d) = y0;
                     *reinterpret_cast<float2 *>(d + 8 * D) = y1;
                 }
             }
-            if (KEEP && owns) {
+            if (i + 1 < p.nc) load_frags();
+        } else if (wantO) {
+            clear(o);
+            if constexpr (TI == 1) {  // the state's nearest tf32 values alone
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    FragA<1> a;
+                    const int k = 16 * ks + t2;
+                    a.set(quad<true, false>(sQ + m0 * KS, KS, gr, k),
+                          quad<true, false>(sQ + m0 * KS, KS, gr + 8, k));
+                    FragB<1> b[NT];
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        float *d = p.keepS + (ch * D + srow(mt)) * D + c0 + 8 * nt + t2;
-                        *reinterpret_cast<float2 *>(d) = make_float2(S[mt][nt][0], S[mt][nt][1]);
-                        *reinterpret_cast<float2 *>(d + 8 * D) =
-                            make_float2(S[mt][nt][2], S[mt][nt][3]);
+                        const float2 *x = sS + k * SP + 8 * nt + gr;
+                        b[nt].set(make_float4(x[0].x, x[SP].x, x[8 * SP].x, x[9 * SP].x));
                     }
-            }
-            if (i + 1 < p.nc) load_w(i + 1);
-        } else if (wantO) {
-            const float4 *s = reinterpret_cast<const float4 *>(w.M + ch * (kC * kC)) +
-                              (size_t)(warp & 3) * 8 * 32 + lane;
+                    mma_step<1, 1, NT>(o, a, b);
+                }
+            } else {
+#pragma unroll 2
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    FragA<2> a;
+                    const int k = 16 * ks + t2;
+                    a.set(quad<true, false>(sQ + m0 * KS, KS, gr, k),
+                          quad<true, false>(sQ + m0 * KS, KS, gr + 8, k));
+                    FragB<2> b[NT];
 #pragma unroll
-            for (int kt = 0; kt < 8; ++kt)
-                if (kt < 2 * ((warp & 3) + 1)) M[kt] = s[kt * 32];
-            clear(o);
-            gemm<TI, TI, NT>(
-                o, 0, D / 8, [&](int m, int k) { return pair<true>(sQ + m0 * KS, KS, m, k); },
-                [&](int n, int k) { return pair<false>(sS, ST, n, k); });
+                    for (int nt = 0; nt < NT; ++nt) b[nt] = parts(sS, 8 * nt + gr, k);
+                    mma_step<2, 2, NT>(o, a, b);
+                }
+            }
             const float s0 = coef[m0 + gr], s1 = coef[m0 + gr + 8];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -542,11 +610,11 @@ __global__ void __launch_bounds__(256) delta_chain(Args p, Scratch w) {
             for (int mt = warp & 3; mt < D / 16; mt += 4) {
                 float acc[NT][4];
                 clear(acc);
-                gemm<TI, 2, NT>(
-                    acc, 0, kC / 8, [&](int m, int k) { return pair<false>(sQ + 16 * mt, KS, m, k); },
+                gemm<TI, 2, NT, false>(
+                    acc, 0, kC / 16,
+                    [&](int m, int k) { return quad<false, false>(sQ + 16 * mt, KS, m, k); },
                     [&](int n, int k) {
-                        const float2 x = pair<false>(sO, L::DS, n, k);
-                        return make_float2(x.x * coef[k], x.y * coef[k + 1]);
+                        return scaled<false>(quad<false, false>(sO, L::DS, n, k), coef, k);
                     });
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
@@ -561,38 +629,59 @@ __global__ void __launch_bounds__(256) delta_chain(Args p, Scratch w) {
             // S = a_C S + K^T (c' Y) (REV: + Q^T dO): the chunk's share is summed
             // by itself, then added, so that rounding does not grow with the chunks
             const float aC = coef[2 * kC];
+            float acc[MT][NT][4];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                float acc[NT][4];
-                clear(acc);
-                const int r0 = 16 * (MT * warp + mt);
-                gemm<TI, 2, NT>(
-                    acc, 0, kC / 8, [&](int m, int k) { return pair<false>(sK + r0, KS, m, k); },
-                    [&](int n, int k) { return pair<false>(sYc, ST, n, k); });
+            for (int mt = 0; mt < MT; ++mt) clear(acc[mt]);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float *d = sS + srow(mt) * ST + 8 * nt + t2;
+            for (int ks = 0; ks < kC / 16; ++ks) {
+                const int k = 16 * ks + t2;
+                FragB<2> b[NT];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float x = fmaf(aC, S[mt][nt][e], acc[nt][e]);
-                        if (REV) x += sG[(srow(mt) + (e & 2 ? 8 : 0)) * ST + 8 * nt + t2 + (e & 1)];
-                        S[mt][nt][e] = x;
-                    }
-                    *reinterpret_cast<float2 *>(d) = make_float2(S[mt][nt][0], S[mt][nt][1]);
-                    *reinterpret_cast<float2 *>(d + 8 * ST) = make_float2(S[mt][nt][2], S[mt][nt][3]);
+                for (int nt = 0; nt < NT; ++nt) b[nt] = parts(sYc, 8 * nt + gr, k);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    FragA<TI> a;
+                    const Tin *ka = sK + 16 * (MT * warp + mt);
+                    a.set(quad<false, false>(ka, KS, gr, k), quad<false, false>(ka, KS, gr + 8, k));
+                    mma_step<TI, 2, NT>(acc[mt], a, b);
                 }
             }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const int n = 8 * nt + t2;
+                    if (KEEP) {  // the state before this chunk
+                        float *d = p.keepS + ((ch0 + c) * D + srow(mt)) * D + c0 + n;
+                        *reinterpret_cast<float2 *>(d) = make_float2(S[mt][nt][0], S[mt][nt][1]);
+                        *reinterpret_cast<float2 *>(d + 8 * D) =
+                            make_float2(S[mt][nt][2], S[mt][nt][3]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float x = fmaf(aC, S[mt][nt][e], acc[mt][nt][e]);
+                        if (REV) x += sG[(srow(mt) + (e & 2 ? 8 : 0)) * ST + n + (e & 1)];
+                        S[mt][nt][e] = x;
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        *reinterpret_cast<float4 *>(sS + (srow(mt) + 8 * h) * SP + n) =
+                            cut2(S[mt][nt][2 * h], S[mt][nt][2 * h + 1]);
+                }
         } else if (!chain && wantO) {
 #pragma unroll
-            for (int kt = 0; kt < 8; ++kt) {
-                if (kt >= 2 * ((warp & 3) + 1)) continue;
+            for (int ks = 0; ks < 4; ++ks) {
+                if (ks > (warp & 3)) continue;
                 FragA<TI> a;
-                a.set(make_float2(M[kt].x, M[kt].y), make_float2(M[kt].z, M[kt].w));
-                float2 b[NT];
+                const float4 w0 = W[2 * ks], w1 = W[2 * ks + 1];
+                a.set(make_float4(w0.x, w0.y, w1.x, w1.y), make_float4(w0.z, w0.w, w1.z, w1.w));
+                FragB<TI> b[NT];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) b[nt] = pair<false>(sY, ST, 8 * nt + gr, 8 * kt + t2);
+                for (int nt = 0; nt < NT; ++nt)
+                    b[nt].set(quad<false, false>(sY, ST, 8 * nt + gr, 16 * ks + t2));
                 mma_step<TI, TI, NT>(o, a, b);
             }
+            if (i + 1 < p.nc) load_frags();
             Tin *od = static_cast<Tin *>(p.o);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -610,7 +699,6 @@ __global__ void __launch_bounds__(256) delta_chain(Args p, Scratch w) {
                 }
             }
         }
-        cp_wait_all();
         __syncthreads();
     }
     if (owns && p.S_out) {
@@ -657,7 +745,7 @@ cudaError_t launch_chain_ns(const Args &p, const Scratch &w, long heads, cudaStr
     static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
     cudaError_t e = raise_smem<delta_chain<Tin, D, NS, REV, KEEP>>(bytes);
     if (e != cudaSuccess) return e;
-    delta_chain<Tin, D, NS, REV, KEEP><<<(unsigned)(heads * (D / NS)), 256, bytes, stream>>>(p, w);
+    delta_chain<Tin, D, NS, REV, KEEP><<<(unsigned)(heads * (D / NS)), 288, bytes, stream>>>(p, w);
     return after_launch();
 }
 

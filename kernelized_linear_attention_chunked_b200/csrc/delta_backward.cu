@@ -61,6 +61,11 @@ __device__ __forceinline__ void store2(Tin *d, float x, float y) {
         *reinterpret_cast<float2 *>(d) = make_float2(x, y);
 }
 
+__device__ __forceinline__ float2 two(const float *p) { return *reinterpret_cast<const float2 *>(p); }
+__device__ __forceinline__ float2 two(const __nv_bfloat16 *p) {
+    return tf::unpack(*reinterpret_cast<const uint32_t *>(p));
+}
+
 template <typename Tin, int D>
 __global__ void __launch_bounds__(256, D <= 64 ? 2 : 1) delta_grad(Args p, Grads gr_) {
     using namespace tf;
@@ -116,13 +121,13 @@ __global__ void __launch_bounds__(256, D <= 64 ? 2 : 1) delta_grad(Args p, Grads
         clear(qk);
         // column 8 nt + g of the warp's tiles is column 16 nt + 8 hf + g of the product
         auto kcol = [&](int n, int k) {
-            return pair<true>(sK, KS, 2 * (n & ~7) + 8 * hf + (n & 7), k);
+            return quad<true, true>(sK, KS, 2 * (n & ~7) + 8 * hf + (n & 7), k);
         };
-        gemm<TI, TI, 4>(
-            kk, 0, D / 8, [&](int m, int k) { return pair<true>(sK + m0 * KS, KS, m, k); }, kcol,
+        gemm<TI, TI, 4, true>(
+            kk, 0, D / 16, [&](int m, int k) { return quad<true, true>(sK + m0 * KS, KS, m, k); }, kcol,
             nt_end);
-        gemm<TI, TI, 4>(
-            qk, 0, D / 8, [&](int m, int k) { return pair<true>(sQ + m0 * KS, KS, m, k); }, kcol,
+        gemm<TI, TI, 4, true>(
+            qk, 0, D / 16, [&](int m, int k) { return quad<true, true>(sQ + m0 * KS, KS, m, k); }, kcol,
             nt_end);
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt) {
@@ -159,19 +164,19 @@ __global__ void __launch_bounds__(256, D <= 64 ? 2 : 1) delta_grad(Args p, Grads
             float md[NF][4], kd[NF][4];
             clear(md);
             clear(kd);
-            gemm<2, TI, NF>(
-                md, 2 * rb, 8, [&](int m, int k) { return pair<false>(sM + m0, kTS, m, k); },
-                [&](int n, int k) { return pair<false>(sO + f0, SS, n, k); });
+            gemm<2, TI, NF, false>(
+                md, rb, 4, [&](int m, int k) { return quad<false, false>(sM + m0, kTS, m, k); },
+                [&](int n, int k) { return quad<false, false>(sO + f0, SS, n, k); });
 #pragma unroll
             for (int nt = 0; nt < NF; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) md[nt][e] *= -p.scale;
-            gemm<2, 2, NF>(
-                md, 2 * rb, 8, [&](int m, int k) { return pair<false>(sN + m0, kTS, m, k); },
-                [&](int n, int k) { return pair<false>(sZ + f0, SS, n, k); });
-            gemm<TI, 2, NF>(
-                kd, 0, D / 8, [&](int m, int k) { return pair<true>(sK + m0 * KS, KS, m, k); },
-                [&](int n, int k) { return pair<false>(sDS + f0, SS, n, k); });
+            gemm<2, 2, NF, false>(
+                md, rb, 4, [&](int m, int k) { return quad<false, false>(sN + m0, kTS, m, k); },
+                [&](int n, int k) { return quad<false, false>(sZ + f0, SS, n, k); });
+            gemm<TI, 2, NF, false>(
+                kd, 0, D / 16, [&](int m, int k) { return quad<true, false>(sK + m0 * KS, KS, m, k); },
+                [&](int n, int k) { return quad<false, false>(sDS + f0, SS, n, k); });
 #pragma unroll
             for (int nt = 0; nt < NF; ++nt)
 #pragma unroll
@@ -189,23 +194,23 @@ __global__ void __launch_bounds__(256, D <= 64 ? 2 : 1) delta_grad(Args p, Grads
         }
         auto ucol = [&](int n, int k) {  // U's row as a column of U^T
             const int j = 2 * (n & ~7) + 8 * hf + (n & 7);
-            const float2 x = pair<true>(sE, SS, j, k);
-            return make_float2(beta[j] * x.x, beta[j] * x.y);
+            const float4 x = quad<true, true>(sE, SS, j, k);
+            return make_float4(beta[j] * x.x, beta[j] * x.y, beta[j] * x.z, beta[j] * x.w);
         };
-        gemm<TI, 2, 4>(
-            pm, 0, SL / 8, [&](int m, int k) { return pair<true>(sO + m0 * SS, SS, m, k); }, ucol,
+        gemm<TI, 2, 4, true>(
+            pm, 0, SL / 16, [&](int m, int k) { return quad<true, true>(sO + m0 * SS, SS, m, k); }, ucol,
             nt_end);
-        gemm<2, 2, 4>(
-            pn, 0, SL / 8, [&](int m, int k) { return pair<true>(sZ + m0 * SS, SS, m, k); }, ucol,
+        gemm<2, 2, 4, true>(
+            pn, 0, SL / 16, [&](int m, int k) { return quad<true, true>(sZ + m0 * SS, SS, m, k); }, ucol,
             nt_end);
-        auto scol = [&](int n, int k) { return pair<true>(sS0 + d0 * SS, SS, n, k); };
-        gemm<TI, 2, ND>(
-            dq, 0, SL / 8, [&](int m, int k) { return pair<true>(sO + m0 * SS, SS, m, k); }, scol);
-        gemm<2, 2, ND>(
-            dr, 0, SL / 8, [&](int m, int k) { return pair<true>(sZ + m0 * SS, SS, m, k); }, scol);
-        gemm<2, 2, ND>(
-            dl, 0, SL / 8, [&](int m, int k) { return pair<true>(sE + m0 * SS, SS, m, k); },
-            [&](int n, int k) { return pair<true>(sDS + d0 * SS, SS, n, k); });
+        auto scol = [&](int n, int k) { return quad<true, true>(sS0 + d0 * SS, SS, n, k); };
+        gemm<TI, 2, ND, true>(
+            dq, 0, SL / 16, [&](int m, int k) { return quad<true, true>(sO + m0 * SS, SS, m, k); }, scol);
+        gemm<2, 2, ND, true>(
+            dr, 0, SL / 16, [&](int m, int k) { return quad<true, true>(sZ + m0 * SS, SS, m, k); }, scol);
+        gemm<2, 2, ND, true>(
+            dl, 0, SL / 16, [&](int m, int k) { return quad<true, true>(sE + m0 * SS, SS, m, k); },
+            [&](int n, int k) { return quad<true, true>(sDS + d0 * SS, SS, n, k); });
         Tin *dv = static_cast<Tin *>(gr_.dv);
         for (int i = tid; i < kC * SL / 2; i += 256) {
             const int r = i / (SL / 2), c = 2 * (i % (SL / 2));
@@ -235,16 +240,16 @@ __global__ void __launch_bounds__(256, D <= 64 ? 2 : 1) delta_grad(Args p, Grads
             dl[nt][e] *= beta[i] * cc[i];
         }
     __syncthreads();
-    auto kc = [&](int n, int k) { return pair<false>(sK + d0, KS, n, k); };
-    gemm<2, TI, ND>(
-        dq, 0, 2 * nt_end, [&](int m, int k) { return pair<true>(sM + m0 * kTS, kTS, m, k); }, kc);
-    gemm<2, TI, ND>(
-        dr, 0, 2 * nt_end, [&](int m, int k) { return pair<true>(sN + m0 * kTS, kTS, m, k); }, kc);
-    gemm<2, TI, ND>(
-        dl, 2 * rb, 8, [&](int m, int k) { return pair<false>(sM + m0, kTS, m, k); },
-        [&](int n, int k) { return pair<false>(sQ + d0, KS, n, k); });
-    gemm<2, TI, ND>(
-        dl, 2 * rb, 8, [&](int m, int k) { return pair<false>(sN + m0, kTS, m, k); }, kc);
+    auto kc = [&](int n, int k) { return quad<false, false>(sK + d0, KS, n, k); };
+    gemm<2, TI, ND, false>(
+        dq, 0, nt_end, [&](int m, int k) { return quad<true, false>(sM + m0 * kTS, kTS, m, k); }, kc);
+    gemm<2, TI, ND, false>(
+        dr, 0, nt_end, [&](int m, int k) { return quad<true, false>(sN + m0 * kTS, kTS, m, k); }, kc);
+    gemm<2, TI, ND, false>(
+        dl, rb, 4, [&](int m, int k) { return quad<false, false>(sM + m0, kTS, m, k); },
+        [&](int n, int k) { return quad<false, false>(sQ + d0, KS, n, k); });
+    gemm<2, TI, ND, false>(
+        dl, rb, 4, [&](int m, int k) { return quad<false, false>(sN + m0, kTS, m, k); }, kc);
 
     float dG[2] = {0.f, 0.f};
 #pragma unroll
@@ -252,7 +257,7 @@ __global__ void __launch_bounds__(256, D <= 64 ? 2 : 1) delta_grad(Args p, Grads
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int i = m0 + gr + 8 * h, n = d0 + 8 * nt + t2;
-            const float2 kx = pair<true>(sK, KS, i, n), qx = pair<true>(sQ, KS, i, n);
+            const float2 kx = two(sK + i * KS + n), qx = two(sQ + i * KS + n);
             const float q0 = dq[nt][2 * h], q1 = dq[nt][2 * h + 1];
             const float r0 = dr[nt][2 * h], r1 = dr[nt][2 * h + 1];
             const float l0 = dl[nt][2 * h], l1 = dl[nt][2 * h + 1];

@@ -15,12 +15,15 @@
 // and SM quadrant, latency 20.6 cycles; three bf16 parts would need as many
 // tensor cycles (6 x k16 against 3 x 2 x k8) and more instructions to form.
 //
-// Fragments use the k order (0 2 4 6 | 1 3 5 7) of each group of eight: the
-// operands' k slots t and t + 4 hold k = 2t and 2t + 1. The order of a sum's
-// terms is free as long as both operands agree, and in this one
-//   - a K-major operand's two values of a lane are neighbours (one load), and
-//   - an accumulator tile (row g, columns 2t, 2t + 1; row g + 8, the same) is,
-//     register for register, an A operand whose k runs over its columns.
+// A product advances sixteen k at a time, in two steps of eight whose k slots t
+// and t + 4 hold two neighbours. Which neighbours is free as long as both
+// operands agree:
+//   narrow  2t, 2t + 1 and 2t + 8, 2t + 9: an accumulator tile (row g, columns
+//           2t, 2t + 1; row g + 8, the same) is then, register for register, an A
+//           operand whose k runs over its columns, and an operand whose k runs
+//           down the rows of memory meets no bank conflict;
+//   wide    4t .. 4t + 3: a lane's four values are one load where k runs along
+//           the rows of memory in both operands.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -54,58 +57,89 @@ __device__ __forceinline__ void split(float x, uint32_t &hi, uint32_t &lo) {
     lo = __float_as_uint(x - __uint_as_float(hi));
 }
 
-// A 16 x 8 A operand: {(g, 2t), (g + 8, 2t), (g, 2t + 1), (g + 8, 2t + 1)}.
+// A 16 x 16 A operand as two 16 x 8 ones: {row g, row g + 8} x {first, second neighbour}.
 template <int TA>
 struct FragA {
+    uint32_t hi[2][4], lo[2][4];
+    // top and bottom: four k of row g and of row g + 8
+    __device__ __forceinline__ void set(float4 top, float4 bottom) {
+        const float x[2][4] = {{top.x, bottom.x, top.y, bottom.y}, {top.z, bottom.z, top.w, bottom.w}};
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (TA == 2)
+                    split(x[h][i], hi[h][i], lo[h][i]);
+                else
+                    hi[h][i] = __float_as_uint(x[h][i]);
+            }
+    }
+};
+
+// A 16 x 8 B operand: four k of column g.
+template <int TB>
+struct FragB {
     uint32_t hi[4], lo[4];
-    __device__ __forceinline__ void set(float2 top, float2 bottom) {
-        const float x[4] = {top.x, bottom.x, top.y, bottom.y};
+    __device__ __forceinline__ void set(float4 v) {
+        const float x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if (TA == 2)
+            if (TB == 2)
                 split(x[i], hi[i], lo[i]);
             else
                 hi[i] = __float_as_uint(x[i]);
         }
     }
+    // the same from values cut before ({hi, lo} each)
+    __device__ __forceinline__ void set(float2 a, float2 b, float2 c, float2 d) {
+        const float2 x[4] = {a, b, c, d};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            hi[i] = __float_as_uint(x[i].x);
+            lo[i] = __float_as_uint(x[i].y);
+        }
+    }
 };
 
-// acc += A B for one 16 x 8 A operand and one 8 x 8 B operand {(2t, g), (2t + 1, g)}.
+// acc += A B over sixteen k.
 // The tensor cores' accumulator drops the bits below its last place, always
-// toward zero, so a long sum kept in it drifts. The eight terms of a step are
-// summed there from zero and added to acc by an ordinary rounded addition:
-// the error of a 64-term product falls from 5e-7 to 1.5e-7 of its norm.
-//
-// The parts of one tile depend on each other (20.6 cycles apart), so a step goes
+// toward zero, so a long sum kept in it drifts. The terms of a step are summed
+// there from zero, the small parts first, and added to acc by an ordinary
+// rounded addition: the error of a chain of products over 64 terms falls from
+// 5e-7 to 2e-7 of its norm.
+// The parts of one tile depend on each other (20.6 cycles apart), so they go
 // part by part over all NT tiles.
 template <int TA, int TB, int NT>
 __device__ __forceinline__ void mma_step(float (&acc)[NT][4], const FragA<TA> &a,
-                                         const float2 (&b)[NT], int nt_end = NT) {
+                                         const FragB<TB> (&b)[NT], int nt_end = NT) {
     float t[NT][4];
-    uint32_t h0[NT], h1[NT], l0[NT], l1[NT];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        if (n >= nt_end) continue;
-        if (TB == 2) {
-            split(b[n].x, h0[n], l0[n]);
-            split(b[n].y, h1[n], l1[n]);
-            mma0(t[n], a.hi, l0[n], l1[n]);
-        } else {
-            h0[n] = __float_as_uint(b[n].x);
-            h1[n] = __float_as_uint(b[n].y);
-            mma0(t[n], TA == 2 ? a.lo : a.hi, h0[n], h1[n]);
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            if (n >= nt_end) continue;
+            const uint32_t *bl = b[n].lo + 2 * h, *bh = b[n].hi + 2 * h;
+            if (TB == 2)
+                h ? mma(t[n], a.hi[h], bl[0], bl[1]) : mma0(t[n], a.hi[h], bl[0], bl[1]);
+            else if (TA == 2)
+                h ? mma(t[n], a.lo[h], bh[0], bh[1]) : mma0(t[n], a.lo[h], bh[0], bh[1]);
+        }
+        if (TA == 2 && TB == 2) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                if (n < nt_end) mma(t[n], a.lo[h], b[n].hi[2 * h], b[n].hi[2 * h + 1]);
         }
     }
-    if (TA == 2 && TB == 2) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-            if (n < nt_end) mma(t[n], a.lo, h0[n], h1[n]);
-    }
-    if (TA == 2 || TB == 2) {
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-            if (n < nt_end) mma(t[n], a.hi, h0[n], h1[n]);
-    }
+        for (int n = 0; n < NT; ++n) {
+            if (n >= nt_end) continue;
+            if (TA == 1 && TB == 1 && h == 0)
+                mma0(t[n], a.hi[h], b[n].hi[2 * h], b[n].hi[2 * h + 1]);
+            else
+                mma(t[n], a.hi[h], b[n].hi[2 * h], b[n].hi[2 * h + 1]);
+        }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         if (n >= nt_end) continue;
@@ -114,42 +148,68 @@ __device__ __forceinline__ void mma_step(float (&acc)[NT][4], const FragA<TA> &a
     }
 }
 
-// Two k neighbours of an operand in shared memory, as floats. `K` says that k
-// runs along the rows of memory (stride 1); otherwise k is the row index.
-template <bool K>
-__device__ __forceinline__ float2 pair(const float *p, int stride, int mn, int k) {
-    if (K) return *reinterpret_cast<const float2 *>(p + mn * stride + k);
-    return make_float2(p[k * stride + mn], p[(k + 1) * stride + mn]);
-}
-template <bool K>
-__device__ __forceinline__ float2 pair(const __nv_bfloat16 *p, int stride, int mn, int k) {
+// The four k from `k` on (k = 16 step + 4t wide, + 2t narrow) of row or column
+// mn of an operand in shared memory. `K`: k runs along the rows of memory;
+// otherwise it is the row index.
+template <bool K, bool WIDE>
+__device__ __forceinline__ float4 quad(const float *p, int stride, int mn, int k) {
+    static_assert(K || !WIDE, "rows of memory four apart share a bank");
+    if (K && WIDE) return *reinterpret_cast<const float4 *>(p + mn * stride + k);
     if (K) {
-        const uint32_t u = *reinterpret_cast<const uint32_t *>(p + mn * stride + k);
-        return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+        const float2 a = *reinterpret_cast<const float2 *>(p + mn * stride + k);
+        const float2 b = *reinterpret_cast<const float2 *>(p + mn * stride + k + 8);
+        return make_float4(a.x, a.y, b.x, b.y);
     }
-    return make_float2(__bfloat162float(p[k * stride + mn]),
-                       __bfloat162float(p[(k + 1) * stride + mn]));
+    p += k * stride + mn;
+    return make_float4(p[0], p[stride], p[8 * stride], p[9 * stride]);
+}
+__device__ __forceinline__ float2 unpack(uint32_t u) {
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+}
+template <bool K, bool WIDE>
+__device__ __forceinline__ float4 quad(const __nv_bfloat16 *p, int stride, int mn, int k) {
+    static_assert(K || !WIDE, "rows of memory four apart share a bank");
+    if (K) {
+        uint2 u;
+        if (WIDE) {
+            u = *reinterpret_cast<const uint2 *>(p + mn * stride + k);
+        } else {
+            u.x = *reinterpret_cast<const uint32_t *>(p + mn * stride + k);
+            u.y = *reinterpret_cast<const uint32_t *>(p + mn * stride + k + 8);
+        }
+        const float2 a = unpack(u.x), b = unpack(u.y);
+        return make_float4(a.x, a.y, b.x, b.y);
+    }
+    p += k * stride + mn;
+    return make_float4(__bfloat162float(p[0]), __bfloat162float(p[stride]),
+                       __bfloat162float(p[8 * stride]), __bfloat162float(p[9 * stride]));
+}
+// A quad times c[.] of its k.
+template <bool WIDE>
+__device__ __forceinline__ float4 scaled(float4 x, const float *c, int k) {
+    return WIDE ? make_float4(x.x * c[k], x.y * c[k + 1], x.z * c[k + 2], x.w * c[k + 3])
+                : make_float4(x.x * c[k], x.y * c[k + 1], x.z * c[k + 8], x.w * c[k + 9]);
 }
 
-// acc[NT] += A B over `kt1 - kt0` groups of eight k. fa(mn, k) and fb(mn, k)
-// give two k neighbours of row mn of A (mn = 0 .. 15) and of column mn of B
-// (mn = 0 .. 8 NT - 1). Columns from 8 * nt_end on are left alone.
-template <int TA, int TB, int NT, class FA, class FB>
-__device__ __forceinline__ void gemm(float (&acc)[NT][4], int kt0, int kt1, FA fa, FB fb,
+// acc[NT] += A B over the sixteens of k from `s0` to `s1`. fa(m, k) and fb(n, k)
+// give quads of row m of A (0 .. 15) and of column n of B (0 .. 8 NT - 1).
+// Columns from 8 * nt_end on are left alone.
+template <int TA, int TB, int NT, bool WIDE, class FA, class FB>
+__device__ __forceinline__ void gemm(float (&acc)[NT][4], int s0, int s1, FA fa, FB fb,
                                      int nt_end = NT) {
-    const int g = (threadIdx.x & 31) >> 2, t2 = 2 * (threadIdx.x & 3);
-#pragma unroll 2
-    for (int kt = kt0; kt < kt1; ++kt) {
-        const int k = 8 * kt + t2;
+    const int g = (threadIdx.x & 31) >> 2, tk = (WIDE ? 4 : 2) * (threadIdx.x & 3);
+    constexpr int G = NT % 2 == 0 ? 2 : 1;  // tiles at a time: more cost registers
+#pragma unroll 1
+    for (int st = s0; st < s1; ++st) {
+        const int k = 16 * st + tk;
         FragA<TA> a;
         a.set(fa(g, k), fa(g + 8, k));
-        constexpr int G = NT % 2 == 0 ? 2 : 1;  // tiles at a time: more cost registers
 #pragma unroll
         for (int n0 = 0; n0 < NT; n0 += G) {
-            float2 b[G];
+            FragB<TB> b[G];
 #pragma unroll
-            for (int nt = 0; nt < G; ++nt)
-                if (n0 + nt < nt_end) b[nt] = fb(8 * (n0 + nt) + g, k);
+            for (int n = 0; n < G; ++n)
+                if (n0 + n < nt_end) b[n].set(fb(8 * (n0 + n) + g, k));
             mma_step<TA, TB, G>(*reinterpret_cast<float(*)[G][4]>(&acc[n0]), a, b, nt_end - n0);
         }
     }

@@ -189,12 +189,12 @@ __global__ void __launch_bounds__(kThreads) bwd_query(Args p) {
         } else {
             clear(s);
             clear(dp);
-            auto qa = [&](int m, int kk) { return pair<true>(sQ + m0 * RS, RS, m, kk); };
-            auto oa = [&](int m, int kk) { return pair<true>(sO + m0 * RS, RS, m, kk); };
-            gemm<TI, TI, 4>(s, 0, D / 8, qa,
-                            [&](int n, int kk) { return pair<true>(k + n0 * RS, RS, n, kk); });
-            gemm<TI, TI, 4>(dp, 0, D / 8, oa,
-                            [&](int n, int kk) { return pair<true>(v + n0 * RS, RS, n, kk); });
+            auto qa = [&](int m, int kk) { return quad<true, true>(sQ + m0 * RS, RS, m, kk); };
+            auto oa = [&](int m, int kk) { return quad<true, true>(sO + m0 * RS, RS, m, kk); };
+            gemm<TI, TI, 4, true>(s, 0, D / 16, qa,
+                            [&](int n, int kk) { return quad<true, true>(k + n0 * RS, RS, n, kk); });
+            gemm<TI, TI, 4, true>(dp, 0, D / 16, oa,
+                            [&](int n, int kk) { return quad<true, true>(v + n0 * RS, RS, n, kk); });
             float ds[2] = {0.f, 0.f}, ns[2] = {0.f, 0.f};
 #pragma unroll
             for (int nt = 0; nt < 4; ++nt)
@@ -228,9 +228,9 @@ __global__ void __launch_bounds__(kThreads) bwd_query(Args p) {
                         make_float2(s[nt][2 * h], s[nt][2 * h + 1]);
             __syncthreads();
             const int d0 = hf * (D / 2);
-            gemm<2, TI, D / 16>(
-                dq, 0, kB / 8, [&](int m, int kk) { return pair<true>(sDS + m0 * kTS, kTS, m, kk); },
-                [&](int n, int kk) { return pair<false>(k + d0, RS, n, kk); });
+            gemm<2, TI, D / 16, false>(
+                dq, 0, kB / 16, [&](int m, int kk) { return quad<true, false>(sDS + m0 * kTS, kTS, m, kk); },
+                [&](int n, int kk) { return quad<false, false>(k + d0, RS, n, kk); });
         }
         cp_wait_all();
         __syncthreads();
@@ -298,12 +298,12 @@ __global__ void __launch_bounds__(kThreads) bwd_key(Args p) {
         } else {
             clear(s);
             clear(dp);
-            gemm<TI, TI, 4>(
-                s, 0, D / 8, [&](int m, int kk) { return pair<true>(sK + m0 * RS, RS, m, kk); },
-                [&](int n, int kk) { return pair<true>(q + n0 * RS, RS, n, kk); });
-            gemm<TI, TI, 4>(
-                dp, 0, D / 8, [&](int m, int kk) { return pair<true>(sV + m0 * RS, RS, m, kk); },
-                [&](int n, int kk) { return pair<true>(o + n0 * RS, RS, n, kk); });
+            gemm<TI, TI, 4, true>(
+                s, 0, D / 16, [&](int m, int kk) { return quad<true, true>(sK + m0 * RS, RS, m, kk); },
+                [&](int n, int kk) { return quad<true, true>(q + n0 * RS, RS, n, kk); });
+            gemm<TI, TI, 4, true>(
+                dp, 0, D / 16, [&](int m, int kk) { return quad<true, true>(sV + m0 * RS, RS, m, kk); },
+                [&](int n, int kk) { return quad<true, true>(o + n0 * RS, RS, n, kk); });
 #pragma unroll
             for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
@@ -325,12 +325,12 @@ __global__ void __launch_bounds__(kThreads) bwd_key(Args p) {
                 *reinterpret_cast<float2 *>(sP + at) = make_float2(dp[nt][2 * h], dp[nt][2 * h + 1]);
             }
         __syncthreads();
-        gemm<2, TI, D / 16>(
-            dk, 0, kB / 8, [&](int m, int kk) { return pair<true>(sDS + m0 * kTS, kTS, m, kk); },
-            [&](int n, int kk) { return pair<false>(q + d0, RS, n, kk); });
-        gemm<2, TI, D / 16>(
-            dv, 0, kB / 8, [&](int m, int kk) { return pair<true>(sP + m0 * kTS, kTS, m, kk); },
-            [&](int n, int kk) { return pair<false>(o + d0, RS, n, kk); });
+        gemm<2, TI, D / 16, false>(
+            dk, 0, kB / 16, [&](int m, int kk) { return quad<true, false>(sDS + m0 * kTS, kTS, m, kk); },
+            [&](int n, int kk) { return quad<false, false>(q + d0, RS, n, kk); });
+        gemm<2, TI, D / 16, false>(
+            dv, 0, kB / 16, [&](int m, int kk) { return quad<true, false>(sP + m0 * kTS, kTS, m, kk); },
+            [&](int n, int kk) { return quad<false, false>(o + d0, RS, n, kk); });
         cp_wait_all();
         __syncthreads();
     }
