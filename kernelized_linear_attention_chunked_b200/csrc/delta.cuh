@@ -49,6 +49,8 @@ constexpr int kC = 64;    // tokens per chunk
 constexpr int kTS = 72;   // row stride of a 64 x 64 fp32 tile in shared memory
 constexpr int kCoef = 256;  // floats of coefficients per chunk: a' [64], c' [64], a_C
 constexpr float kMinLog = -200.f;
+constexpr int kLoaders = 128;     // threads of delta_chain that copy
+constexpr int kChainThreads = 256 + kLoaders;
 
 // Row stride of a [64, D] tile in shared memory: rows start four 32-bit banks
 // apart (eight for fp32), so a K-major fragment load has no bank conflict.
@@ -98,16 +100,26 @@ __device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;
 
 // Rows [t0, t0 + ROWS) of the [nrows, D] matrix that starts at row `row0`, columns [c0, c0 + N), to
 // a tile with row stride `stride`; rows from nrows on become zero.
-template <typename T, int N, int ROWS = kC>
+// NTH threads take part, tid = 0 .. NTH - 1.
+template <typename T, int N, int NTH, int ROWS = kC>
 __device__ __forceinline__ void load_tile(T *dst, int stride, const T *src, size_t row0, int t0,
-                                          int nrows, int D, int c0, int tid, int nthreads) {
+                                          int nrows, int D, int c0, int tid) {
     constexpr int PER = 16 / sizeof(T);
     constexpr int CH = N / PER;
-    for (int i = tid; i < ROWS * CH; i += nthreads) {
-        const int r = i / CH, c = (i % CH) * PER;
-        const bool have = t0 + r < nrows;
-        const T *s = src + (row0 + (have ? t0 + r : 0)) * (size_t)D + c0 + c;
-        cp16(dst + r * stride + c, s, have);
+    constexpr int RPP = NTH / CH;  // rows per pass
+    static_assert(NTH % CH == 0, "whole rows per pass");
+    const int r0 = tid / CH, c = (tid % CH) * PER;
+    const T *s = src + (row0 + t0 + r0) * (size_t)D + c0 + c;
+    T *d = dst + r0 * stride + c;
+    if (t0 + ROWS <= nrows) {
+#pragma unroll
+        for (int r = 0; r < ROWS; r += RPP)
+            if (ROWS % RPP == 0 || r0 + r < ROWS) cp16(d + r * stride, s + (size_t)r * D, true);
+    } else {
+        for (int r = 0; r < ROWS && r0 + r < ROWS; r += RPP) {
+            const bool have = t0 + r0 + r < nrows;
+            cp16(d + r * stride, have ? s + (size_t)r * D : src, have);
+        }
     }
 }
 
@@ -257,12 +269,12 @@ __global__ void __launch_bounds__(128) delta_prep(Args p, Scratch f, Scratch r) 
     const int t0 = (int)(ch % p.nc) * kC;
     const size_t row0 = head * (size_t)p.T;
 
-    load_tile<Tin, D>(sK, KS, static_cast<const Tin *>(p.k), row0, t0, p.T, D, 0, tid, 128);
+    load_tile<Tin, D, 128>(sK, KS, static_cast<const Tin *>(p.k), row0, t0, p.T, D, 0, tid);
     if (BACK || p.o)
-        load_tile<Tin, D>(sQ, KS, static_cast<const Tin *>(p.q), row0, t0, p.T, D, 0, tid, 128);
-    load_tile<Tin, D>(sV, KS, static_cast<const Tin *>(p.v), row0, t0, p.T, D, 0, tid, 128);
+        load_tile<Tin, D, 128>(sQ, KS, static_cast<const Tin *>(p.q), row0, t0, p.T, D, 0, tid);
+    load_tile<Tin, D, 128>(sV, KS, static_cast<const Tin *>(p.v), row0, t0, p.T, D, 0, tid);
     if (BACK)
-        load_tile<Tin, D>(sO, KS, static_cast<const Tin *>(p.d_o), row0, t0, p.T, D, 0, tid, 128);
+        load_tile<Tin, D, 128>(sO, KS, static_cast<const Tin *>(p.d_o), row0, t0, p.T, D, 0, tid);
     cp_commit();
     if (warp == 0) cumulate(p.g, row0, t0, p.T, G);
     if (tid >= 64) {
@@ -404,14 +416,14 @@ __device__ __forceinline__ float4 cut2(float x, float y) {
 // The walk over the chunks, one CTA per (head, NS value columns). Warps 0-3
 // carry the chain: they hold the state in registers (fp32, D / 4 rows each)
 // and take two dependent products per chunk. Warps 4-7 take the products that
-// hang off it: the outputs (forward) or Q^T dO (REV). Warp 8 brings K, Q and
+// hang off it: the outputs (forward) or Q^T dO (REV). Warps 8-11 bring K, Q and
 // the coefficients by asynchronous copies up to three chunks ahead, and calls
 // the next chunks' W, XV and M into L2; those come straight from there into
 // the fragments that use them, one chunk ahead. The state and the errors, B
 // operands that four warps read, are cut into their tf32 parts by the warp
 // that writes them.
 template <typename Tin, int D, int NS, bool REV, bool KEEP>
-__global__ void __launch_bounds__(288, 1) delta_chain(Args p, Scratch w) {
+__global__ void __launch_bounds__(kChainThreads, 1) delta_chain(Args p, Scratch w) {
     using namespace tf;
     using L = ChainSmem<Tin, D, NS, REV>;
     constexpr int KS = L::KS, SP = L::SP, ST = L::ST, NT = NS / 8, TI = Parts<Tin>::N;
@@ -429,24 +441,26 @@ __global__ void __launch_bounds__(288, 1) delta_chain(Args p, Scratch w) {
     const size_t ch0 = head * p.nc;
     auto chunk_of = [&](int i) { return REV ? p.nc - 1 - i : i; };
 
-    if (warp == 8) {
+    if (warp >= 8) {
         // ---------------- copies ----------------
+        const int lt = tid - 256;
         auto fetch = [&](int i) {
             if (i < p.nc) {
                 uint8_t *s = sm + L::STAGE + (i % L::STAGES) * L::STAGE_BYTES;
                 const int c = chunk_of(i);
-                load_tile<Tin, D>(reinterpret_cast<Tin *>(s + L::K), KS, static_cast<const Tin *>(p.k),
-                                  row0, c * kC, p.T, D, 0, lane, 32);
+                load_tile<Tin, D, kLoaders>(reinterpret_cast<Tin *>(s + L::K), KS,
+                                            static_cast<const Tin *>(p.k), row0, c * kC, p.T, D, 0, lt);
                 if (REV || wantO)
-                    load_tile<Tin, D>(reinterpret_cast<Tin *>(s + L::Q), KS,
-                                      static_cast<const Tin *>(p.q), row0, c * kC, p.T, D, 0, lane, 32);
+                    load_tile<Tin, D, kLoaders>(reinterpret_cast<Tin *>(s + L::Q), KS,
+                                                static_cast<const Tin *>(p.q), row0, c * kC, p.T, D, 0,
+                                                lt);
                 if (REV)
-                    load_tile<Tin, NS>(reinterpret_cast<Tin *>(s + L::DO), L::DS,
-                                       static_cast<const Tin *>(p.d_o), row0, c * kC, p.T, D, c0, lane,
-                                       32);
+                    load_tile<Tin, NS, kLoaders>(reinterpret_cast<Tin *>(s + L::DO), L::DS,
+                                                 static_cast<const Tin *>(p.d_o), row0, c * kC, p.T, D,
+                                                 c0, lt);
                 const float *cf = w.coef + (ch0 + c) * kCoef;
-                for (int j = lane; j < kCoef / 4; j += 32) cp16(s + L::COEF + j * 16, cf + j * 4, true);
-                if (slice == 0 && lane == 0) {
+                if (lt < kCoef / 4) cp16(s + L::COEF + lt * 16, cf + lt * 4, true);
+                if (slice == 0 && lt == kLoaders - 1) {
                     prefetch_l2(w.W + (ch0 + c) * (kC * D), kC * D * 4);
                     prefetch_l2(w.Y + (ch0 + c) * (kC * D), kC * D * 4);
                     if (wantO) prefetch_l2(w.M + (ch0 + c) * (kC * kC), kC * kC * 4);
@@ -745,7 +759,7 @@ cudaError_t launch_chain_ns(const Args &p, const Scratch &w, long heads, cudaStr
     static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
     cudaError_t e = raise_smem<delta_chain<Tin, D, NS, REV, KEEP>>(bytes);
     if (e != cudaSuccess) return e;
-    delta_chain<Tin, D, NS, REV, KEEP><<<(unsigned)(heads * (D / NS)), 288, bytes, stream>>>(p, w);
+    delta_chain<Tin, D, NS, REV, KEEP><<<(unsigned)(heads * (D / NS)), kChainThreads, bytes, stream>>>(p, w);
     return after_launch();
 }
 

@@ -90,15 +90,15 @@ __global__ void __launch_bounds__(256, D <= 64 ? 2 : 1) delta_grad(Args p, Grads
     const size_t row0 = head * (size_t)p.T;
 
     auto load_slice = [&](int c0) {
-        load_tile<Tin, SL>(sO, SS, static_cast<const Tin *>(p.d_o), row0, t0, p.T, D, c0, tid, 256);
-        load_tile<float, SL>(sE, SS, gr_.E, ch * kC, 0, kC, D, c0, tid, 256);
-        load_tile<float, SL>(sZ, SS, gr_.Z, ch * kC, 0, kC, D, c0, tid, 256);
-        load_tile<float, SL, D>(sS0, SS, gr_.S0, ch * D, 0, D, D, c0, tid, 256);
-        load_tile<float, SL, D>(sDS, SS, gr_.dS, ch * D, 0, D, D, c0, tid, 256);
+        load_tile<Tin, SL, 256>(sO, SS, static_cast<const Tin *>(p.d_o), row0, t0, p.T, D, c0, tid);
+        load_tile<float, SL, 256>(sE, SS, gr_.E, ch * kC, 0, kC, D, c0, tid);
+        load_tile<float, SL, 256>(sZ, SS, gr_.Z, ch * kC, 0, kC, D, c0, tid);
+        load_tile<float, SL, 256, D>(sS0, SS, gr_.S0, ch * D, 0, D, D, c0, tid);
+        load_tile<float, SL, 256, D>(sDS, SS, gr_.dS, ch * D, 0, D, D, c0, tid);
         cp_commit();
     };
-    load_tile<Tin, D>(sK, KS, static_cast<const Tin *>(p.k), row0, t0, p.T, D, 0, tid, 256);
-    load_tile<Tin, D>(sQ, KS, static_cast<const Tin *>(p.q), row0, t0, p.T, D, 0, tid, 256);
+    load_tile<Tin, D, 256>(sK, KS, static_cast<const Tin *>(p.k), row0, t0, p.T, D, 0, tid);
+    load_tile<Tin, D, 256>(sQ, KS, static_cast<const Tin *>(p.q), row0, t0, p.T, D, 0, tid);
     load_slice(0);
     if (warp == 0) cumulate(p.g, row0, t0, p.T, G);
     if (tid >= 192) {

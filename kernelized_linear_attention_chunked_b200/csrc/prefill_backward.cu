@@ -119,15 +119,12 @@ __global__ void __launch_bounds__(kThreads) bwd_query(Args p) {
     auto tileV = [&](int u) { return tileK(u) + kB * RS; };
     auto prefetch = [&](int u) {
         const int t = (u % (qt + 1)) * kB;
-        load_tile<Tin, D>(tileK(u), RS, static_cast<const Tin *>(p.k), row0, t, p.T, D, 0, tid,
-                          kThreads);
-        load_tile<Tin, D>(tileV(u), RS, static_cast<const Tin *>(p.v), row0, t, p.T, D, 0, tid,
-                          kThreads);
+        load_tile<Tin, D, kThreads>(tileK(u), RS, static_cast<const Tin *>(p.k), row0, t, p.T, D, 0, tid);
+        load_tile<Tin, D, kThreads>(tileV(u), RS, static_cast<const Tin *>(p.v), row0, t, p.T, D, 0, tid);
         cp_commit();
     };
-    load_tile<Tin, D>(sQ, RS, static_cast<const Tin *>(p.q), row0, qt * kB, p.T, D, 0, tid, kThreads);
-    load_tile<Tin, D>(sO, RS, static_cast<const Tin *>(p.d_o), row0, qt * kB, p.T, D, 0, tid,
-                      kThreads);
+    load_tile<Tin, D, kThreads>(sQ, RS, static_cast<const Tin *>(p.q), row0, qt * kB, p.T, D, 0, tid);
+    load_tile<Tin, D, kThreads>(sO, RS, static_cast<const Tin *>(p.d_o), row0, qt * kB, p.T, D, 0, tid);
     prefetch(0);
     cp_wait_all();
     __syncthreads();
@@ -258,18 +255,16 @@ __global__ void __launch_bounds__(kThreads) bwd_key(Args p) {
     auto tileO = [&](int u) { return tileQ(u) + kB * RS; };
     auto stats = [&](int u) { return reinterpret_cast<float4 *>(sm + L::STAT) + (u & 1) * kB; };
     auto prefetch = [&](int u) {
-        load_tile<Tin, D>(tileQ(u), RS, static_cast<const Tin *>(p.q), row0, u * kB, p.T, D, 0, tid,
-                          kThreads);
-        load_tile<Tin, D>(tileO(u), RS, static_cast<const Tin *>(p.d_o), row0, u * kB, p.T, D, 0,
-                          tid, kThreads);
+        load_tile<Tin, D, kThreads>(tileQ(u), RS, static_cast<const Tin *>(p.q), row0, u * kB, p.T, D, 0, tid);
+        load_tile<Tin, D, kThreads>(tileO(u), RS, static_cast<const Tin *>(p.d_o), row0, u * kB, p.T, D, 0, tid);
         if (tid < kB) {
             const bool have = u * kB + tid < p.T;
             delta::cp16(stats(u) + tid, p.stat + row0 + (have ? u * kB + tid : 0), have);
         }
         cp_commit();
     };
-    load_tile<Tin, D>(sK, RS, static_cast<const Tin *>(p.k), row0, kt * kB, p.T, D, 0, tid, kThreads);
-    load_tile<Tin, D>(sV, RS, static_cast<const Tin *>(p.v), row0, kt * kB, p.T, D, 0, tid, kThreads);
+    load_tile<Tin, D, kThreads>(sK, RS, static_cast<const Tin *>(p.k), row0, kt * kB, p.T, D, 0, tid);
+    load_tile<Tin, D, kThreads>(sV, RS, static_cast<const Tin *>(p.v), row0, kt * kB, p.T, D, 0, tid);
     prefetch(kt);
     cp_wait_all();
     __syncthreads();
