@@ -146,7 +146,7 @@ __device__ __forceinline__ void cumulate(const float *g, size_t row0, int t0, in
 }
 
 // sX = (1 + A)^-1 for the strictly lower triangular A (64 x 64, both with row
-// stride kTS), by four warps. Diagonal 16 x 16 blocks by forward substitution,
+// stride kTS), by the CTA's first four warps. Diagonal 16 x 16 blocks by forward substitution,
 // one column per lane; then the blocks below them, 16 to 32 to 64 rows, by
 //     X21 = -X22 (A21 X11),
 // where a warp's own columns need no other warp's. The blocks above the
@@ -154,7 +154,7 @@ __device__ __forceinline__ void cumulate(const float *g, size_t row0, int t0, in
 __device__ __forceinline__ void invert(const float *sA, float *sX, int warp, int lane) {
     using namespace tf;
     const int g = lane >> 2, t2 = 2 * (lane & 3);
-    {
+    if (warp < 4) {
         const int j = lane & 15;
         const float *A = sA + 16 * warp * kTS + 16 * warp;
         float x[16];
@@ -171,7 +171,7 @@ __device__ __forceinline__ void invert(const float *sA, float *sX, int warp, int
         }
     }
     __syncthreads();
-    {  // blocks (1, 0) and (3, 2): warp w takes eight columns of pair w / 2
+    if (warp < 4) {  // blocks (1, 0) and (3, 2): warp w takes eight columns of pair w / 2
         const int r0 = 32 * (warp >> 1), c = r0 + 8 * (warp & 1);
         float acc[1][4];
         clear(acc);
@@ -192,7 +192,7 @@ __device__ __forceinline__ void invert(const float *sA, float *sX, int warp, int
         *reinterpret_cast<float2 *>(O + (g + 8) * kTS + t2) = make_float2(-acc[0][2], -acc[0][3]);
     }
     __syncthreads();
-    {  // the lower left 32 x 32 block: warp w takes its columns 8 w .. 8 w + 7
+    if (warp < 4) {  // the lower left 32 x 32 block: warp w takes its columns 8 w .. 8 w + 7
         const int c = 8 * warp;
         float *P = sX + 32 + c;
 #pragma unroll
@@ -239,19 +239,21 @@ struct PrepSmem {
     static constexpr int BYTES = COEF + 3 * kC * 4;
 };
 
-template <int D>
-__device__ __forceinline__ void store_frags(float *dst, const float (&acc)[D / 8][4], int warp,
+// Tiles first .. first + N - 1 of row block rb of a [64, D] matrix in fragment order.
+template <int D, int N>
+__device__ __forceinline__ void store_frags(float *dst, const float (&acc)[N][4], int rb, int first,
                                             int lane) {
-    float4 *d = reinterpret_cast<float4 *>(dst) + (size_t)warp * (D / 8) * 32 + lane;
+    float4 *d = reinterpret_cast<float4 *>(dst) + (size_t)(rb * (D / 8) + first) * 32 + lane;
 #pragma unroll
-    for (int nt = 0; nt < D / 8; ++nt)
+    for (int nt = 0; nt < N; ++nt)
         d[nt * 32] = make_float4(acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]);
 }
 
-// What each chunk needs of itself alone; 4 warps, warp w = rows 16 w .. 16 w + 15.
+// What each chunk needs of itself alone. 8 warps: 16 rows (warp % 4) and half the
+// columns each, of a triangular product every other eight.
 // f: the forward chain's operands; r: the reverse chain's (BACK only).
 template <typename Tin, int D, bool BACK>
-__global__ void __launch_bounds__(128) delta_prep(Args p, Scratch f, Scratch r) {
+__global__ void __launch_bounds__(256) delta_prep(Args p, Scratch f, Scratch r) {
     using namespace tf;
     using L = PrepSmem<Tin, D, BACK>;
     constexpr int KS = L::KS, TI = Parts<Tin>::N;
@@ -269,17 +271,17 @@ __global__ void __launch_bounds__(128) delta_prep(Args p, Scratch f, Scratch r) 
     const int t0 = (int)(ch % p.nc) * kC;
     const size_t row0 = head * (size_t)p.T;
 
-    load_tile<Tin, D, 128>(sK, KS, static_cast<const Tin *>(p.k), row0, t0, p.T, D, 0, tid);
+    load_tile<Tin, D, 256>(sK, KS, static_cast<const Tin *>(p.k), row0, t0, p.T, D, 0, tid);
     if (BACK || p.o)
-        load_tile<Tin, D, 128>(sQ, KS, static_cast<const Tin *>(p.q), row0, t0, p.T, D, 0, tid);
-    load_tile<Tin, D, 128>(sV, KS, static_cast<const Tin *>(p.v), row0, t0, p.T, D, 0, tid);
+        load_tile<Tin, D, 256>(sQ, KS, static_cast<const Tin *>(p.q), row0, t0, p.T, D, 0, tid);
+    load_tile<Tin, D, 256>(sV, KS, static_cast<const Tin *>(p.v), row0, t0, p.T, D, 0, tid);
     if (BACK)
-        load_tile<Tin, D, 128>(sO, KS, static_cast<const Tin *>(p.d_o), row0, t0, p.T, D, 0, tid);
+        load_tile<Tin, D, 256>(sO, KS, static_cast<const Tin *>(p.d_o), row0, t0, p.T, D, 0, tid);
     cp_commit();
     if (warp == 0) cumulate(p.g, row0, t0, p.T, G);
-    if (tid >= 64) {
-        const int t = t0 + tid - 64;
-        beta[tid - 64] = t < p.T ? p.beta[row0 + t] : 0.f;
+    if (tid >= 192) {
+        const int t = t0 + tid - 192;
+        beta[tid - 192] = t < p.T ? p.beta[row0 + t] : 0.f;
     }
     cp_wait_all();
     __syncthreads();
@@ -300,88 +302,95 @@ __global__ void __launch_bounds__(128) delta_prep(Args p, Scratch f, Scratch r) 
     }
     __syncthreads();
 
-    const int m0 = 16 * warp, nt_end = 2 * (warp + 1);  // column tiles up to the diagonal block
-    float kk[8][4], qk[8][4];
-    clear(kk);
-    clear(qk);
-    gemm<TI, TI, 8, true>(
-        kk, 0, D / 16, [&](int m, int k) { return quad<true, true>(sK + m0 * KS, KS, m, k); },
-        [&](int n, int k) { return quad<true, true>(sK, KS, n, k); }, nt_end);
-    if (BACK || p.o)
-        gemm<TI, TI, 8, true>(
-            qk, 0, D / 16, [&](int m, int k) { return quad<true, true>(sQ + m0 * KS, KS, m, k); },
-            [&](int n, int k) { return quad<true, true>(sK, KS, n, k); }, nt_end);
+    const int rb = warp & 3, hf = warp >> 2, m0 = 16 * rb;
+    const int nt_end = rb + 1;  // this warp's column tiles up to the diagonal block
+    {
+        float kk[4][4], qk[4][4];
+        clear(kk);
+        clear(qk);
+        // column 8 nt + g of the warp's tiles is column 16 nt + 8 hf + g of the product
+        auto kcol = [&](int n, int k) {
+            return quad<true, true>(sK, KS, 2 * (n & ~7) + 8 * hf + (n & 7), k);
+        };
+        gemm<TI, TI, 4, true>(
+            kk, 0, D / 16, [&](int m, int k) { return quad<true, true>(sK + m0 * KS, KS, m, k); }, kcol,
+            nt_end);
+        if (BACK || p.o)
+            gemm<TI, TI, 4, true>(
+                qk, 0, D / 16, [&](int m, int k) { return quad<true, true>(sQ + m0 * KS, KS, m, k); },
+                kcol, nt_end);
+        float4 *d = BACK ? nullptr
+                         : reinterpret_cast<float4 *>(f.M + ch * (kC * kC)) + (size_t)rb * 8 * 32 + lane;
 #pragma unroll
-    for (int nt = 0; nt < 8; ++nt) {
-        if (nt >= nt_end) continue;
+        for (int nt = 0; nt < 4; ++nt) {
+            if (nt >= nt_end) continue;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int i = m0 + gr + (e & 2 ? 8 : 0), j = 8 * nt + t2 + (e & 1);
-            const float dec = i >= j ? expf((float)(G[i] - G[j])) : 0.f;
-            sA[i * kTS + j] = i > j ? kk[nt][e] * dec * beta[j] : 0.f;
-            qk[nt][e] = i >= j ? qk[nt][e] * dec : 0.f;
-            if (BACK)
-                sM[i * kTS + j] = qk[nt][e];
-            else
-                qk[nt][e] *= p.scale * beta[j];
+            for (int e = 0; e < 4; ++e) {
+                const int i = m0 + gr + (e & 2 ? 8 : 0), j = 8 * (2 * nt + hf) + t2 + (e & 1);
+                const float dec = i >= j ? expf((float)(G[i] - G[j])) : 0.f;
+                sA[i * kTS + j] = i > j ? kk[nt][e] * dec * beta[j] : 0.f;
+                qk[nt][e] = i >= j ? qk[nt][e] * dec : 0.f;
+                if (BACK)
+                    sM[i * kTS + j] = qk[nt][e];
+                else
+                    qk[nt][e] *= p.scale * beta[j];
+            }
+            if (!BACK && p.o)
+                d[(2 * nt + hf) * 32] = make_float4(qk[nt][0], qk[nt][1], qk[nt][2], qk[nt][3]);
         }
-    }
-    if (!BACK && p.o) {
-        float4 *d = reinterpret_cast<float4 *>(f.M + ch * (kC * kC)) + (size_t)warp * 8 * 32 + lane;
-#pragma unroll
-        for (int nt = 0; nt < 8; ++nt)
-            if (nt < nt_end) d[nt * 32] = make_float4(qk[nt][0], qk[nt][1], qk[nt][2], qk[nt][3]);
     }
     __syncthreads();
     invert(sA, sX, warp, lane);
 
-    float acc[D / 8][4];
+    constexpr int ND = D / 16;  // this warp's tiles of a [64, D] product
+    const int d0 = hf * (D / 2), td = hf * ND;
+    float acc[ND][4];
     clear(acc);
-    gemm<2, TI, D / 8, false>(  // X V
-        acc, 0, warp + 1, [&](int m, int k) { return quad<true, false>(sX + m0 * kTS, kTS, m, k); },
-        [&](int n, int k) { return quad<false, false>(sV, KS, n, k); });
-    store_frags<D>(f.Y + ch * (kC * D), acc, warp, lane);
+    gemm<2, TI, ND, false>(  // X V
+        acc, 0, rb + 1, [&](int m, int k) { return quad<true, false>(sX + m0 * kTS, kTS, m, k); },
+        [&](int n, int k) { return quad<false, false>(sV + d0, KS, n, k); });
+    store_frags<D>(f.Y + ch * (kC * D), acc, rb, td, lane);
+    auto kcols = [&](int n, int k) { return quad<false, false>(sK + d0, KS, n, k); };
     clear(acc);
-    gemm<2, TI, D / 8, false>(  // X diag(a) K
-        acc, 0, warp + 1,
+    gemm<2, TI, ND, false>(  // X diag(a) K
+        acc, 0, rb + 1,
         [&](int m, int k) {
             return scaled<false>(quad<true, false>(sX + m0 * kTS, kTS, m, k), ca, k);
         },
-        [&](int n, int k) { return quad<false, false>(sK, KS, n, k); });
-    store_frags<D>(f.W + ch * (kC * D), acc, warp, lane);
+        kcols);
+    store_frags<D>(f.W + ch * (kC * D), acc, rb, td, lane);
     if (!BACK) return;
 
     // Z0 = X^T (scale diag(beta) M^T dO), W' = X^T diag(beta c) K: the
     // transposed factors reach from a row's own block to the last one
     clear(acc);
-    gemm<2, TI, D / 8, false>(
-        acc, warp, 4, [&](int m, int k) { return quad<false, false>(sM + m0, kTS, m, k); },
-        [&](int n, int k) { return quad<false, false>(sO, KS, n, k); });
+    gemm<2, TI, ND, false>(
+        acc, rb, 4, [&](int m, int k) { return quad<false, false>(sM + m0, kTS, m, k); },
+        [&](int n, int k) { return quad<false, false>(sO + d0, KS, n, k); });
     __syncthreads();  // every warp has read V
     {
         const float s0 = p.scale * beta[m0 + gr], s1 = p.scale * beta[m0 + gr + 8];
 #pragma unroll
-        for (int nt = 0; nt < D / 8; ++nt) {
-            *reinterpret_cast<float2 *>(sP + (m0 + gr) * KS + 8 * nt + t2) =
-                make_float2(s0 * acc[nt][0], s0 * acc[nt][1]);
-            *reinterpret_cast<float2 *>(sP + (m0 + gr + 8) * KS + 8 * nt + t2) =
-                make_float2(s1 * acc[nt][2], s1 * acc[nt][3]);
+        for (int nt = 0; nt < ND; ++nt) {
+            float *x = sP + (m0 + gr) * KS + d0 + 8 * nt + t2;
+            *reinterpret_cast<float2 *>(x) = make_float2(s0 * acc[nt][0], s0 * acc[nt][1]);
+            *reinterpret_cast<float2 *>(x + 8 * KS) = make_float2(s1 * acc[nt][2], s1 * acc[nt][3]);
         }
     }
     __syncthreads();
     clear(acc);
-    gemm<2, 2, D / 8, false>(
-        acc, warp, 4, [&](int m, int k) { return quad<false, false>(sX + m0, kTS, m, k); },
-        [&](int n, int k) { return quad<false, false>(sP, KS, n, k); });
-    store_frags<D>(r.Y + ch * (kC * D), acc, warp, lane);
+    gemm<2, 2, ND, false>(
+        acc, rb, 4, [&](int m, int k) { return quad<false, false>(sX + m0, kTS, m, k); },
+        [&](int n, int k) { return quad<false, false>(sP + d0, KS, n, k); });
+    store_frags<D>(r.Y + ch * (kC * D), acc, rb, td, lane);
     clear(acc);
-    gemm<2, TI, D / 8, false>(
-        acc, warp, 4,
+    gemm<2, TI, ND, false>(
+        acc, rb, 4,
         [&](int m, int k) {
             return scaled<false>(quad<false, false>(sX + m0, kTS, m, k), bc, k);
         },
-        [&](int n, int k) { return quad<false, false>(sK, KS, n, k); });
-    store_frags<D>(r.W + ch * (kC * D), acc, warp, lane);
+        kcols);
+    store_frags<D>(r.W + ch * (kC * D), acc, rb, td, lane);
 }
 
 template <typename Tin, int D, int NS, bool REV>
@@ -749,7 +758,7 @@ cudaError_t launch_prep(const Args &p, const Scratch &f, const Scratch &r, long 
     static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
     cudaError_t e = raise_smem<delta_prep<Tin, D, BACK>>(bytes);
     if (e != cudaSuccess) return e;
-    delta_prep<Tin, D, BACK><<<(unsigned)(heads * p.nc), 128, bytes, stream>>>(p, f, r);
+    delta_prep<Tin, D, BACK><<<(unsigned)(heads * p.nc), 256, bytes, stream>>>(p, f, r);
     return after_launch();
 }
 
