@@ -123,26 +123,39 @@ __device__ __forceinline__ void load_tile(T *dst, int stride, const T *src, size
     }
 }
 
-// The running sums of one chunk's log decays, by one warp: G[64] (64 bits).
-__device__ __forceinline__ void cumulate(const float *g, size_t row0, int t0, int T, double *G) {
+// The running sums of one chunk's log decays, in base 2 and as two floats each (a
+// 64-bit sum's upper and lower part): an exponent is taken as (hi_i - hi_j) +
+// (lo_i - lo_j), whose error is 2^-24 of the difference, not of the sums. One
+// warp; v: tokens 2 lane and 2 lane + 1 of the chunk.
+__device__ __forceinline__ float2 load_decays(const float *g, size_t row0, int t0, int T) {
+    const int t = t0 + 2 * (threadIdx.x & 31);
+    return make_float2(t < T ? g[row0 + t] : 0.f, t + 1 < T ? g[row0 + t + 1] : 0.f);
+}
+__device__ __forceinline__ void cumulate(float2 v, float *hi, float *lo) {
     const int lane = threadIdx.x & 31;
-    double x[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int t = t0 + 2 * lane + i;
-        float v = t < T ? g[row0 + t] : 0.f;
-        v = v < kMinLog ? kMinLog : v;
-        x[i] = v;
-    }
-    x[1] += x[0];
-    double sum = x[1];
+    const double x0 = v.x < kMinLog ? kMinLog : v.x;
+    double x1 = v.y < kMinLog ? kMinLog : v.y;
+    x1 += x0;
+    double sum = x1;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
         const double up = __shfl_up_sync(0xffffffffu, sum, off);
         if (lane >= off) sum += up;
     }
-    G[2 * lane] = sum - x[1] + x[0];
-    G[2 * lane + 1] = sum;
+    constexpr double kLog2e = 1.4426950408889634;
+    const double s0 = (sum - x1 + x0) * kLog2e, s1 = sum * kLog2e;
+    const float h0 = (float)s0, h1 = (float)s1;
+    *reinterpret_cast<float2 *>(hi + 2 * lane) = make_float2(h0, h1);
+    *reinterpret_cast<float2 *>(lo + 2 * lane) =
+        make_float2((float)(s0 - (double)h0), (float)(s1 - (double)h1));
+}
+
+// exp(G_i - G_j) for two neighbouring j of the sums hi, lo.
+__device__ __forceinline__ float2 decay2(float hi_i, float lo_i, const float *hi, const float *lo,
+                                         int j) {
+    const float2 h = *reinterpret_cast<const float2 *>(hi + j);
+    const float2 l = *reinterpret_cast<const float2 *>(lo + j);
+    return make_float2(exp2f((hi_i - h.x) + (lo_i - l.x)), exp2f((hi_i - h.y) + (lo_i - l.y)));
 }
 
 // sX = (1 + A)^-1 for the strictly lower triangular A (64 x 64, both with row
@@ -159,12 +172,11 @@ __device__ __forceinline__ void invert(const float *sA, float *sX, int warp, int
         const float *A = sA + 16 * warp * kTS + 16 * warp;
         float x[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float s = i == j ? 1.f : 0.f;
+        for (int i = 0; i < 16; ++i) x[i] = i == j ? 1.f : 0.f;
 #pragma unroll
-            for (int m = 0; m < i; ++m) s = fmaf(-A[i * kTS + m], x[m], s);
-            x[i] = s;
-        }
+        for (int m = 0; m < 15; ++m)  // x[m] is final: take it out of the rows below
+#pragma unroll
+            for (int i = m + 1; i < 16; ++i) x[i] = fmaf(-A[i * kTS + m], x[m], x[i]);
         if (lane < 16) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) sX[(16 * warp + i) * kTS + 16 * warp + j] = x[i];
@@ -234,9 +246,8 @@ struct PrepSmem {
     static constexpr int K = 0, Q = IN, V = 2 * IN, DO = V + (BACK ? P : IN);
     static constexpr int A = DO + (BACK ? IN : 0);
     static constexpr int X = A + kC * kTS * 4, M = X + kC * kTS * 4;
-    static constexpr int G = M + (BACK ? kC * kTS * 4 : 0);
-    static constexpr int COEF = G + kC * 8;  // beta, a, beta c
-    static constexpr int BYTES = COEF + 3 * kC * 4;
+    static constexpr int COEF = M + (BACK ? kC * kTS * 4 : 0);  // beta, a, beta c, G (hi, lo)
+    static constexpr int BYTES = COEF + 5 * kC * 4;
 };
 
 // Tiles first .. first + N - 1 of row block rb of a [64, D] matrix in fragment order.
@@ -262,8 +273,8 @@ __global__ void __launch_bounds__(256) delta_prep(Args p, Scratch f, Scratch r) 
     Tin *sV = reinterpret_cast<Tin *>(sm + L::V), *sO = reinterpret_cast<Tin *>(sm + L::DO);
     float *sA = reinterpret_cast<float *>(sm + L::A), *sX = reinterpret_cast<float *>(sm + L::X);
     float *sM = reinterpret_cast<float *>(sm + L::M), *sP = reinterpret_cast<float *>(sm + L::V);
-    double *G = reinterpret_cast<double *>(sm + L::G);
     float *beta = reinterpret_cast<float *>(sm + L::COEF), *ca = beta + kC, *bc = ca + kC;
+    float *ghi = bc + kC, *glo = ghi + kC;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int gr = lane >> 2, t2 = 2 * (lane & 3);
     const size_t ch = blockIdx.x;  // head * nc + chunk
@@ -271,6 +282,8 @@ __global__ void __launch_bounds__(256) delta_prep(Args p, Scratch f, Scratch r) 
     const int t0 = (int)(ch % p.nc) * kC;
     const size_t row0 = head * (size_t)p.T;
 
+    float2 v2 = make_float2(0.f, 0.f);
+    if (warp == 0) v2 = load_decays(p.g, row0, t0, p.T);
     load_tile<Tin, D, 256>(sK, KS, static_cast<const Tin *>(p.k), row0, t0, p.T, D, 0, tid);
     if (BACK || p.o)
         load_tile<Tin, D, 256>(sQ, KS, static_cast<const Tin *>(p.q), row0, t0, p.T, D, 0, tid);
@@ -278,7 +291,7 @@ __global__ void __launch_bounds__(256) delta_prep(Args p, Scratch f, Scratch r) 
     if (BACK)
         load_tile<Tin, D, 256>(sO, KS, static_cast<const Tin *>(p.d_o), row0, t0, p.T, D, 0, tid);
     cp_commit();
-    if (warp == 0) cumulate(p.g, row0, t0, p.T, G);
+    if (warp == 0) cumulate(v2, ghi, glo);
     if (tid >= 192) {
         const int t = t0 + tid - 192;
         beta[tid - 192] = t < p.T ? p.beta[row0 + t] : 0.f;
@@ -286,7 +299,8 @@ __global__ void __launch_bounds__(256) delta_prep(Args p, Scratch f, Scratch r) 
     cp_wait_all();
     __syncthreads();
     if (tid < kC) {
-        const float a = expf((float)G[tid]), c = expf((float)(G[kC - 1] - G[tid]));
+        const float a = exp2f(ghi[tid] + glo[tid]);
+        const float c = exp2f((ghi[kC - 1] - ghi[tid]) + (glo[kC - 1] - glo[tid]));
         ca[tid] = a;
         bc[tid] = beta[tid] * c;
         float *cf = f.coef + ch * kCoef;
@@ -304,39 +318,57 @@ __global__ void __launch_bounds__(256) delta_prep(Args p, Scratch f, Scratch r) 
 
     const int rb = warp & 3, hf = warp >> 2, m0 = 16 * rb;
     const int nt_end = rb + 1;  // this warp's column tiles up to the diagonal block
+    const bool wantQ = BACK || p.o;
     {
+        // K K^T and Q K^T together: they share their B operand
+        const int t4 = 4 * (lane & 3);
         float kk[4][4], qk[4][4];
         clear(kk);
         clear(qk);
-        // column 8 nt + g of the warp's tiles is column 16 nt + 8 hf + g of the product
-        auto kcol = [&](int n, int k) {
-            return quad<true, true>(sK, KS, 2 * (n & ~7) + 8 * hf + (n & 7), k);
-        };
-        gemm<TI, TI, 4, true>(
-            kk, 0, D / 16, [&](int m, int k) { return quad<true, true>(sK + m0 * KS, KS, m, k); }, kcol,
-            nt_end);
-        if (BACK || p.o)
-            gemm<TI, TI, 4, true>(
-                qk, 0, D / 16, [&](int m, int k) { return quad<true, true>(sQ + m0 * KS, KS, m, k); },
-                kcol, nt_end);
+#pragma unroll 1
+        for (int ks = 0; ks < D / 16; ++ks) {
+            const int k = 16 * ks + t4;
+            FragA<TI> ak, aq;
+            ak.set(quad<true, true>(sK + m0 * KS, KS, gr, k), quad<true, true>(sK + m0 * KS, KS, gr + 8, k));
+            if (wantQ)
+                aq.set(quad<true, true>(sQ + m0 * KS, KS, gr, k),
+                       quad<true, true>(sQ + m0 * KS, KS, gr + 8, k));
+#pragma unroll
+            for (int nt = 0; nt < 4; nt += 2) {
+                if (nt >= nt_end) continue;
+                FragB<TI> b[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e)  // beyond the diagonal block: computed, not used
+                    b[e].set(quad<true, true>(sK, KS, 8 * (2 * (nt + e) + hf) + gr, k));
+                mma_step<TI, TI, 2>(*reinterpret_cast<float(*)[2][4]>(&kk[nt]), ak, b);
+                if (wantQ) mma_step<TI, TI, 2>(*reinterpret_cast<float(*)[2][4]>(&qk[nt]), aq, b);
+            }
+        }
         float4 *d = BACK ? nullptr
                          : reinterpret_cast<float4 *>(f.M + ch * (kC * kC)) + (size_t)rb * 8 * 32 + lane;
+        const float gh[2] = {ghi[m0 + gr], ghi[m0 + gr + 8]}, gl[2] = {glo[m0 + gr], glo[m0 + gr + 8]};
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt) {
             if (nt >= nt_end) continue;
+            const int j = 8 * (2 * nt + hf) + t2;
+            const float2 be = *reinterpret_cast<const float2 *>(beta + j);
+            float m[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int i = m0 + gr + (e & 2 ? 8 : 0), j = 8 * (2 * nt + hf) + t2 + (e & 1);
-                const float dec = i >= j ? expf((float)(G[i] - G[j])) : 0.f;
-                sA[i * kTS + j] = i > j ? kk[nt][e] * dec * beta[j] : 0.f;
-                qk[nt][e] = i >= j ? qk[nt][e] * dec : 0.f;
-                if (BACK)
-                    sM[i * kTS + j] = qk[nt][e];
-                else
-                    qk[nt][e] *= p.scale * beta[j];
+            for (int h = 0; h < 2; ++h) {
+                const int i = m0 + gr + 8 * h;
+                const float2 dec = decay2(gh[h], gl[h], ghi, glo, j);
+                // (above the diagonal a decay may be infinite: chosen away, not multiplied)
+                *reinterpret_cast<float2 *>(sA + i * kTS + j) =
+                    make_float2(i > j ? kk[nt][2 * h] * dec.x * be.x : 0.f,
+                                i > j + 1 ? kk[nt][2 * h + 1] * dec.y * be.y : 0.f);
+                m[2 * h] = i >= j ? qk[nt][2 * h] * dec.x : 0.f;
+                m[2 * h + 1] = i >= j + 1 ? qk[nt][2 * h + 1] * dec.y : 0.f;
+                if (BACK) *reinterpret_cast<float2 *>(sM + i * kTS + j) = make_float2(m[2 * h], m[2 * h + 1]);
             }
-            if (!BACK && p.o)
-                d[(2 * nt + hf) * 32] = make_float4(qk[nt][0], qk[nt][1], qk[nt][2], qk[nt][3]);
+            if (!BACK && wantQ) {
+                const float s0 = p.scale * be.x, s1 = p.scale * be.y;
+                d[(2 * nt + hf) * 32] = make_float4(s0 * m[0], s1 * m[1], s0 * m[2], s1 * m[3]);
+            }
         }
     }
     __syncthreads();

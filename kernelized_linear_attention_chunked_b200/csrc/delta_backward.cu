@@ -48,9 +48,8 @@ struct GradSmem {
     static constexpr int E = DO + kC * SS * (int)sizeof(Tin), Z = E + kC * SS * 4;
     static constexpr int S0 = Z + kC * SS * 4, DS = S0 + D * SS * 4;
     static constexpr int M = DS + D * SS * 4, N = M + kC * kTS * 4;
-    static constexpr int G = N + kC * kTS * 4;
-    static constexpr int VEC = G + kC * 8;  // beta, a, c, dbeta [2], dG [2], end [8]
-    static constexpr int BYTES = VEC + (7 * kC + 8) * 4;
+    static constexpr int VEC = N + kC * kTS * 4;  // beta, a, c, G (hi, lo), dbeta [2], dG [2], end [8]
+    static constexpr int BYTES = VEC + (9 * kC + 8) * 4;
 };
 
 template <typename Tin>
@@ -79,9 +78,9 @@ __global__ void __launch_bounds__(256, D <= 64 ? 2 : 1) delta_grad(Args p, Grads
     float *sE = reinterpret_cast<float *>(sm + L::E), *sZ = reinterpret_cast<float *>(sm + L::Z);
     float *sS0 = reinterpret_cast<float *>(sm + L::S0), *sDS = reinterpret_cast<float *>(sm + L::DS);
     float *sM = reinterpret_cast<float *>(sm + L::M), *sN = reinterpret_cast<float *>(sm + L::N);
-    double *G = reinterpret_cast<double *>(sm + L::G);
     float *beta = reinterpret_cast<float *>(sm + L::VEC), *ca = beta + kC, *cc = ca + kC;
-    float *sdb = cc + kC, *sdG = sdb + 2 * kC, *send = sdG + 2 * kC;
+    float *ghi = cc + kC, *glo = ghi + kC;
+    float *sdb = glo + kC, *sdG = sdb + 2 * kC, *send = sdG + 2 * kC;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int gr = lane >> 2, t2 = 2 * (lane & 3);
     const int rb = warp & 3, hf = warp >> 2, m0 = 16 * rb;
@@ -97,10 +96,12 @@ __global__ void __launch_bounds__(256, D <= 64 ? 2 : 1) delta_grad(Args p, Grads
         load_tile<float, SL, 256, D>(sDS, SS, gr_.dS, ch * D, 0, D, D, c0, tid);
         cp_commit();
     };
+    float2 v2 = make_float2(0.f, 0.f);
+    if (warp == 0) v2 = load_decays(p.g, row0, t0, p.T);
     load_tile<Tin, D, 256>(sK, KS, static_cast<const Tin *>(p.k), row0, t0, p.T, D, 0, tid);
     load_tile<Tin, D, 256>(sQ, KS, static_cast<const Tin *>(p.q), row0, t0, p.T, D, 0, tid);
     load_slice(0);
-    if (warp == 0) cumulate(p.g, row0, t0, p.T, G);
+    if (warp == 0) cumulate(v2, ghi, glo);
     if (tid >= 192) {
         const int t = t0 + tid - 192;
         beta[tid - 192] = t < p.T ? p.beta[row0 + t] : 0.f;
@@ -108,8 +109,8 @@ __global__ void __launch_bounds__(256, D <= 64 ? 2 : 1) delta_grad(Args p, Grads
     cp_wait_all();
     __syncthreads();
     if (tid < kC) {
-        ca[tid] = expf((float)G[tid]);
-        cc[tid] = expf((float)(G[kC - 1] - G[tid]));
+        ca[tid] = exp2f(ghi[tid] + glo[tid]);
+        cc[tid] = exp2f((ghi[kC - 1] - ghi[tid]) + (glo[kC - 1] - glo[tid]));
     }
     // this warp's tiles of a 64 x 64 product: columns 8 (2 nt + hf), up to the diagonal block
     const int nt_end = rb + 1;
@@ -132,12 +133,17 @@ __global__ void __launch_bounds__(256, D <= 64 ? 2 : 1) delta_grad(Args p, Grads
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt) {
             if (nt >= nt_end) continue;
+            const int j = col(nt, 0);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int i = row(e), j = col(nt, e);
-                const float dec = i >= j ? expf((float)(G[i] - G[j])) : 0.f;
-                sN[i * kTS + j] = i > j ? kk[nt][e] * dec : 0.f;
-                sM[i * kTS + j] = i >= j ? qk[nt][e] * dec : 0.f;
+            for (int h = 0; h < 2; ++h) {
+                const int i = row(2 * h);
+                const float2 dec = decay2(ghi[i], glo[i], ghi, glo, j);
+                *reinterpret_cast<float2 *>(sN + i * kTS + j) =
+                    make_float2(i > j ? kk[nt][2 * h] * dec.x : 0.f,
+                                i > j + 1 ? kk[nt][2 * h + 1] * dec.y : 0.f);
+                *reinterpret_cast<float2 *>(sM + i * kTS + j) =
+                    make_float2(i >= j ? qk[nt][2 * h] * dec.x : 0.f,
+                                i >= j + 1 ? qk[nt][2 * h + 1] * dec.y : 0.f);
             }
         }
     }
@@ -222,12 +228,17 @@ __global__ void __launch_bounds__(256, D <= 64 ? 2 : 1) delta_grad(Args p, Grads
 #pragma unroll
     for (int nt = 0; nt < 4; ++nt) {
         if (nt >= nt_end) continue;
+        const int j = col(nt, 0);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int i = row(e), j = col(nt, e);
-            const float dec = i >= j ? expf((float)(G[i] - G[j])) : 0.f;
-            sM[i * kTS + j] = i >= j ? p.scale * pm[nt][e] * dec : 0.f;
-            sN[i * kTS + j] = i > j ? -pn[nt][e] * dec : 0.f;
+        for (int h = 0; h < 2; ++h) {
+            const int i = row(2 * h);
+            const float2 dec = decay2(ghi[i], glo[i], ghi, glo, j);
+            *reinterpret_cast<float2 *>(sM + i * kTS + j) =
+                make_float2(i >= j ? p.scale * pm[nt][2 * h] * dec.x : 0.f,
+                            i >= j + 1 ? p.scale * pm[nt][2 * h + 1] * dec.y : 0.f);
+            *reinterpret_cast<float2 *>(sN + i * kTS + j) =
+                make_float2(i > j ? -pn[nt][2 * h] * dec.x : 0.f,
+                            i > j + 1 ? -pn[nt][2 * h + 1] * dec.y : 0.f);
         }
     }
 #pragma unroll

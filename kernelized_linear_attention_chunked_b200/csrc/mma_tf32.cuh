@@ -180,9 +180,19 @@ __device__ __forceinline__ float4 quad(const __nv_bfloat16 *p, int stride, int m
         const float2 a = unpack(u.x), b = unpack(u.y);
         return make_float4(a.x, a.y, b.x, b.y);
     }
-    p += k * stride + mn;
-    return make_float4(__bfloat162float(p[0]), __bfloat162float(p[stride]),
-                       __bfloat162float(p[8 * stride]), __bfloat162float(p[9 * stride]));
+    // a transposed 16 x 8 matrix load: lanes 0 .. 15 name the rows, and lane (g, t)
+    // gets rows 2t, 2t + 1 and 2t + 8, 2t + 9 of column g. Every lane of the warp
+    // asks for the same mn - g and k - 2t; rows are 16-byte aligned.
+    const int lane = threadIdx.x & 31;
+    const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(
+        p + (k - 2 * (lane & 3) + (lane & 15)) * stride + mn - (lane >> 2)));
+    uint32_t u, v;
+    asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0, %1}, [%2];"
+                 : "=r"(u), "=r"(v)
+                 : "r"(at)
+                 : "memory");
+    const float2 a = unpack(u), b = unpack(v);
+    return make_float4(a.x, a.y, b.x, b.y);
 }
 // A quad times c[.] of its k.
 template <bool WIDE>
