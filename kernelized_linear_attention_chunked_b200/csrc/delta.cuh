@@ -328,20 +328,20 @@ __global__ void __launch_bounds__(256) delta_prep(Args p, Scratch f, Scratch r) 
 #pragma unroll 1
         for (int ks = 0; ks < D / 16; ++ks) {
             const int k = 16 * ks + t4;
-            FragA<TI> ak, aq;
-            ak.set(quad<true, true>(sK + m0 * KS, KS, gr, k), quad<true, true>(sK + m0 * KS, KS, gr + 8, k));
+            FragA<TI> ak[1], aq[1];
+            ak[0].set(quad<true, true>(sK + m0 * KS, KS, gr, k), quad<true, true>(sK + m0 * KS, KS, gr + 8, k));
             if (wantQ)
-                aq.set(quad<true, true>(sQ + m0 * KS, KS, gr, k),
+                aq[0].set(quad<true, true>(sQ + m0 * KS, KS, gr, k),
                        quad<true, true>(sQ + m0 * KS, KS, gr + 8, k));
 #pragma unroll
             for (int nt = 0; nt < 4; nt += 2) {
                 if (nt >= nt_end) continue;
-                FragB<TI> b[2];
+                FragB<TI> b[1][2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e)  // beyond the diagonal block: computed, not used
-                    b[e].set(quad<true, true>(sK, KS, 8 * (2 * (nt + e) + hf) + gr, k));
-                mma_step<TI, TI, 2>(*reinterpret_cast<float(*)[2][4]>(&kk[nt]), ak, b);
-                if (wantQ) mma_step<TI, TI, 2>(*reinterpret_cast<float(*)[2][4]>(&qk[nt]), aq, b);
+                    b[0][e].set(quad<true, true>(sK, KS, 8 * (2 * (nt + e) + hf) + gr, k));
+                mma_step<TI, TI, 2, 1>(*reinterpret_cast<float(*)[2][4]>(&kk[nt]), ak, b);
+                if (wantQ) mma_step<TI, TI, 2, 1>(*reinterpret_cast<float(*)[2][4]>(&qk[nt]), aq, b);
             }
         }
         float4 *d = BACK ? nullptr
@@ -428,11 +428,10 @@ __global__ void __launch_bounds__(256) delta_prep(Args p, Scratch f, Scratch r) 
 template <typename Tin, int D, int NS, bool REV>
 struct ChainSmem {
     static constexpr int KS = row_stride<D>();
-    static constexpr int SP = NS + 2;  // row stride of {hi, lo} pairs: rows 2t start 8t banks on
-    static constexpr int ST = NS + 4;  // row stride of fp32 B operands: rows 2t start 8t (24t) banks on
+    static constexpr int ST = NS + 4;  // row stride of B operands: rows 2t start 8t banks on
     static constexpr int DS = NS + 8;  // row stride of the dO slice
     static constexpr int IN = kC * KS * (int)sizeof(Tin);
-    static constexpr int S = 0, YC = S + D * SP * 8, Y = YC + kC * SP * 8;
+    static constexpr int S = 0, YC = S + D * ST * 4, Y = YC + kC * ST * 4;
     static constexpr int GQ = Y + kC * ST * 4;  // REV: Q^T diag(scale a) dO
     static constexpr int STAGE = GQ + (REV ? D * ST * 4 : 0);
     // one stage: K, Q, coefficients, (REV) the dO slice
@@ -445,32 +444,26 @@ struct ChainSmem {
     static constexpr int BYTES = STAGE + STAGES * STAGE_BYTES;
 };
 
-// {hi, lo} of two neighbours, 16 bytes.
-__device__ __forceinline__ float4 cut2(float x, float y) {
-    uint32_t h0, l0, h1, l1;
-    tf::split(x, h0, l0);
-    tf::split(y, h1, l1);
-    return make_float4(__uint_as_float(h0), __uint_as_float(l0), __uint_as_float(h1),
-                       __uint_as_float(l1));
-}
-
 // The walk over the chunks, one CTA per (head, NS value columns). Warps 0-3
 // carry the chain: they hold the state in registers (fp32, D / 4 rows each)
 // and take two dependent products per chunk. Warps 4-7 take the products that
 // hang off it: the outputs (forward) or Q^T dO (REV). Warps 8-11 bring K, Q and
 // the coefficients by asynchronous copies up to three chunks ahead, and calls
 // the next chunks' W, XV and M into L2; those come straight from there into
-// the fragments that use them, one chunk ahead. The state and the errors, B
-// operands that four warps read, are cut into their tf32 parts by the warp
-// that writes them.
+// the fragments that use them, one chunk ahead. The state and the errors pass
+// between the warps as fp32 and are cut into tf32 parts by each reader: shared
+// memory's bandwidth is what the walk runs out of, not its instructions (cut by
+// the writer, as pairs, the walk took 348 us instead of 339 us at B2 H16 T16384
+// d64).
 template <typename Tin, int D, int NS, bool REV, bool KEEP>
 __global__ void __launch_bounds__(kChainThreads, 1) delta_chain(Args p, Scratch w) {
     using namespace tf;
     using L = ChainSmem<Tin, D, NS, REV>;
-    constexpr int KS = L::KS, SP = L::SP, ST = L::ST, NT = NS / 8, TI = Parts<Tin>::N;
+    constexpr int KS = L::KS, ST = L::ST, NT = NS / 8, TI = Parts<Tin>::N;
     constexpr int MT = D >= 64 ? D / 64 : 1;  // 16-row tiles of the state per chain warp
+    constexpr int KP = D >= 32 ? 2 : 1;       // sixteens of k at a time
     extern __shared__ __align__(16) uint8_t sm[];
-    float2 *sS = reinterpret_cast<float2 *>(sm + L::S), *sYc = reinterpret_cast<float2 *>(sm + L::YC);
+    float *sS = reinterpret_cast<float *>(sm + L::S), *sYc = reinterpret_cast<float *>(sm + L::YC);
     float *sY = reinterpret_cast<float *>(sm + L::Y), *sG = reinterpret_cast<float *>(sm + L::GQ);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int gr = lane >> 2, t2 = 2 * (lane & 3);
@@ -540,7 +533,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain(Args p, Scratch 
                                                               8 * nt + t2);
                     S[mt][nt][2 * h] = x.x;
                     S[mt][nt][2 * h + 1] = x.y;
-                    *reinterpret_cast<float4 *>(sS + r * SP + 8 * nt + t2) = cut2(x.x, x.y);
+                    *reinterpret_cast<float2 *>(sS + r * ST + 8 * nt + t2) = x;
                 }
     }
     // the next chunk's W and XV (chain) or M (outputs), as fragments
@@ -580,26 +573,29 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain(Args p, Scratch 
         const Tin *sO = reinterpret_cast<const Tin *>(st + L::DO);
         const float *coef = reinterpret_cast<const float *>(st + L::COEF);
         float o[NT][4];
-        // a column's four k of the state or the errors, in parts
-        auto parts = [&](const float2 *x, int n, int k) {
-            x += k * SP + n;
-            FragB<2> b;
-            b.set(x[0], x[SP], x[8 * SP], x[9 * SP]);
-            return b;
+        // W's or M's columns 16 ks .. as an A operand
+        auto frag_a = [&](auto &a, int ks) {
+            const float4 w0 = W[2 * ks], w1 = W[2 * ks + 1];
+            a.set(make_float4(w0.x, w0.y, w1.x, w1.y), make_float4(w0.z, w0.w, w1.z, w1.w));
         };
+        // a column's four k of the state or the errors
+        auto column = [&](const float *x, int n, int k) { return quad<false, false>(x, ST, n, k); };
         if (chain) {
             // E = XV - W S0 (REV: Z = Z0 + W' dS)
             float acc[NT][4];
             clear(acc);
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-                FragA<2> a;
-                const float4 w0 = W[2 * ks], w1 = W[2 * ks + 1];
-                a.set(make_float4(w0.x, w0.y, w1.x, w1.y), make_float4(w0.z, w0.w, w1.z, w1.w));
-                FragB<2> b[NT];
+            for (int k0 = 0; k0 < D / 16; k0 += KP) {
+                FragA<2> a[KP];
+                FragB<2> b[KP][NT];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) b[nt] = parts(sS, 8 * nt + gr, 16 * ks + t2);
-                mma_step<2, 2, NT>(acc, a, b);
+                for (int s = 0; s < KP; ++s) {
+                    frag_a(a[s], k0 + s);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        b[s][nt].set(column(sS, 8 * nt + gr, 16 * (k0 + s) + t2));
+                }
+                mma_step<2, 2, NT, KP>(acc, a, b);
             }
             const float k0 = coef[kC + m0 + gr], k1 = coef[kC + m0 + gr + 8];
 #pragma unroll
@@ -610,8 +606,10 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain(Args p, Scratch 
                 const float2 y1 = make_float2(fmaf(sg, acc[nt][2], Y0[nt].z),
                                               fmaf(sg, acc[nt][3], Y0[nt].w));
                 const int n = 8 * nt + t2;
-                *reinterpret_cast<float4 *>(sYc + (m0 + gr) * SP + n) = cut2(k0 * y0.x, k0 * y0.y);
-                *reinterpret_cast<float4 *>(sYc + (m0 + gr + 8) * SP + n) = cut2(k1 * y1.x, k1 * y1.y);
+                *reinterpret_cast<float2 *>(sYc + (m0 + gr) * ST + n) =
+                    make_float2(k0 * y0.x, k0 * y0.y);
+                *reinterpret_cast<float2 *>(sYc + (m0 + gr + 8) * ST + n) =
+                    make_float2(k1 * y1.x, k1 * y1.y);
                 if (wantO) {
                     *reinterpret_cast<float2 *>(sY + (m0 + gr) * ST + n) = y0;
                     *reinterpret_cast<float2 *>(sY + (m0 + gr + 8) * ST + n) = y1;
@@ -625,34 +623,9 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain(Args p, Scratch 
             if (i + 1 < p.nc) load_frags();
         } else if (wantO) {
             clear(o);
-            if constexpr (TI == 1) {  // the state's nearest tf32 values alone
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    FragA<1> a;
-                    const int k = 16 * ks + t2;
-                    a.set(quad<true, false>(sQ + m0 * KS, KS, gr, k),
-                          quad<true, false>(sQ + m0 * KS, KS, gr + 8, k));
-                    FragB<1> b[NT];
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const float2 *x = sS + k * SP + 8 * nt + gr;
-                        b[nt].set(make_float4(x[0].x, x[SP].x, x[8 * SP].x, x[9 * SP].x));
-                    }
-                    mma_step<1, 1, NT>(o, a, b);
-                }
-            } else {
-#pragma unroll 2
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    FragA<2> a;
-                    const int k = 16 * ks + t2;
-                    a.set(quad<true, false>(sQ + m0 * KS, KS, gr, k),
-                          quad<true, false>(sQ + m0 * KS, KS, gr + 8, k));
-                    FragB<2> b[NT];
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) b[nt] = parts(sS, 8 * nt + gr, k);
-                    mma_step<2, 2, NT>(o, a, b);
-                }
-            }
+            gemm<TI, TI, NT, false>(
+                o, 0, D / 16, [&](int m, int k) { return quad<true, false>(sQ + m0 * KS, KS, m, k); },
+                [&](int n, int k) { return column(sS, n, k); });
             const float s0 = coef[m0 + gr], s1 = coef[m0 + gr + 8];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -688,17 +661,22 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain(Args p, Scratch 
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) clear(acc[mt]);
 #pragma unroll
-            for (int ks = 0; ks < kC / 16; ++ks) {
-                const int k = 16 * ks + t2;
-                FragB<2> b[NT];
+            for (int k0 = 0; k0 < kC / 16; k0 += 2) {
+                FragB<2> b[2][NT];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) b[nt] = parts(sYc, 8 * nt + gr, k);
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        b[s][nt].set(column(sYc, 8 * nt + gr, 16 * (k0 + s) + t2));
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
-                    FragA<TI> a;
+                    FragA<TI> a[2];
                     const Tin *ka = sK + 16 * (MT * warp + mt);
-                    a.set(quad<false, false>(ka, KS, gr, k), quad<false, false>(ka, KS, gr + 8, k));
-                    mma_step<TI, 2, NT>(acc[mt], a, b);
+#pragma unroll
+                    for (int s = 0; s < 2; ++s)
+                        a[s].set(quad<false, false>(ka, KS, gr, 16 * (k0 + s) + t2),
+                                 quad<false, false>(ka, KS, gr + 8, 16 * (k0 + s) + t2));
+                    mma_step<TI, 2, NT, 2>(acc[mt], a, b);
                 }
             }
 #pragma unroll
@@ -720,21 +698,20 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain(Args p, Scratch 
                     }
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
-                        *reinterpret_cast<float4 *>(sS + (srow(mt) + 8 * h) * SP + n) =
-                            cut2(S[mt][nt][2 * h], S[mt][nt][2 * h + 1]);
+                        *reinterpret_cast<float2 *>(sS + (srow(mt) + 8 * h) * ST + n) =
+                            make_float2(S[mt][nt][2 * h], S[mt][nt][2 * h + 1]);
                 }
         } else if (!chain && wantO) {
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
                 if (ks > (warp & 3)) continue;
-                FragA<TI> a;
-                const float4 w0 = W[2 * ks], w1 = W[2 * ks + 1];
-                a.set(make_float4(w0.x, w0.y, w1.x, w1.y), make_float4(w0.z, w0.w, w1.z, w1.w));
-                FragB<TI> b[NT];
+                FragA<TI> a[1];
+                frag_a(a[0], ks);
+                FragB<TI> b[1][NT];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
-                    b[nt].set(quad<false, false>(sY, ST, 8 * nt + gr, 16 * ks + t2));
-                mma_step<TI, TI, NT>(o, a, b);
+                    b[0][nt].set(column(sY, 8 * nt + gr, 16 * ks + t2));
+                mma_step<TI, TI, NT, 1>(o, a, b);
             }
             if (i + 1 < p.nc) load_frags();
             Tin *od = static_cast<Tin *>(p.o);

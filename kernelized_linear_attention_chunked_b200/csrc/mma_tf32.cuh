@@ -90,62 +90,47 @@ struct FragB {
                 hi[i] = __float_as_uint(x[i]);
         }
     }
-    // the same from values cut before ({hi, lo} each)
-    __device__ __forceinline__ void set(float2 a, float2 b, float2 c, float2 d) {
-        const float2 x[4] = {a, b, c, d};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            hi[i] = __float_as_uint(x[i].x);
-            lo[i] = __float_as_uint(x[i].y);
-        }
-    }
 };
 
-// acc += A B over sixteen k.
+// acc += A B over KS sixteens of k.
 // The tensor cores' accumulator drops the bits below its last place, always
-// toward zero, so a long sum kept in it drifts. The terms of a step are summed
+// toward zero, so a long sum kept in it drifts. The terms of sixteen k are summed
 // there from zero, the small parts first, and added to acc by an ordinary
 // rounded addition: the error of a chain of products over 64 terms falls from
 // 5e-7 to 2e-7 of its norm.
-// The parts of one tile depend on each other (20.6 cycles apart), so they go
-// part by part over all NT tiles.
-template <int TA, int TB, int NT>
-__device__ __forceinline__ void mma_step(float (&acc)[NT][4], const FragA<TA> &a,
-                                         const FragB<TB> (&b)[NT], int nt_end = NT) {
-    float t[NT][4];
+// Those terms depend on each other (20.6 cycles apart), so they go level by level
+// over all KS * NT tiles; a warp that has its SM quadrant to itself wants four.
+template <int TA, int TB, int NT, int KS>
+__device__ __forceinline__ void mma_step(float (&acc)[NT][4], const FragA<TA> (&a)[KS],
+                                         const FragB<TB> (&b)[KS][NT], int nt_end = NT) {
+    float t[KS][NT][4];
+    constexpr int SMALL = TA == 2 && TB == 2 ? 4 : TA == 2 || TB == 2 ? 2 : 0;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int l = 0; l < SMALL + 2; ++l) {
+        const int h = l < SMALL ? (l * 2) / (SMALL > 0 ? SMALL : 1) : l - SMALL;  // which eight
+        const bool alo = l < SMALL && TA == 2 && (TB == 1 || (l & 1));
+        const bool blo = l < SMALL && !alo;
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                if (n >= nt_end) continue;
+                const uint32_t(&x)[4] = alo ? a[s].lo[h] : a[s].hi[h];
+                const uint32_t *y = (blo ? b[s][n].lo : b[s][n].hi) + 2 * h;
+                if (l == 0)
+                    mma0(t[s][n], x, y[0], y[1]);
+                else
+                    mma(t[s][n], x, y[0], y[1]);
+            }
+    }
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             if (n >= nt_end) continue;
-            const uint32_t *bl = b[n].lo + 2 * h, *bh = b[n].hi + 2 * h;
-            if (TB == 2)
-                h ? mma(t[n], a.hi[h], bl[0], bl[1]) : mma0(t[n], a.hi[h], bl[0], bl[1]);
-            else if (TA == 2)
-                h ? mma(t[n], a.lo[h], bh[0], bh[1]) : mma0(t[n], a.lo[h], bh[0], bh[1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[n][i] += t[s][n][i];
         }
-        if (TA == 2 && TB == 2) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-                if (n < nt_end) mma(t[n], a.lo[h], b[n].hi[2 * h], b[n].hi[2 * h + 1]);
-        }
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            if (n >= nt_end) continue;
-            if (TA == 1 && TB == 1 && h == 0)
-                mma0(t[n], a.hi[h], b[n].hi[2 * h], b[n].hi[2 * h + 1]);
-            else
-                mma(t[n], a.hi[h], b[n].hi[2 * h], b[n].hi[2 * h + 1]);
-        }
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        if (n >= nt_end) continue;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[n][i] += t[n][i];
-    }
 }
 
 // The four k from `k` on (k = 16 step + 4t wide, + 2t narrow) of row or column
@@ -212,15 +197,15 @@ __device__ __forceinline__ void gemm(float (&acc)[NT][4], int s0, int s1, FA fa,
 #pragma unroll 1
     for (int st = s0; st < s1; ++st) {
         const int k = 16 * st + tk;
-        FragA<TA> a;
-        a.set(fa(g, k), fa(g + 8, k));
+        FragA<TA> a[1];
+        a[0].set(fa(g, k), fa(g + 8, k));
 #pragma unroll
         for (int n0 = 0; n0 < NT; n0 += G) {
-            FragB<TB> b[G];
+            FragB<TB> b[1][G];
 #pragma unroll
             for (int n = 0; n < G; ++n)
-                if (n0 + n < nt_end) b[n].set(fb(8 * (n0 + n) + g, k));
-            mma_step<TA, TB, G>(*reinterpret_cast<float(*)[G][4]>(&acc[n0]), a, b, nt_end - n0);
+                if (n0 + n < nt_end) b[0][n].set(fb(8 * (n0 + n) + g, k));
+            mma_step<TA, TB, G, 1>(*reinterpret_cast<float(*)[G][4]>(&acc[n0]), a, b, nt_end - n0);
         }
     }
 }
