@@ -962,8 +962,8 @@ int kata_delta_backward(const void *q, const void *k, const void *v, int dtype, 
 static int check_prefill_backward(int dtype, int B, int H, int T, int d) {
     int st = check_common(dtype, B, H, d);
     if (st) return st;
-    // one CTA per 64 rows and head
-    if (T <= 0 || T > (1 << 24) || (long)B * H * (((long)T + 63) / 64) > 0x7FFFFFFFL)
+    // one CTA per 32 rows and head at least
+    if (T <= 0 || T > (1 << 24) || (long)B * H * (((long)T + 31) / 32) > 0x7FFFFFFFL)
         return fail(KATA_ERR_INVALID_ARG, "T=%d must be positive, and B*H*T smaller", T);
     return KATA_OK;
 }

@@ -48,7 +48,7 @@ static_assert(kStages == 2 * kBufs && kStages % kSets == 0, "slots of a step");
 constexpr int kThreads = 32 * (kWorkerWarps + 4);
 
 struct BwdParams {
-    int T, tiles, steps;  // tokens; 128-row tiles and 64-row steps per head
+    int T, heads, tiles, steps;  // tokens; 128-row tiles and 64-row steps per head
     long pitch;           // rows per head of the statistics: 128 * tiles
     float eps;
     float *inv, *dhi, *dlo;  // [heads][pitch]: 1 / den, -delta as two floats
@@ -144,9 +144,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::BAR);
     uint32_t *slot = reinterpret_cast<uint32_t *>(sm + L::SLOT);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int head = blockIdx.x;
+    const int head = blockIdx.x % p.heads;
     // the longest walks launch first: the last queries, the first keys
-    const int tile = KEYS ? (int)blockIdx.y : p.tiles - 1 - (int)blockIdx.y;
+    const int at = blockIdx.x / p.heads, tile = KEYS ? at : p.tiles - 1 - at;
     const ErrCtx err{p.err};
     // steps of one walk: keys up to the diagonal, or queries from it on
     const int first = KEYS ? 2 * tile : 0;
@@ -485,6 +485,7 @@ cudaError_t launch(const PrefillBackwardArgs &a, cudaStream_t stream) {
         return cudaErrorInvalidValue;
     BwdParams p;
     p.T = a.T;
+    p.heads = (int)a.heads;
     p.tiles = (a.T + 127) / 128;
     p.steps = (a.T + kStep - 1) / kStep;
     p.pitch = 128L * p.tiles;
@@ -493,7 +494,7 @@ cudaError_t launch(const PrefillBackwardArgs &a, cudaStream_t stream) {
     p.dhi = p.inv + a.heads * p.pitch;
     p.dlo = p.dhi + a.heads * p.pitch;
     p.err = a.err;
-    const dim3 grid((unsigned)a.heads, (unsigned)p.tiles);
+    const unsigned grid = (unsigned)(a.heads * p.tiles);
     cudaError_t e;
     using Q = BwdCfg<DH, false>;
     using K = BwdCfg<DH, true>;
@@ -512,7 +513,7 @@ cudaError_t launch(const PrefillBackwardArgs &a, cudaStream_t stream) {
 }  // namespace
 
 bool prefill_backward_tc_applies(int dtype, int T, int d) {
-    return dtype == 1 && (d == 32 || d == 64) && (T + 127) / 128 <= 65535;
+    return dtype == 1 && (d == 32 || d == 64);
 }
 
 size_t prefill_backward_tc_workspace_bytes(long heads, int T) {
