@@ -24,12 +24,22 @@
 // thread needs longer for a step's waits and MMAs than the tensor pipe), one of the
 // output products, a TMA producer. Every wait is bounded.
 //
-// Rounding: scores, dP, den and delta are fp32 or wider; P and dS are rounded
-// to bf16 as operands (2^-9 of each term), the same size as the rounding of the
-// results. The rows of the first 128 queries sum den and delta in 64 bits, and
-// delta is two floats: with few keys dP - delta is a small difference. It
-// stays exact because S and dP come out of the same products with the same
-// bits in both modes and both walks.
+// Rounding: scores, dP, den and delta are fp32 or wider. P is rounded to bf16 as
+// an operand (its terms add up without cancelling: dV's error is 1.4 times its own
+// last rounding). dS is a difference whose terms do cancel in dQ and dK, so it goes
+// in as two bf16 parts (16 bits): with one, dQ and dK were off by up to 3.1e-3 of
+// their norm, with two by 1.7e-3, the last rounding alone (12 % more time). The
+// rows of the first 128 queries sum den and delta in 64 bits, and delta is two
+// floats: with few keys dP - delta is a small difference. It stays exact because
+// S and dP come out of the same products with the same bits in both modes and
+// both walks.
+//
+// Measured on B200 at B2 H8 T8192 d64 (344 GFLOP as five products per causal
+// pair; nine and a half are run): queries 482 us, keys 415 us, 383 TFLOP/s of the
+// five. What bounds it: the keys' workers, which read two statistics per column
+// from shared memory (1700 of the 4000 cycles that a buffer is in use), and for the
+// queries the single threads that issue the products (66 cycles per MMA against 48
+// for the operands' shared-memory reads).
 #include "kata_internal.h"
 #include "tc_tiles.cuh"
 
@@ -85,6 +95,9 @@ struct BwdCfg {
     // over half an SM's shared memory: a second CTA could not have tensor memory
     static constexpr int BYTES = NEED > 118 * 1024 ? NEED : 118 * 1024;
     static constexpr uint32_t ACC = 128 * kBufs;             // first accumulator column
+    // columns of a group's parts in its half of a buffer: dS's upper part at 64 ..
+    // 79, P (keys) at 0 .. 15, dS's lower part where neither is
+    static constexpr uint32_t DS_LO = KEYS ? 64 + 16 : 0;
     static_assert(ACC + 2 * DH <= 512, "tensor-memory budget");
     static_assert(SLOT % 8 == 0 && BAR % 8 == 0, "barriers");
     static constexpr int S_WARP = kWorkerWarps, O_WARP = S_WARP + kSets, TMA_WARP = O_WARP + 1;
@@ -260,8 +273,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // 16 rows on; a group's columns lie in its own half
                 auto a = [&](int kk) { return buf + 8 * kk + (kk < 2 ? 0 : 16); };
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mma_ts(tmem + L::ACC, a(kk) + 64, t0 + kk * L::ROW, id, s > n1 || kk > 0);
+                for (int kk = 0; kk < 4; ++kk) {
+                    mma_ts(tmem + L::ACC, a(kk) + L::DS_LO, t0 + kk * L::ROW, id, s > n1 || kk > 0);
+                    mma_ts(tmem + L::ACC, a(kk) + 64, t0 + kk * L::ROW, id, 1);
+                }
                 if (KEYS) {
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
@@ -382,6 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float *stats = reinterpret_cast<const float *>(sm + L::STREAM + st * L::STAGE + L::STATS);
             const bool few = KEYS ? step < 2 : tile == 0;  // rows that may see few keys
             uint32_t sv[2][16], dv[2][16];
+            uint32_t low[KEYS ? 2 : 1][8];
             load(b, half, sv[0], dv[0]);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
@@ -391,6 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (c == 0) load(b, half + 16, sv[1], dv[1]);
                 if (on_diagonal(step)) mask(step * kStep + half + 16 * c, x);
                 uint32_t pk[8], dk[8];
+                uint32_t(&dl_)[8] = low[KEYS ? c : 0];
 #pragma unroll
                 for (int e = 0; e < 16; e += 4) {
                     float4 iv = make_float4(inv, inv, inv, inv), dh = make_float4(dhi, dhi, dhi, dhi);
@@ -409,7 +426,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                                    h ? f2(dh.z, dh.w) : f2(dh.x, dh.y));
                         if (few) t = add(t, h ? f2(dl.z, dl.w) : f2(dl.x, dl.y));
                         const float2 ds = un(mul(w, t));
-                        dk[e / 2 + h] = pack_bf16x2(ds.x, ds.y);
+                        const uint32_t up = pack_bf16x2(ds.x, ds.y);
+                        dk[e / 2 + h] = up;
+                        dl_[e / 2 + h] = pack_bf16x2(ds.x - __uint_as_float(up << 16),
+                                                     ds.y - __uint_as_float(up & 0xFFFF0000u));
                         if (KEYS) {
                             const float2 pp = un(mul(v, w));
                             pk[e / 2 + h] = pack_bf16x2(pp.x, pp.y);
@@ -419,6 +439,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // over columns of this group's half that have been read by now
                 if (KEYS) tmem_st8(lanes + 128 * b + half + 8 * c, pk);
                 tmem_st8(lanes + 128 * b + 64 + half + 8 * c, dk);
+                if (!KEYS) {
+                    tmem_st8(lanes + 128 * b + L::DS_LO + half + 8 * c, low[0]);
+                } else if (c == 1) {  // over the second sixteen columns of dP
+                    tmem_st8(lanes + 128 * b + L::DS_LO + half, low[0]);
+                    tmem_st8(lanes + 128 * b + L::DS_LO + half + 8, low[KEYS ? 1 : 0]);
+                }
             }
             tmem_st_wait();
             tc_fence_before();
