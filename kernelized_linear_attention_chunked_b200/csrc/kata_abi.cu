@@ -970,7 +970,7 @@ static int check_prefill_backward(int dtype, int B, int H, int T, int d) {
 
 size_t kata_prefill_backward_workspace_bytes(int B, int H, int T, int d, int dtype) {
     if (check_prefill_backward(dtype, B, H, T, d)) return 0;
-    return kata::prefill_backward_workspace_bytes(dtype, (long)B * H, T, d);
+    return kata::prefill_backward_workspace_bytes(dtype, (long)B * H, T);
 }
 
 int kata_prefill_backward(const void *q, const void *k, const void *v, int dtype, int B, int H,
@@ -987,7 +987,7 @@ int kata_prefill_backward(const void *q, const void *k, const void *v, int dtype
     KATA_REQUIRE_PTR(dq);
     KATA_REQUIRE_PTR(dk);
     KATA_REQUIRE_PTR(dv);
-    const size_t need = kata::prefill_backward_workspace_bytes(dtype, (long)B * H, T, d);
+    const size_t need = kata::prefill_backward_workspace_bytes(dtype, (long)B * H, T);
     if (ws_bytes < need || !workspace)
         return fail(KATA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, need);
     KATA_REQUIRE_PTR(workspace);

@@ -132,11 +132,10 @@ struct PrefillBackwardArgs {
     void *dq, *dk, *dv, *ws;
     unsigned int *err;
 };
-// tcgen05 form (prefill_backward_tc.cu): bf16, d = 32 or 64.
-bool prefill_backward_tc_applies(int dtype, int T, int d);
+// bf16: tcgen05 (prefill_backward_tc.cu)
 size_t prefill_backward_tc_workspace_bytes(long heads, int T);
 cudaError_t prefill_backward_tc(const PrefillBackwardArgs &a, cudaStream_t stream);
-size_t prefill_backward_workspace_bytes(int dtype, long heads, int T, int d);
+size_t prefill_backward_workspace_bytes(int dtype, long heads, int T);
 cudaError_t prefill_backward(const PrefillBackwardArgs &a, cudaStream_t stream);
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }

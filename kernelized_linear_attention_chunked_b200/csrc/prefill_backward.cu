@@ -11,8 +11,8 @@
 // quadratic in T. Each sum is owned by one CTA: no atomics, the same bits on
 // every run.
 //
-// This file: fp32 inputs, and bf16 inputs with d = 16, in split-tf32 products
-// (mma_tf32.cuh), which keep fp32 accuracy. Two launches: bwd_query (one CTA
+// This file: fp32 inputs, in split-tf32 products (mma_tf32.cuh), which keep fp32
+// accuracy; bf16 inputs are prefill_backward_tc.cu's. Two launches: bwd_query (one CTA
 // per ROWS queries: den and delta over the keys, then dQ) and bwd_key (one CTA
 // per ROWS keys: dK, dV). bwd_query leaves den and delta of every row for
 // bwd_key. ROWS is 64, or 32 where 64 would leave SMs idle.
@@ -47,12 +47,12 @@ struct Args {
 
 // Four warps per 16 rows, each 16 columns of a ROWS x 64 product and ND 8-column
 // tiles of a ROWS x D one.
-template <typename Tin, int D, int ROWS>
+template <int D, int ROWS>
 struct BwdCfg {
     static constexpr int THREADS = ROWS / 16 * 128;
     static constexpr int ND = D >= 32 ? D / 32 : 1;
     static constexpr int RS = D + 8;
-    static constexpr int OWN = ROWS * RS * (int)sizeof(Tin), IN = kB * RS * (int)sizeof(Tin);
+    static constexpr int OWN = ROWS * RS * 4, IN = kB * RS * 4;
     static constexpr int A0 = 0, A1 = OWN;     // the CTA's own rows: q, dO or k, v
     static constexpr int B0 = 2 * OWN;         // two stages of the other side's two tiles
     static constexpr int DS = B0 + 4 * IN;     // ROWS x 64 products
@@ -64,8 +64,8 @@ struct BwdCfg {
 
 // s and dP in 64 bits for two rows (0, 8 on) of q, o against four columns (0, 1,
 // 8, 9 on) of k, v, in the layout of two accumulator tiles.
-template <typename Tin, int D>
-__device__ __forceinline__ void dots64(const Tin *q, const Tin *o, const Tin *k, const Tin *v,
+template <int D>
+__device__ __forceinline__ void dots64(const float *q, const float *o, const float *k, const float *v,
                                        double (&s)[2][4], double (&dp)[2][4]) {
     constexpr int RS = D + 8;
 #pragma unroll
@@ -77,14 +77,14 @@ __device__ __forceinline__ void dots64(const Tin *q, const Tin *o, const Tin *k,
         double a[2], b[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            a[h] = to_f32(q[8 * h * RS + c]);
-            b[h] = to_f32(o[8 * h * RS + c]);
+            a[h] = q[8 * h * RS + c];
+            b[h] = o[8 * h * RS + c];
         }
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const double x = to_f32(k[(8 * n + e) * RS + c]), y = to_f32(v[(8 * n + e) * RS + c]);
+                const double x = k[(8 * n + e) * RS + c], y = v[(8 * n + e) * RS + c];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     s[n][2 * h + e] = fma(a[h], x, s[n][2 * h + e]);
@@ -94,38 +94,30 @@ __device__ __forceinline__ void dots64(const Tin *q, const Tin *o, const Tin *k,
     }
 }
 
-template <typename Tin>
-__device__ __forceinline__ void store2(Tin *d, float x, float y) {
-    if constexpr (sizeof(Tin) == 2)
-        *reinterpret_cast<__nv_bfloat162 *>(d) = __floats2bfloat162_rn(x, y);
-    else
-        *reinterpret_cast<float2 *>(d) = make_float2(x, y);
-}
-
 // Columns d0 .. of rows m0 .. of a tile that starts at row t0 of a [T, D] matrix
-template <typename Tin, int D, int N>
+template <int D, int N>
 __device__ __forceinline__ void store_rows(void *dst, size_t row0, int t0, int T,
                                            const float (&acc)[N][4], int m0, int d0, int gr, int t2) {
-    Tin *o = static_cast<Tin *>(dst);
+    float *o = static_cast<float *>(dst);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int t = t0 + m0 + gr + 8 * h;
         if (t >= T) continue;
 #pragma unroll
         for (int nt = 0; nt < N; ++nt)
-            store2(o + (row0 + t) * (size_t)D + d0 + 8 * nt + t2, acc[nt][2 * h],
-                   acc[nt][2 * h + 1]);
+            *reinterpret_cast<float2 *>(o + (row0 + t) * (size_t)D + d0 + 8 * nt + t2) =
+                make_float2(acc[nt][2 * h], acc[nt][2 * h + 1]);
     }
 }
 
 // One CTA per (head, ROWS queries). Two walks over the key tiles up to the
 // diagonal: den and delta, then dQ.
-template <typename Tin, int D, int ROWS>
-__global__ void __launch_bounds__(BwdCfg<Tin, D, ROWS>::THREADS) bwd_query(Args p) {
-    using L = BwdCfg<Tin, D, ROWS>;
-    constexpr int RS = L::RS, TI = Parts<Tin>::N, ND = L::ND, TH = L::THREADS;
+template <int D, int ROWS>
+__global__ void __launch_bounds__(BwdCfg<D, ROWS>::THREADS) bwd_query(Args p) {
+    using L = BwdCfg<D, ROWS>;
+    constexpr int RS = L::RS, ND = L::ND, TH = L::THREADS;
     extern __shared__ __align__(16) uint8_t sm[];
-    Tin *sQ = reinterpret_cast<Tin *>(sm + L::A0), *sO = reinterpret_cast<Tin *>(sm + L::A1);
+    float *sQ = reinterpret_cast<float *>(sm + L::A0), *sO = reinterpret_cast<float *>(sm + L::A1);
     float *sDS = reinterpret_cast<float *>(sm + L::DS);
     double *red = reinterpret_cast<double *>(sm + L::RED);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -137,16 +129,16 @@ __global__ void __launch_bounds__(BwdCfg<Tin, D, ROWS>::THREADS) bwd_query(Args 
     const int walk = (min(q0 + ROWS, p.T) + kB - 1) / kB;  // key tiles with a key that a query sees
     const bool few = q0 == 0 && m0 == 0;  // this warp's rows are the first sixteen queries
 
-    auto tileK = [&](int u) { return reinterpret_cast<Tin *>(sm + L::B0 + (u & 1) * 2 * L::IN); };
+    auto tileK = [&](int u) { return reinterpret_cast<float *>(sm + L::B0 + (u & 1) * 2 * L::IN); };
     auto tileV = [&](int u) { return tileK(u) + kB * RS; };
     auto prefetch = [&](int u) {
         const int t = (u < walk ? u : u - walk) * kB;
-        load_tile<Tin, D, TH>(tileK(u), RS, static_cast<const Tin *>(p.k), row0, t, p.T, D, 0, tid);
-        load_tile<Tin, D, TH>(tileV(u), RS, static_cast<const Tin *>(p.v), row0, t, p.T, D, 0, tid);
+        load_tile<float, D, TH>(tileK(u), RS, static_cast<const float *>(p.k), row0, t, p.T, D, 0, tid);
+        load_tile<float, D, TH>(tileV(u), RS, static_cast<const float *>(p.v), row0, t, p.T, D, 0, tid);
         cp_commit();
     };
-    load_tile<Tin, D, TH, ROWS>(sQ, RS, static_cast<const Tin *>(p.q), row0, q0, p.T, D, 0, tid);
-    load_tile<Tin, D, TH, ROWS>(sO, RS, static_cast<const Tin *>(p.d_o), row0, q0, p.T, D, 0, tid);
+    load_tile<float, D, TH, ROWS>(sQ, RS, static_cast<const float *>(p.q), row0, q0, p.T, D, 0, tid);
+    load_tile<float, D, TH, ROWS>(sO, RS, static_cast<const float *>(p.d_o), row0, q0, p.T, D, 0, tid);
     prefetch(0);
     cp_wait_all();
     __syncthreads();
@@ -159,7 +151,7 @@ __global__ void __launch_bounds__(BwdCfg<Tin, D, ROWS>::THREADS) bwd_query(Args 
         if (u + 1 < 2 * walk) prefetch(u + 1);
         const bool second = u >= walk;
         const int k0 = (second ? u - walk : u) * kB;
-        const Tin *k = tileK(u), *v = tileV(u);
+        const float *k = tileK(u), *v = tileV(u);
         if (u == walk) {  // the rows' sums are complete: join the lanes, then the column quarters
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -194,7 +186,7 @@ __global__ void __launch_bounds__(BwdCfg<Tin, D, ROWS>::THREADS) bwd_query(Args 
         float s[2][4], dp[2][4];
         if (few && k0 == 0 && n0 == 0) {
             double s64[2][4], dp64[2][4];
-            dots64<Tin, D>(sQ + gr * RS, sO + gr * RS, k + t2 * RS, v + t2 * RS, s64, dp64);
+            dots64<D>(sQ + gr * RS, sO + gr * RS, k + t2 * RS, v + t2 * RS, s64, dp64);
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
@@ -214,10 +206,10 @@ __global__ void __launch_bounds__(BwdCfg<Tin, D, ROWS>::THREADS) bwd_query(Args 
         } else {
             clear(s);
             clear(dp);
-            gemm<TI, TI, 2, true>(
+            gemm<2, 2, 2, true>(
                 s, 0, D / 16, [&](int m, int kk) { return quad<true, true>(sQ + m0 * RS, RS, m, kk); },
                 [&](int n, int kk) { return quad<true, true>(k + n0 * RS, RS, n, kk); });
-            gemm<TI, TI, 2, true>(
+            gemm<2, 2, 2, true>(
                 dp, 0, D / 16, [&](int m, int kk) { return quad<true, true>(sO + m0 * RS, RS, m, kk); },
                 [&](int n, int kk) { return quad<true, true>(v + n0 * RS, RS, n, kk); });
             float ds[2] = {0.f, 0.f}, ns[2] = {0.f, 0.f};
@@ -253,7 +245,7 @@ __global__ void __launch_bounds__(BwdCfg<Tin, D, ROWS>::THREADS) bwd_query(Args 
                         make_float2(s[nt][2 * h], s[nt][2 * h + 1]);
             __syncthreads();
             if (d0 < D)
-                gemm<2, TI, ND, false>(
+                gemm<2, 2, ND, false>(
                     dq, 0, kB / 16,
                     [&](int m, int kk) { return quad<true, false>(sDS + m0 * kTS, kTS, m, kk); },
                     [&](int n, int kk) { return quad<false, false>(k + d0, RS, n, kk); });
@@ -261,17 +253,17 @@ __global__ void __launch_bounds__(BwdCfg<Tin, D, ROWS>::THREADS) bwd_query(Args 
         cp_wait_all();
         __syncthreads();
     }
-    if (d0 < D) store_rows<Tin, D>(p.dq, row0, q0, p.T, dq, m0, d0, gr, t2);
+    if (d0 < D) store_rows<D>(p.dq, row0, q0, p.T, dq, m0, d0, gr, t2);
 }
 
 // One CTA per (head, ROWS keys): the query steps from the diagonal on. Rows of
 // its ROWS x 64 tiles are keys: s^T = K Q^T, dP^T = V dO^T.
-template <typename Tin, int D, int ROWS>
-__global__ void __launch_bounds__(BwdCfg<Tin, D, ROWS>::THREADS) bwd_key(Args p) {
-    using L = BwdCfg<Tin, D, ROWS>;
-    constexpr int RS = L::RS, TI = Parts<Tin>::N, ND = L::ND, TH = L::THREADS;
+template <int D, int ROWS>
+__global__ void __launch_bounds__(BwdCfg<D, ROWS>::THREADS) bwd_key(Args p) {
+    using L = BwdCfg<D, ROWS>;
+    constexpr int RS = L::RS, ND = L::ND, TH = L::THREADS;
     extern __shared__ __align__(16) uint8_t sm[];
-    Tin *sK = reinterpret_cast<Tin *>(sm + L::A0), *sV = reinterpret_cast<Tin *>(sm + L::A1);
+    float *sK = reinterpret_cast<float *>(sm + L::A0), *sV = reinterpret_cast<float *>(sm + L::A1);
     float *sDS = reinterpret_cast<float *>(sm + L::DS), *sP = reinterpret_cast<float *>(sm + L::P);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int gr = lane >> 2, t2 = 2 * (lane & 3);
@@ -280,12 +272,12 @@ __global__ void __launch_bounds__(BwdCfg<Tin, D, ROWS>::THREADS) bwd_key(Args p)
     const int k0 = (int)(blockIdx.x % p.tiles) * ROWS;  // the keys that most queries see first
     const size_t row0 = head * (size_t)p.T;
 
-    auto tileQ = [&](int u) { return reinterpret_cast<Tin *>(sm + L::B0 + (u & 1) * 2 * L::IN); };
+    auto tileQ = [&](int u) { return reinterpret_cast<float *>(sm + L::B0 + (u & 1) * 2 * L::IN); };
     auto tileO = [&](int u) { return tileQ(u) + kB * RS; };
     auto stats = [&](int u) { return reinterpret_cast<float4 *>(sm + L::STAT) + (u & 1) * kB; };
     auto prefetch = [&](int u) {
-        load_tile<Tin, D, TH>(tileQ(u), RS, static_cast<const Tin *>(p.q), row0, u * kB, p.T, D, 0, tid);
-        load_tile<Tin, D, TH>(tileO(u), RS, static_cast<const Tin *>(p.d_o), row0, u * kB, p.T, D, 0,
+        load_tile<float, D, TH>(tileQ(u), RS, static_cast<const float *>(p.q), row0, u * kB, p.T, D, 0, tid);
+        load_tile<float, D, TH>(tileO(u), RS, static_cast<const float *>(p.d_o), row0, u * kB, p.T, D, 0,
                               tid);
         if (tid < kB) {
             const bool have = u * kB + tid < p.T;
@@ -293,8 +285,8 @@ __global__ void __launch_bounds__(BwdCfg<Tin, D, ROWS>::THREADS) bwd_key(Args p)
         }
         cp_commit();
     };
-    load_tile<Tin, D, TH, ROWS>(sK, RS, static_cast<const Tin *>(p.k), row0, k0, p.T, D, 0, tid);
-    load_tile<Tin, D, TH, ROWS>(sV, RS, static_cast<const Tin *>(p.v), row0, k0, p.T, D, 0, tid);
+    load_tile<float, D, TH, ROWS>(sK, RS, static_cast<const float *>(p.k), row0, k0, p.T, D, 0, tid);
+    load_tile<float, D, TH, ROWS>(sV, RS, static_cast<const float *>(p.v), row0, k0, p.T, D, 0, tid);
     const int first = k0 / kB;
     prefetch(first);
     cp_wait_all();
@@ -305,15 +297,15 @@ __global__ void __launch_bounds__(BwdCfg<Tin, D, ROWS>::THREADS) bwd_key(Args p)
     clear(dv);
     for (int u = first; u < p.steps; ++u) {
         if (u + 1 < p.steps) prefetch(u + 1);
-        const Tin *q = tileQ(u), *o = tileO(u);
+        const float *q = tileQ(u), *o = tileO(u);
         const float4 *st = stats(u);
         float s[2][4], dp[2][4];
         clear(s);
         clear(dp);
-        gemm<TI, TI, 2, true>(
+        gemm<2, 2, 2, true>(
             s, 0, D / 16, [&](int m, int kk) { return quad<true, true>(sK + m0 * RS, RS, m, kk); },
             [&](int n, int kk) { return quad<true, true>(q + n0 * RS, RS, n, kk); });
-        gemm<TI, TI, 2, true>(
+        gemm<2, 2, 2, true>(
             dp, 0, D / 16, [&](int m, int kk) { return quad<true, true>(sV + m0 * RS, RS, m, kk); },
             [&](int n, int kk) { return quad<true, true>(o + n0 * RS, RS, n, kk); });
 #pragma unroll
@@ -329,7 +321,7 @@ __global__ void __launch_bounds__(BwdCfg<Tin, D, ROWS>::THREADS) bwd_key(Args p)
             }
         if (u == 0 && n0 == 0 && k0 + m0 == 0) {  // the first sixteen queries (and keys) in 64 bits
             double s64[2][4], dp64[2][4];
-            dots64<Tin, D>(sK + gr * RS, sV + gr * RS, q + t2 * RS, o + t2 * RS, s64, dp64);
+            dots64<D>(sK + gr * RS, sV + gr * RS, q + t2 * RS, o + t2 * RS, s64, dp64);
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
@@ -352,11 +344,11 @@ __global__ void __launch_bounds__(BwdCfg<Tin, D, ROWS>::THREADS) bwd_key(Args p)
             }
         __syncthreads();
         if (d0 < D) {
-            gemm<2, TI, ND, false>(
+            gemm<2, 2, ND, false>(
                 dk, 0, kB / 16,
                 [&](int m, int kk) { return quad<true, false>(sDS + m0 * kTS, kTS, m, kk); },
                 [&](int n, int kk) { return quad<false, false>(q + d0, RS, n, kk); });
-            gemm<2, TI, ND, false>(
+            gemm<2, 2, ND, false>(
                 dv, 0, kB / 16,
                 [&](int m, int kk) { return quad<true, false>(sP + m0 * kTS, kTS, m, kk); },
                 [&](int n, int kk) { return quad<false, false>(o + d0, RS, n, kk); });
@@ -365,56 +357,50 @@ __global__ void __launch_bounds__(BwdCfg<Tin, D, ROWS>::THREADS) bwd_key(Args p)
         __syncthreads();
     }
     if (d0 < D) {
-        store_rows<Tin, D>(p.dk, row0, k0, p.T, dk, m0, d0, gr, t2);
-        store_rows<Tin, D>(p.dv, row0, k0, p.T, dv, m0, d0, gr, t2);
+        store_rows<D>(p.dk, row0, k0, p.T, dk, m0, d0, gr, t2);
+        store_rows<D>(p.dv, row0, k0, p.T, dv, m0, d0, gr, t2);
     }
 }
 
-template <typename Tin, int D, int ROWS>
+template <int D, int ROWS>
 cudaError_t run(Args p, long heads, cudaStream_t stream) {
-    using L = BwdCfg<Tin, D, ROWS>;
+    using L = BwdCfg<D, ROWS>;
     static_assert(L::BYTES <= 227 * 1024, "shared memory of one CTA");
     p.tiles = (p.T + ROWS - 1) / ROWS;
     cudaError_t e;
-    if ((e = delta::raise_smem<bwd_query<Tin, D, ROWS>>(L::BYTES)) != cudaSuccess) return e;
-    if ((e = delta::raise_smem<bwd_key<Tin, D, ROWS>>(L::BYTES)) != cudaSuccess) return e;
+    if ((e = delta::raise_smem<bwd_query<D, ROWS>>(L::BYTES)) != cudaSuccess) return e;
+    if ((e = delta::raise_smem<bwd_key<D, ROWS>>(L::BYTES)) != cudaSuccess) return e;
     const unsigned grid = (unsigned)(heads * p.tiles);
-    bwd_query<Tin, D, ROWS><<<grid, L::THREADS, L::BYTES, stream>>>(p);
+    bwd_query<D, ROWS><<<grid, L::THREADS, L::BYTES, stream>>>(p);
     if ((e = after_launch()) != cudaSuccess) return e;
-    bwd_key<Tin, D, ROWS><<<grid, L::THREADS, L::BYTES, stream>>>(p);
+    bwd_key<D, ROWS><<<grid, L::THREADS, L::BYTES, stream>>>(p);
     return after_launch();
 }
 
 // 32 rows per CTA where 64 would not give every SM two
-template <typename Tin, int D>
+template <int D>
 cudaError_t run_rows(const Args &p, long heads, cudaStream_t stream) {
     const bool small = heads * ((p.T + 63) / 64) < 2 * 148;
-    return small ? run<Tin, D, 32>(p, heads, stream) : run<Tin, D, 64>(p, heads, stream);
-}
-
-template <typename Tin>
-cudaError_t run_d(const Args &p, long heads, int d, cudaStream_t stream) {
-    switch (d) {
-        case 16: return run_rows<Tin, 16>(p, heads, stream);
-        case 32: return run_rows<Tin, 32>(p, heads, stream);
-        case 64: return run_rows<Tin, 64>(p, heads, stream);
-        default: return cudaErrorInvalidValue;
-    }
+    return small ? run<D, 32>(p, heads, stream) : run<D, 64>(p, heads, stream);
 }
 
 }  // namespace
 
-size_t prefill_backward_workspace_bytes(int dtype, long heads, int T, int d) {
-    return prefill_backward_tc_applies(dtype, T, d) ? prefill_backward_tc_workspace_bytes(heads, T)
-                                                    : (size_t)heads * T * sizeof(float4);
+size_t prefill_backward_workspace_bytes(int dtype, long heads, int T) {
+    return dtype == 1 ? prefill_backward_tc_workspace_bytes(heads, T)
+                      : (size_t)heads * T * sizeof(float4);
 }
 
 cudaError_t prefill_backward(const PrefillBackwardArgs &a, cudaStream_t stream) {
-    if (prefill_backward_tc_applies(a.dtype, a.T, a.d)) return prefill_backward_tc(a, stream);
-    Args p{a.q, a.k, a.v, a.d_o, a.dq, a.dk, a.dv, static_cast<float4 *>(a.ws), a.T, 0,
-           (a.T + kB - 1) / kB, a.eps};
-    if (a.dtype == 0) return run_d<float>(p, a.heads, a.d, stream);
-    return a.d == 16 ? run_rows<__nv_bfloat16, 16>(p, a.heads, stream) : cudaErrorInvalidValue;
+    if (a.dtype == 1) return prefill_backward_tc(a, stream);
+    const Args p{a.q, a.k, a.v, a.d_o, a.dq, a.dk, a.dv, static_cast<float4 *>(a.ws), a.T, 0,
+                 (a.T + kB - 1) / kB, a.eps};
+    switch (a.d) {
+        case 16: return run_rows<16>(p, a.heads, stream);
+        case 32: return run_rows<32>(p, a.heads, stream);
+        case 64: return run_rows<64>(p, a.heads, stream);
+        default: return cudaErrorInvalidValue;
+    }
 }
 
 }  // namespace kata

@@ -1,5 +1,5 @@
 // Gradients of the causal kernelized prefill on the tcgen05 tensor cores, for
-// bf16 inputs with d = 32 or 64 and any T. The formulas are in
+// bf16 inputs and any T. The formulas are in
 // prefill_backward.cu; this file is about how the products are fed.
 //
 // One kernel in two modes, two launches:
@@ -57,6 +57,8 @@ constexpr int kWorkerWarps = 4 * kGroups;
 static_assert(kStages == 2 * kBufs && kStages % kSets == 0, "slots of a step");
 constexpr int kThreads = 32 * (kWorkerWarps + 4);
 
+constexpr uint32_t kSwizzle32 = 6;  // rows of 32 bytes, 16-byte chunks swapped every four rows
+
 struct BwdParams {
     int T, heads, tiles, steps;  // tokens; 128-row tiles and 64-row steps per head
     long pitch;           // rows per head of the statistics: 128 * tiles
@@ -82,7 +84,7 @@ enum BwdBar {
 template <int DH, bool KEYS>
 struct BwdCfg {
     static constexpr int ROW = 2 * DH;                       // bytes per row, one swizzle atom
-    static constexpr uint32_t SW = DH == 64 ? kSwizzle128 : kSwizzle64;
+    static constexpr uint32_t SW = DH == 64 ? kSwizzle128 : DH == 32 ? kSwizzle64 : kSwizzle32;
     static constexpr int OWN = 128 * ROW;                    // one own tile
     static constexpr int TILE = kStep * ROW;                 // one streamed tile
     static constexpr int STATS = 2 * TILE;                   // keys: inv, dhi, dlo of a step
@@ -454,11 +456,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(&bar[kOver + st]);
             }
         }
-        // half of the columns each: set 0 those of dQ or dK, set 1 (keys) those of dV
-        if (ok) ok = (KEYS || set == 0) && warp_wait(&bar[kOutDone], 0, err, 0x833);
+        // half of the columns each (sixteen at least): set 0 those of dQ or dK, set 1
+        // (keys) those of dV
+        constexpr int COLS = DH >= 32 ? DH / 2 : DH;
+        if (ok)
+            ok = (KEYS || set == 0) && (DH >= 32 || (group & 1) == 0) &&
+                 warp_wait(&bar[kOutDone], 0, err, 0x833);
         tc_fence_after();
-        constexpr int COLS = DH / 2;
-        const uint32_t col0 = L::ACC + group * COLS;
+        const uint32_t col0 = L::ACC + set * DH + (group & 1) * COLS;
         const float scale = set == 0 ? 2.f : 1.f;
         __nv_bfloat16 *out = set == 0 ? p.out0 : p.out1;
         uint4 *dst = reinterpret_cast<uint4 *>(out + ((size_t)head * p.T + row) * DH +
@@ -499,7 +504,9 @@ bool map_rows(CUtensorMap *m, const void *base, int d, int T, long heads) {
     cuuint32_t es[3] = {1, 1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
                es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               d == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               d == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
+               : d == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
+                         : CU_TENSOR_MAP_SWIZZLE_32B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -538,16 +545,17 @@ cudaError_t launch(const PrefillBackwardArgs &a, cudaStream_t stream) {
 
 }  // namespace
 
-bool prefill_backward_tc_applies(int dtype, int T, int d) {
-    return dtype == 1 && (d == 32 || d == 64);
-}
-
 size_t prefill_backward_tc_workspace_bytes(long heads, int T) {
     return (size_t)heads * ((T + 127) / 128) * 128 * 3 * sizeof(float);
 }
 
 cudaError_t prefill_backward_tc(const PrefillBackwardArgs &a, cudaStream_t stream) {
-    return a.d == 64 ? launch<64>(a, stream) : launch<32>(a, stream);
+    switch (a.d) {
+        case 16: return launch<16>(a, stream);
+        case 32: return launch<32>(a, stream);
+        case 64: return launch<64>(a, stream);
+        default: return cudaErrorInvalidValue;
+    }
 }
 
 }  // namespace kata
