@@ -10,9 +10,10 @@
 //     dK = R + L,  R = PN K - diag(a) Z S0^T              (k_i as the reader)
 //                  L = PM^T Q + PN^T K + diag(c) U dS^T   (k_j as the written key)
 // and for the running sums G of the log decays, since each term carries
-// exp(G_i - G_j) with i the reading and j the written token,
-//     dG_i = q_i . dQ_i + k_i . R_i - k_i . L_i,
-//     dg_t = sum_{i >= t in the chunk} dG_i + (a_C <S0, dS> + sum_j k_j . (c_j U_j dS^T)).
+// exp(G_i - G_j) with i the reading and j the written token, with
+// x_ij = PM_ij (q_i.k_j) + PN_ij (k_i.k_j) and w_j = k_j . (c_j U_j dS^T),
+//     dG_i = sum_j x_ij - sum_j x_ji + scale a_i q_i.(S0 dO_i) - a_i k_i.(S0 Z_i) - w_i,
+//     dg_t = sum_{i >= t in the chunk} dG_i + (a_C <S0, dS> + sum_j w_j).
 //
 // Four launches: delta_prep (the operands of both walks), the two walks (the
 // states and errors forwards, their gradients backwards; neither needs the
@@ -23,8 +24,9 @@
 // CTA's shared memory, and sums the products over the columns in registers.
 // 8 warps: row block warp % 4, and one half of the columns (of a 64 x 64
 // product: every other 8 columns, so that the two halves of a triangular one
-// have equal work). All products are split tf32 (mma_tf32.cuh): dg is a
-// difference of large terms and comes out in fp32.
+// have equal work). Products that share an operand go together. What dbeta and dg
+// are made of is in two tf32 parts (mma_tf32.cuh); what only dQ and dK are made of
+// is in one for bf16 inputs, whose results are rounded to 8 bits next.
 #include "delta.cuh"
 
 namespace kata {
@@ -48,8 +50,10 @@ struct GradSmem {
     static constexpr int E = DO + kC * SS * (int)sizeof(Tin), Z = E + kC * SS * 4;
     static constexpr int S0 = Z + kC * SS * 4, DS = S0 + D * SS * 4;
     static constexpr int M = DS + D * SS * 4, N = M + kC * kTS * 4;
-    static constexpr int VEC = N + kC * kTS * 4;  // beta, a, c, G (hi, lo), dbeta [2], dG [2], end [8]
-    static constexpr int BYTES = VEC + (9 * kC + 8) * 4;
+    // beta, a, c, G (hi, lo); sums of column halves: dbeta, dG, w; column sums of x per row
+    // block [4]; the chunk's sums per warp [8]
+    static constexpr int VEC = N + kC * kTS * 4;
+    static constexpr int BYTES = VEC + (15 * kC + 8) * 4;
 };
 
 template <typename Tin>
@@ -80,7 +84,8 @@ __global__ void __launch_bounds__(256, D <= 64 ? 2 : 1) delta_grad(Args p, Grads
     float *sM = reinterpret_cast<float *>(sm + L::M), *sN = reinterpret_cast<float *>(sm + L::N);
     float *beta = reinterpret_cast<float *>(sm + L::VEC), *ca = beta + kC, *cc = ca + kC;
     float *ghi = cc + kC, *glo = ghi + kC;
-    float *sdb = glo + kC, *sdG = sdb + 2 * kC, *send = sdG + 2 * kC;
+    float *sdb = glo + kC, *sdG = sdb + 2 * kC, *sw = sdG + 2 * kC;
+    float *sx = sw + 2 * kC, *send = sx + 4 * kC;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int gr = lane >> 2, t2 = 2 * (lane & 3);
     const int rb = warp & 3, hf = warp >> 2, m0 = 16 * rb;
@@ -155,7 +160,7 @@ __global__ void __launch_bounds__(256, D <= 64 ? 2 : 1) delta_grad(Args p, Grads
     clear(dq);
     clear(dr);
     clear(dl);
-    float db[2] = {0.f, 0.f}, end = 0.f;
+    float db[2] = {0.f, 0.f}, w[2] = {0.f, 0.f}, end = 0.f;  // rows gr, gr + 8
     const float aC = ca[kC - 1];
     const int d0 = hf * (D / 2);  // this warp's columns of a [64, D] product
     for (int c0 = 0; c0 < D; c0 += SL) {
@@ -191,30 +196,40 @@ __global__ void __launch_bounds__(256, D <= 64 ? 2 : 1) delta_grad(Args p, Grads
                     const float E = sE[i * SS + f0 + 8 * nt + t2 + (e & 1)];
                     const float ckd = cc[i] * kd[nt][e];
                     db[e >> 1] = fmaf(E, ckd - md[nt][e], db[e >> 1]);
-                    end = fmaf(beta[i] * E, ckd, end);
+                    w[e >> 1] = fmaf(beta[i] * E, ckd, w[e >> 1]);
                 }
         }
         for (int i = tid; i < D * SL; i += 256) {
             const int at = (i / SL) * SS + i % SL;
             end = fmaf(aC * sS0[at], sDS[at], end);
         }
-        auto ucol = [&](int n, int k) {  // U's row as a column of U^T
-            const int j = 2 * (n & ~7) + 8 * hf + (n & 7);
-            const float4 x = quad<true, true>(sE, SS, j, k);
-            return make_float4(beta[j] * x.x, beta[j] * x.y, beta[j] * x.z, beta[j] * x.w);
-        };
-        gemm<TI, 2, 4, true>(
-            pm, 0, SL / 16, [&](int m, int k) { return quad<true, true>(sO + m0 * SS, SS, m, k); }, ucol,
-            nt_end);
-        gemm<2, 2, 4, true>(
-            pn, 0, SL / 16, [&](int m, int k) { return quad<true, true>(sZ + m0 * SS, SS, m, k); }, ucol,
-            nt_end);
-        auto scol = [&](int n, int k) { return quad<true, true>(sS0 + d0 * SS, SS, n, k); };
-        gemm<TI, 2, ND, true>(
-            dq, 0, SL / 16, [&](int m, int k) { return quad<true, true>(sO + m0 * SS, SS, m, k); }, scol);
-        gemm<2, 2, ND, true>(
-            dr, 0, SL / 16, [&](int m, int k) { return quad<true, true>(sZ + m0 * SS, SS, m, k); }, scol);
-        gemm<2, 2, ND, true>(
+        const int t4 = 4 * (lane & 3);
+#pragma unroll 1
+        for (int ks = 0; ks < SL / 16; ++ks) {  // dO and Z against U's rows and S0's
+            const int k = 16 * ks + t4;
+            FragA<TI> ao[1];
+            FragA<2> az[1];
+            ao[0].set(quad<true, true>(sO + m0 * SS, SS, gr, k), quad<true, true>(sO + m0 * SS, SS, gr + 8, k));
+            az[0].set(quad<true, true>(sZ + m0 * SS, SS, gr, k), quad<true, true>(sZ + m0 * SS, SS, gr + 8, k));
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt) {
+                if (nt >= nt_end) continue;
+                const int j = 8 * (2 * nt + hf) + gr;
+                const float4 x = quad<true, true>(sE, SS, j, k);
+                FragB<2> b[1][1];
+                b[0][0].set(make_float4(beta[j] * x.x, beta[j] * x.y, beta[j] * x.z, beta[j] * x.w));
+                mma_step<TI, 2, 1, 1>(*reinterpret_cast<float(*)[1][4]>(&pm[nt]), ao, b);
+                mma_step<2, 2, 1, 1>(*reinterpret_cast<float(*)[1][4]>(&pn[nt]), az, b);
+            }
+#pragma unroll
+            for (int nt = 0; nt < ND; ++nt) {
+                FragB<2> b[1][1];
+                b[0][0].set(quad<true, true>(sS0 + d0 * SS, SS, 8 * nt + gr, k));
+                mma_step<TI, 2, 1, 1>(*reinterpret_cast<float(*)[1][4]>(&dq[nt]), ao, b);
+                mma_step<2, 2, 1, 1>(*reinterpret_cast<float(*)[1][4]>(&dr[nt]), az, b);
+            }
+        }
+        gemm<TI, TI, ND, true>(
             dl, 0, SL / 16, [&](int m, int k) { return quad<true, true>(sE + m0 * SS, SS, m, k); },
             [&](int n, int k) { return quad<true, true>(sDS + d0 * SS, SS, n, k); });
         Tin *dv = static_cast<Tin *>(gr_.dv);
@@ -224,83 +239,114 @@ __global__ void __launch_bounds__(256, D <= 64 ? 2 : 1) delta_grad(Args p, Grads
                 store2(dv + (row0 + t0 + r) * (size_t)D + c0 + c, sZ[r * SS + c], sZ[r * SS + c + 1]);
         }
     }
-    __syncthreads();  // M and N are read; PM and PN take their places
+    // x, its sums over rows and columns, and PM and PN in the places of M and N (each
+    // thread overwrites the values that it alone reads here)
+    __syncthreads();
+    float dG[2] = {0.f, 0.f};
 #pragma unroll
     for (int nt = 0; nt < 4; ++nt) {
         if (nt >= nt_end) continue;
         const int j = col(nt, 0);
+        float2 cs = make_float2(0.f, 0.f);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int i = row(2 * h);
             const float2 dec = decay2(ghi[i], glo[i], ghi, glo, j);
-            *reinterpret_cast<float2 *>(sM + i * kTS + j) =
-                make_float2(i >= j ? p.scale * pm[nt][2 * h] * dec.x : 0.f,
-                            i >= j + 1 ? p.scale * pm[nt][2 * h + 1] * dec.y : 0.f);
-            *reinterpret_cast<float2 *>(sN + i * kTS + j) =
-                make_float2(i > j ? -pn[nt][2 * h] * dec.x : 0.f,
-                            i > j + 1 ? -pn[nt][2 * h + 1] * dec.y : 0.f);
+            float2 *pM = reinterpret_cast<float2 *>(sM + i * kTS + j);
+            float2 *pN = reinterpret_cast<float2 *>(sN + i * kTS + j);
+            const float2 m = *pM, n = *pN;  // zero above the diagonal
+            const float m0_ = p.scale * pm[nt][2 * h], m1_ = p.scale * pm[nt][2 * h + 1];
+            const float x0 = m0_ * m.x - pn[nt][2 * h] * n.x, x1 = m1_ * m.y - pn[nt][2 * h + 1] * n.y;
+            dG[h] += x0 + x1;
+            cs.x += x0;
+            cs.y += x1;
+            *pM = make_float2(i >= j ? m0_ * dec.x : 0.f, i >= j + 1 ? m1_ * dec.y : 0.f);
+            *pN = make_float2(i > j ? -pn[nt][2 * h] * dec.x : 0.f,
+                              i > j + 1 ? -pn[nt][2 * h + 1] * dec.y : 0.f);
         }
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) {
+            cs.x += __shfl_xor_sync(0xffffffffu, cs.x, off);
+            cs.y += __shfl_xor_sync(0xffffffffu, cs.y, off);
+        }
+        if (gr == 0) *reinterpret_cast<float2 *>(sx + rb * kC + j) = cs;
     }
-#pragma unroll
-    for (int nt = 0; nt < ND; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int i = row(e);
-            dq[nt][e] *= p.scale * ca[i];
-            dr[nt][e] *= -ca[i];
-            dl[nt][e] *= beta[i] * cc[i];
-        }
-    __syncthreads();
-    auto kc = [&](int n, int k) { return quad<false, false>(sK + d0, KS, n, k); };
-    gemm<2, TI, ND, false>(
-        dq, 0, nt_end, [&](int m, int k) { return quad<true, false>(sM + m0 * kTS, kTS, m, k); }, kc);
-    gemm<2, TI, ND, false>(
-        dr, 0, nt_end, [&](int m, int k) { return quad<true, false>(sN + m0 * kTS, kTS, m, k); }, kc);
-    gemm<2, TI, ND, false>(
-        dl, rb, 4, [&](int m, int k) { return quad<false, false>(sM + m0, kTS, m, k); },
-        [&](int n, int k) { return quad<false, false>(sQ + d0, KS, n, k); });
-    gemm<2, TI, ND, false>(
-        dl, rb, 4, [&](int m, int k) { return quad<false, false>(sN + m0, kTS, m, k); }, kc);
-
-    float dG[2] = {0.f, 0.f};
 #pragma unroll
     for (int nt = 0; nt < ND; ++nt)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int i = m0 + gr + 8 * h, n = d0 + 8 * nt + t2;
             const float2 kx = two(sK + i * KS + n), qx = two(sQ + i * KS + n);
-            const float q0 = dq[nt][2 * h], q1 = dq[nt][2 * h + 1];
-            const float r0 = dr[nt][2 * h], r1 = dr[nt][2 * h + 1];
-            const float l0 = dl[nt][2 * h], l1 = dl[nt][2 * h + 1];
-            dG[h] = fmaf(qx.x, q0, fmaf(kx.x, r0 - l0, dG[h]));
-            dG[h] = fmaf(qx.y, q1, fmaf(kx.y, r1 - l1, dG[h]));
-            if (t0 + i < p.T) {
-                const size_t at = (row0 + t0 + i) * (size_t)D + n;
-                store2(static_cast<Tin *>(gr_.dq) + at, q0, q1);
-                store2(static_cast<Tin *>(gr_.dk) + at, r0 + l0, r1 + l1);
-            }
+            const float sa = p.scale * ca[i], bc = beta[i] * cc[i];
+            float *q2 = &dq[nt][2 * h], *r2 = &dr[nt][2 * h], *l2 = &dl[nt][2 * h];
+            q2[0] *= sa;
+            q2[1] *= sa;
+            r2[0] *= -ca[i];
+            r2[1] *= -ca[i];
+            dG[h] = fmaf(qx.x, q2[0], fmaf(qx.y, q2[1], dG[h]));
+            dG[h] = fmaf(kx.x, r2[0], fmaf(kx.y, r2[1], dG[h]));
+            r2[0] = fmaf(bc, l2[0], r2[0]);  // from here on dK
+            r2[1] = fmaf(bc, l2[1], r2[1]);
         }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
+        end += w[h];
 #pragma unroll
         for (int off = 1; off < 4; off <<= 1) {
             dG[h] += __shfl_xor_sync(0xffffffffu, dG[h], off);
             db[h] += __shfl_xor_sync(0xffffffffu, db[h], off);
+            w[h] += __shfl_xor_sync(0xffffffffu, w[h], off);
         }
         if ((lane & 3) == 0) {
             sdG[hf * kC + m0 + gr + 8 * h] = dG[h];
             sdb[hf * kC + m0 + gr + 8 * h] = db[h];
+            sw[hf * kC + m0 + gr + 8 * h] = w[h];
         }
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) end += __shfl_xor_sync(0xffffffffu, end, off);
     if (lane == 0) send[warp] = end;
     __syncthreads();
+#pragma unroll 1
+    for (int ks = 0; ks < nt_end; ++ks) {  // PM and PN against K
+        const int k = 16 * ks + t2;
+        FragA<TI> am[1], an[1];
+        am[0].set(quad<true, false>(sM + m0 * kTS, kTS, gr, k), quad<true, false>(sM + m0 * kTS, kTS, gr + 8, k));
+        an[0].set(quad<true, false>(sN + m0 * kTS, kTS, gr, k), quad<true, false>(sN + m0 * kTS, kTS, gr + 8, k));
+#pragma unroll
+        for (int nt = 0; nt < ND; ++nt) {
+            FragB<TI> b[1][1];
+            b[0][0].set(quad<false, false>(sK + d0, KS, 8 * nt + gr, k));
+            mma_step<TI, TI, 1, 1>(*reinterpret_cast<float(*)[1][4]>(&dq[nt]), am, b);
+            mma_step<TI, TI, 1, 1>(*reinterpret_cast<float(*)[1][4]>(&dr[nt]), an, b);
+        }
+    }
+    gemm<TI, TI, ND, false>(
+        dr, rb, 4, [&](int m, int k) { return quad<false, false>(sM + m0, kTS, m, k); },
+        [&](int n, int k) { return quad<false, false>(sQ + d0, KS, n, k); });
+    gemm<TI, TI, ND, false>(
+        dr, rb, 4, [&](int m, int k) { return quad<false, false>(sN + m0, kTS, m, k); },
+        [&](int n, int k) { return quad<false, false>(sK + d0, KS, n, k); });
+#pragma unroll
+    for (int nt = 0; nt < ND; ++nt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int i = m0 + gr + 8 * h;
+            if (t0 + i >= p.T) continue;
+            const size_t at = (row0 + t0 + i) * (size_t)D + d0 + 8 * nt + t2;
+            store2(static_cast<Tin *>(gr_.dq) + at, dq[nt][2 * h], dq[nt][2 * h + 1]);
+            store2(static_cast<Tin *>(gr_.dk) + at, dr[nt][2 * h], dr[nt][2 * h + 1]);
+        }
     if (warp == 0) {  // dg: sums from each token to the chunk's end, two tokens per lane
         double tail = 0.0;
         for (int w = 0; w < 8; ++w) tail += send[w];
         const int i = 2 * lane;
-        const double x0 = (double)sdG[i] + sdG[kC + i], x1 = (double)sdG[i + 1] + sdG[kC + i + 1];
+        double x0 = (double)sdG[i] + sdG[kC + i] - sw[i] - sw[kC + i];
+        double x1 = (double)sdG[i + 1] + sdG[kC + i + 1] - sw[i + 1] - sw[kC + i + 1];
+        for (int b = i / 16; b < 4; ++b) {  // the row blocks that see column i
+            x0 -= sx[b * kC + i];
+            x1 -= sx[b * kC + i + 1];
+        }
         double sum = x0 + x1;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
