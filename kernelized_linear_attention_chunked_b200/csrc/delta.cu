@@ -26,7 +26,7 @@ template <typename Tin, int D>
 cudaError_t prefill_d(const Args &p, const Scratch &w, long heads, cudaStream_t stream) {
     cudaError_t e = launch_prep<Tin, D, false>(p, w, Scratch{}, heads, stream);
     if (e != cudaSuccess) return e;
-    return launch_chain<Tin, D, false, false>(p, w, heads, stream);
+    return launch_chain<Tin, D>(p, w, heads, stream);
 }
 
 template <typename Tin>

@@ -17,7 +17,7 @@
 // minus infinity (the state starts anew) does not make inf - inf.
 //
 // Two launches. delta_prep: one CTA per (chunk, head), everything that needs
-// no state (W = X diag(a) K, XV, M). delta_chain: one CTA per (head, slice of
+// no state (W = X diag(a) K, XV, M). delta_chain: one CTA per (head, 16
 // value columns) walks the chunks; columns of the state are independent, so
 // the slices never meet. Its two products per chunk, E = XV - W S0 and
 // S_C = .. + K^T (..E), are the serial part, so the inverse is applied to K
@@ -444,7 +444,7 @@ struct ChainSmem {
     static constexpr int BYTES = STAGE + STAGES * STAGE_BYTES;
 };
 
-// The walk over the chunks, one CTA per (head, NS value columns). Warps 0-3
+// The walk over the chunks, one CTA per (head, NS value columns): `cta` of them. Warps 0-3
 // carry the chain: they hold the state in registers (fp32, D / 4 rows each)
 // and take two dependent products per chunk. Warps 4-7 take the products that
 // hang off it: the outputs (forward) or Q^T dO (REV). Warps 8-11 bring K, Q and
@@ -456,7 +456,7 @@ struct ChainSmem {
 // the writer, as pairs, the walk took 348 us instead of 339 us at B2 H16 T16384
 // d64).
 template <typename Tin, int D, int NS, bool REV, bool KEEP>
-__global__ void __launch_bounds__(kChainThreads, 1) delta_chain(Args p, Scratch w) {
+__device__ __forceinline__ void walk_chunks(const Args &p, const Scratch &w, const unsigned cta) {
     using namespace tf;
     using L = ChainSmem<Tin, D, NS, REV>;
     constexpr int KS = L::KS, ST = L::ST, NT = NS / 8, TI = Parts<Tin>::N;
@@ -467,8 +467,8 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain(Args p, Scratch 
     float *sY = reinterpret_cast<float *>(sm + L::Y), *sG = reinterpret_cast<float *>(sm + L::GQ);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int gr = lane >> 2, t2 = 2 * (lane & 3);
-    const size_t head = blockIdx.x / (D / NS);
-    const int slice = blockIdx.x % (D / NS), c0 = slice * NS;
+    const size_t head = cta / (D / NS);
+    const int slice = cta % (D / NS), c0 = slice * NS;
     const size_t row0 = head * (size_t)p.T;
     const int m0 = 16 * (warp & 3);
     const bool wantO = !REV && p.o != nullptr;
@@ -745,6 +745,26 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_chain(Args p, Scratch 
     }
 }
 
+constexpr int kSlice = 16;  // value columns per CTA
+
+template <typename Tin, int D>
+__global__ void __launch_bounds__(kChainThreads, 1) delta_chain(Args p, Scratch w) {
+    walk_chunks<Tin, D, kSlice, false, false>(p, w, blockIdx.x);
+}
+
+// The gradients' two walks in one launch, the longer one's CTAs first: neither
+// needs the other, and few heads leave most SMs idle (34 -> 20 us for both at
+// B1 H6 T777 d32 fp32; no difference where either fills the GPU).
+template <typename Tin, int D>
+__global__ void __launch_bounds__(kChainThreads, 1)
+    delta_walks(Args back, Scratch wb, Args forth, Scratch wf) {
+    const unsigned half = gridDim.x / 2;
+    if (blockIdx.x < half)
+        walk_chunks<Tin, D, kSlice, true, true>(back, wb, blockIdx.x);
+    else
+        walk_chunks<Tin, D, kSlice, false, true>(forth, wf, blockIdx.x - half);
+}
+
 // Kernels with over 48 KB of dynamic shared memory need their limit raised,
 // once per device (the attribute is the current device's).
 template <auto Kern>
@@ -771,19 +791,27 @@ cudaError_t launch_prep(const Args &p, const Scratch &f, const Scratch &r, long 
     return after_launch();
 }
 
-template <typename Tin, int D, int NS, bool REV, bool KEEP>
-cudaError_t launch_chain_ns(const Args &p, const Scratch &w, long heads, cudaStream_t stream) {
-    constexpr int bytes = ChainSmem<Tin, D, NS, REV>::BYTES;
+template <typename Tin, int D>
+cudaError_t launch_chain(const Args &p, const Scratch &w, long heads, cudaStream_t stream) {
+    constexpr int bytes = ChainSmem<Tin, D, kSlice, false>::BYTES;
     static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
-    cudaError_t e = raise_smem<delta_chain<Tin, D, NS, REV, KEEP>>(bytes);
+    cudaError_t e = raise_smem<delta_chain<Tin, D>>(bytes);
     if (e != cudaSuccess) return e;
-    delta_chain<Tin, D, NS, REV, KEEP><<<(unsigned)(heads * (D / NS)), kChainThreads, bytes, stream>>>(p, w);
+    delta_chain<Tin, D><<<(unsigned)(heads * (D / kSlice)), kChainThreads, bytes, stream>>>(p, w);
     return after_launch();
 }
 
-template <typename Tin, int D, bool REV, bool KEEP>
-cudaError_t launch_chain(const Args &p, const Scratch &w, long heads, cudaStream_t stream) {
-    return launch_chain_ns<Tin, D, 16, REV, KEEP>(p, w, heads, stream);
+template <typename Tin, int D>
+cudaError_t launch_walks(const Args &back, const Scratch &wb, const Args &forth, const Scratch &wf,
+                         long heads, cudaStream_t stream) {
+    constexpr int b0 = ChainSmem<Tin, D, kSlice, true>::BYTES;
+    constexpr int b1 = ChainSmem<Tin, D, kSlice, false>::BYTES, bytes = b0 > b1 ? b0 : b1;
+    static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
+    cudaError_t e = raise_smem<delta_walks<Tin, D>>(bytes);
+    if (e != cudaSuccess) return e;
+    delta_walks<Tin, D><<<(unsigned)(2 * heads * (D / kSlice)), kChainThreads, bytes, stream>>>(
+        back, wb, forth, wf);
+    return after_launch();
 }
 
 inline int chunks_of(int T) { return (T + kC - 1) / kC; }

@@ -15,9 +15,8 @@
 //     dG_i = sum_j x_ij - sum_j x_ji + scale a_i q_i.(S0 dO_i) - a_i k_i.(S0 Z_i) - w_i,
 //     dg_t = sum_{i >= t in the chunk} dG_i + (a_C <S0, dS> + sum_j w_j).
 //
-// Four launches: delta_prep (the operands of both walks), the two walks (the
-// states and errors forwards, their gradients backwards; neither needs the
-// other), and delta_grad, one CTA per (chunk, head), for everything above. The
+// Three launches: delta_prep (the operands of both walks), delta_walks (the
+// states and errors forwards, their gradients backwards), and delta_grad, one CTA per (chunk, head), for everything above. The
 // states and errors of every chunk are kept in the workspace in fp32.
 //
 // delta_grad takes the value columns in slices of 32, so that d = 128 fits a
@@ -391,13 +390,12 @@ cudaError_t backward_d(const DeltaArgs &a, const DeltaGrads &g, cudaStream_t str
     fw.S_in = a.S_in;
     fw.keepY = E;
     fw.keepS = S0;
-    if ((e = launch_chain<Tin, D, false, true>(fw, f, a.heads, stream)) != cudaSuccess) return e;
     Args bw = p;
     bw.S_in = g.dS_out;
     bw.S_out = g.dS_in;
     bw.keepY = Z;
     bw.keepS = dS;
-    if ((e = launch_chain<Tin, D, true, true>(bw, r, a.heads, stream)) != cudaSuccess) return e;
+    if ((e = launch_walks<Tin, D>(bw, r, fw, f, a.heads, stream)) != cudaSuccess) return e;
 
     constexpr int bytes = GradSmem<Tin, D>::BYTES;
     static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
