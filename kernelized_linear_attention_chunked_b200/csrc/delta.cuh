@@ -36,11 +36,10 @@
 // rounded to bf16 at the end, takes the one-part form.
 #pragma once
 
-#include <atomic>
-
 #include "kata_common.cuh"
 #include "kata_internal.h"
 #include "mma_tf32.cuh"
+#include "tc_tiles.cuh"
 
 namespace kata {
 namespace delta {
@@ -188,7 +187,8 @@ __device__ __forceinline__ void invert(const float *sA, float *sX, int warp, int
         float acc[1][4];
         clear(acc);
         gemm<2, 2, 1, false>(
-            acc, 0, 1, [&](int m, int k) { return quad<true, false>(sA + (r0 + 16) * kTS + r0, kTS, m, k); },
+            acc, 0, 1,
+            [&](int m, int k) { return quad<true, false>(sA + (r0 + 16) * kTS + r0, kTS, m, k); },
             [&](int n, int k) { return quad<false, false>(sX + r0 * kTS + c, kTS, n, k); });
         float *P = sX + r0 * kTS + c + 16;
         *reinterpret_cast<float2 *>(P + g * kTS + t2) = make_float2(acc[0][0], acc[0][1]);
@@ -207,33 +207,41 @@ __device__ __forceinline__ void invert(const float *sA, float *sX, int warp, int
     if (warp < 4) {  // the lower left 32 x 32 block: warp w takes its columns 8 w .. 8 w + 7
         const int c = 8 * warp;
         float *P = sX + 32 + c;
+        // rows m0 .. of A (32 columns) times a 32 x 8 B: both sixteens of k at once, or one
+        auto product = [&](float(&acc)[1][4], const float *A, const float *B, bool first, bool second) {
+            FragA<2> a[2];
+            FragB<2> b[2][1];
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
-            float acc[1][4];
-            clear(acc);
-            gemm<2, 2, 1, false>(  // X11's rows above its diagonal blocks hold no values
-                acc, warp >= 2 ? 1 : 0, 2,
-                [&](int m, int k) { return quad<true, false>(sA + (32 + 16 * mt) * kTS, kTS, m, k); },
-                [&](int n, int k) { return quad<false, false>(sX + c, kTS, n, k); });
-            *reinterpret_cast<float2 *>(P + (16 * mt + g) * kTS + t2) =
-                make_float2(acc[0][0], acc[0][1]);
-            *reinterpret_cast<float2 *>(P + (16 * mt + g + 8) * kTS + t2) =
-                make_float2(acc[0][2], acc[0][3]);
-        }
-        __syncwarp();
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
-            float acc[1][4];
-            clear(acc);
-            gemm<2, 2, 1, false>(
-                acc, 0, mt + 1,
-                [&](int m, int k) { return quad<true, false>(sX + (32 + 16 * mt) * kTS + 32, kTS, m, k); },
-                [&](int n, int k) { return quad<false, false>(P, kTS, n, k); });
-            float *O = sX + (32 + 16 * mt) * kTS + c;
-            *reinterpret_cast<float2 *>(O + g * kTS + t2) = make_float2(-acc[0][0], -acc[0][1]);
+            for (int s = 0; s < 2; ++s) {
+                a[s].set(quad<true, false>(A, kTS, g, 16 * s + t2), quad<true, false>(A, kTS, g + 8, 16 * s + t2));
+                float4 x = quad<false, false>(B, kTS, g, 16 * s + t2);
+                if (!(s ? second : first)) x = make_float4(0.f, 0.f, 0.f, 0.f);
+                b[s][0].set(x);
+            }
+            mma_step<2, 2, 1, 2>(acc, a, b);
+        };
+        auto put = [&](float *O, const float(&acc)[1][4], float sign) {
+            *reinterpret_cast<float2 *>(O + g * kTS + t2) = make_float2(sign * acc[0][0], sign * acc[0][1]);
             *reinterpret_cast<float2 *>(O + (g + 8) * kTS + t2) =
-                make_float2(-acc[0][2], -acc[0][3]);
+                make_float2(sign * acc[0][2], sign * acc[0][3]);
+        };
+        float acc[2][1][4];
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {  // X11 has nothing above its diagonal blocks
+            clear(acc[mt]);
+            product(acc[mt], sA + (32 + 16 * mt) * kTS, sX + c, warp < 2, true);
         }
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) put(P + 16 * mt * kTS, acc[mt], 1.f);
+        __syncwarp();
+        clear(acc[0]);  // nor X22, so its first row block takes one sixteen
+        gemm<2, 2, 1, false>(
+            acc[0], 0, 1, [&](int m, int k) { return quad<true, false>(sX + 32 * kTS + 32, kTS, m, k); },
+            [&](int n, int k) { return quad<false, false>(P, kTS, n, k); });
+        clear(acc[1]);
+        product(acc[1], sX + 48 * kTS + 32, P, true, true);
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) put(sX + (32 + 16 * mt) * kTS + c, acc[mt], -1.f);
     }
     __syncthreads();
 }
@@ -282,6 +290,7 @@ __global__ void __launch_bounds__(256) delta_prep(Args p, Scratch f, Scratch r) 
     const int t0 = (int)(ch % p.nc) * kC;
     const size_t row0 = head * (size_t)p.T;
 
+    if (tid == 0) sm100::launch_dependents();  // the walks: they wait for this grid's end
     float2 v2 = make_float2(0.f, 0.f);
     if (warp == 0) v2 = load_decays(p.g, row0, t0, p.T);
     load_tile<Tin, D, 256>(sK, KS, static_cast<const Tin *>(p.k), row0, t0, p.T, D, 0, tid);
@@ -749,6 +758,7 @@ constexpr int kSlice = 16;  // value columns per CTA
 
 template <typename Tin, int D>
 __global__ void __launch_bounds__(kChainThreads, 1) delta_chain(Args p, Scratch w) {
+    sm100::grid_dependency_wait();  // delta_prep
     walk_chunks<Tin, D, kSlice, false, false>(p, w, blockIdx.x);
 }
 
@@ -759,25 +769,12 @@ template <typename Tin, int D>
 __global__ void __launch_bounds__(kChainThreads, 1)
     delta_walks(Args back, Scratch wb, Args forth, Scratch wf) {
     const unsigned half = gridDim.x / 2;
+    sm100::grid_dependency_wait();  // delta_prep
+    if (threadIdx.x == 0) sm100::launch_dependents();
     if (blockIdx.x < half)
         walk_chunks<Tin, D, kSlice, true, true>(back, wb, blockIdx.x);
     else
         walk_chunks<Tin, D, kSlice, false, true>(forth, wf, blockIdx.x - half);
-}
-
-// Kernels with over 48 KB of dynamic shared memory need their limit raised,
-// once per device (the attribute is the current device's).
-template <auto Kern>
-inline cudaError_t raise_smem(int bytes) {
-    static std::atomic<unsigned long long> done{0};  // one bit per device ordinal < 64
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
-    if (bit && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
-    e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess && bit) done.fetch_or(bit, std::memory_order_release);
-    return e;
 }
 
 template <typename Tin, int D, bool BACK>
@@ -785,7 +782,7 @@ cudaError_t launch_prep(const Args &p, const Scratch &f, const Scratch &r, long 
                         cudaStream_t stream) {
     constexpr int bytes = PrepSmem<Tin, D, BACK>::BYTES;
     static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
-    cudaError_t e = raise_smem<delta_prep<Tin, D, BACK>>(bytes);
+    cudaError_t e = tc::set_smem_once<delta_prep<Tin, D, BACK>>(bytes);
     if (e != cudaSuccess) return e;
     delta_prep<Tin, D, BACK><<<(unsigned)(heads * p.nc), 256, bytes, stream>>>(p, f, r);
     return after_launch();
@@ -795,10 +792,11 @@ template <typename Tin, int D>
 cudaError_t launch_chain(const Args &p, const Scratch &w, long heads, cudaStream_t stream) {
     constexpr int bytes = ChainSmem<Tin, D, kSlice, false>::BYTES;
     static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
-    cudaError_t e = raise_smem<delta_chain<Tin, D>>(bytes);
+    cudaError_t e = tc::set_smem_once<delta_chain<Tin, D>>(bytes);
     if (e != cudaSuccess) return e;
-    delta_chain<Tin, D><<<(unsigned)(heads * (D / kSlice)), kChainThreads, bytes, stream>>>(p, w);
-    return after_launch();
+    e = tc::launch_overlapped(delta_chain<Tin, D>, (unsigned)(heads * (D / kSlice)), kChainThreads, bytes,
+                              stream, p, w);
+    return e != cudaSuccess ? e : after_launch();
 }
 
 template <typename Tin, int D>
@@ -807,11 +805,11 @@ cudaError_t launch_walks(const Args &back, const Scratch &wb, const Args &forth,
     constexpr int b0 = ChainSmem<Tin, D, kSlice, true>::BYTES;
     constexpr int b1 = ChainSmem<Tin, D, kSlice, false>::BYTES, bytes = b0 > b1 ? b0 : b1;
     static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
-    cudaError_t e = raise_smem<delta_walks<Tin, D>>(bytes);
+    cudaError_t e = tc::set_smem_once<delta_walks<Tin, D>>(bytes);
     if (e != cudaSuccess) return e;
-    delta_walks<Tin, D><<<(unsigned)(2 * heads * (D / kSlice)), kChainThreads, bytes, stream>>>(
-        back, wb, forth, wf);
-    return after_launch();
+    e = tc::launch_overlapped(delta_walks<Tin, D>, (unsigned)(2 * heads * (D / kSlice)), kChainThreads,
+                              bytes, stream, back, wb, forth, wf);
+    return e != cudaSuccess ? e : after_launch();
 }
 
 inline int chunks_of(int T) { return (T + kC - 1) / kC; }

@@ -104,6 +104,7 @@ __global__ void __launch_bounds__(256, D <= 64 ? 2 : 1) delta_grad(Args p, Grads
     if (warp == 0) v2 = load_decays(p.g, row0, t0, p.T);
     load_tile<Tin, D, 256>(sK, KS, static_cast<const Tin *>(p.k), row0, t0, p.T, D, 0, tid);
     load_tile<Tin, D, 256>(sQ, KS, static_cast<const Tin *>(p.q), row0, t0, p.T, D, 0, tid);
+    sm100::grid_dependency_wait();  // delta_walks
     load_slice(0);
     if (warp == 0) cumulate(v2, ghi, glo);
     if (tid >= 192) {
@@ -399,10 +400,10 @@ cudaError_t backward_d(const DeltaArgs &a, const DeltaGrads &g, cudaStream_t str
 
     constexpr int bytes = GradSmem<Tin, D>::BYTES;
     static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
-    if ((e = raise_smem<delta_grad<Tin, D>>(bytes)) != cudaSuccess) return e;
-    delta_grad<Tin, D><<<(unsigned)chunks, 256, bytes, stream>>>(
-        p, Grads{g.dq, g.dk, g.dv, g.dg, g.dbeta, E, Z, S0, dS});
-    return after_launch();
+    if ((e = tc::set_smem_once<delta_grad<Tin, D>>(bytes)) != cudaSuccess) return e;
+    e = tc::launch_overlapped(delta_grad<Tin, D>, (unsigned)chunks, 256, bytes, stream, p,
+                              Grads{g.dq, g.dk, g.dv, g.dg, g.dbeta, E, Z, S0, dS});
+    return e != cudaSuccess ? e : after_launch();
 }
 
 template <typename Tin>

@@ -137,6 +137,7 @@ __global__ void __launch_bounds__(BwdCfg<D, ROWS>::THREADS) bwd_query(Args p) {
         load_tile<float, D, TH>(tileV(u), RS, static_cast<const float *>(p.v), row0, t, p.T, D, 0, tid);
         cp_commit();
     };
+    if (tid == 0) sm100::launch_dependents();  // bwd_key: it waits for this grid's end
     load_tile<float, D, TH, ROWS>(sQ, RS, static_cast<const float *>(p.q), row0, q0, p.T, D, 0, tid);
     load_tile<float, D, TH, ROWS>(sO, RS, static_cast<const float *>(p.d_o), row0, q0, p.T, D, 0, tid);
     prefetch(0);
@@ -288,6 +289,7 @@ __global__ void __launch_bounds__(BwdCfg<D, ROWS>::THREADS) bwd_key(Args p) {
     load_tile<float, D, TH, ROWS>(sK, RS, static_cast<const float *>(p.k), row0, k0, p.T, D, 0, tid);
     load_tile<float, D, TH, ROWS>(sV, RS, static_cast<const float *>(p.v), row0, k0, p.T, D, 0, tid);
     const int first = k0 / kB;
+    sm100::grid_dependency_wait();  // bwd_query's statistics
     prefetch(first);
     cp_wait_all();
     __syncthreads();
@@ -368,13 +370,13 @@ cudaError_t run(Args p, long heads, cudaStream_t stream) {
     static_assert(L::BYTES <= 227 * 1024, "shared memory of one CTA");
     p.tiles = (p.T + ROWS - 1) / ROWS;
     cudaError_t e;
-    if ((e = delta::raise_smem<bwd_query<D, ROWS>>(L::BYTES)) != cudaSuccess) return e;
-    if ((e = delta::raise_smem<bwd_key<D, ROWS>>(L::BYTES)) != cudaSuccess) return e;
+    if ((e = tc::set_smem_once<bwd_query<D, ROWS>>(L::BYTES)) != cudaSuccess) return e;
+    if ((e = tc::set_smem_once<bwd_key<D, ROWS>>(L::BYTES)) != cudaSuccess) return e;
     const unsigned grid = (unsigned)(heads * p.tiles);
     bwd_query<D, ROWS><<<grid, L::THREADS, L::BYTES, stream>>>(p);
     if ((e = after_launch()) != cudaSuccess) return e;
-    bwd_key<D, ROWS><<<grid, L::THREADS, L::BYTES, stream>>>(p);
-    return after_launch();
+    e = tc::launch_overlapped(bwd_key<D, ROWS>, grid, L::THREADS, L::BYTES, stream, p);
+    return e != cudaSuccess ? e : after_launch();
 }
 
 // 32 rows per CTA where 64 would not give every SM two

@@ -205,6 +205,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tma_load_3d(sm + L::OWN + h * L::TILE, &own1, 0, tile * 128 + h * kStep, head,
                             &bar[kOwn]);
             }
+            // the keys start on their own tiles while the last queries finish
+            if (KEYS)
+                grid_dependency_wait();
+            else
+                launch_dependents();
             int issued = 0;
             for (int s = 0, st = 0, par = 1; s < n; ++s) {
                 if (s >= kStages && !wait_over(st, par, 0x801)) break;
@@ -539,8 +544,8 @@ cudaError_t launch(const PrefillBackwardArgs &a, cudaStream_t stream) {
     if ((e = after_launch()) != cudaSuccess) return e;
     p.out0 = static_cast<__nv_bfloat16 *>(a.dk);
     p.out1 = static_cast<__nv_bfloat16 *>(a.dv);
-    backward_kernel<DH, true><<<grid, kThreads, K::BYTES, stream>>>(mk, mv, mq, mo, p);
-    return after_launch();
+    e = launch_overlapped(backward_kernel<DH, true>, grid, kThreads, K::BYTES, stream, mk, mv, mq, mo, p);
+    return e != cudaSuccess ? e : after_launch();
 }
 
 }  // namespace

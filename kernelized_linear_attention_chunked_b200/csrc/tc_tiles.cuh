@@ -103,6 +103,24 @@ inline cudaError_t set_smem_once(int bytes) {
     return e;
 }
 
+// Launch a kernel that may start while the one before it in the stream still runs;
+// it waits for it itself (grid_dependency_wait).
+template <class... P, class... A>
+inline cudaError_t launch_overlapped(void (*kern)(P...), unsigned grid, int threads, int bytes,
+                                     cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // [rows, d] bf16 rows in boxes of 128 rows x box_x columns. Q and K use
 // box_x = 64 with the 128-byte swizzle (for d = 32 the box reaches past the row
 // and the extra columns are zero-filled); V uses box_x = d, one swizzle atom
