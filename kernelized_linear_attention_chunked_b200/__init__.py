@@ -1,8 +1,12 @@
 """Causal kernelized linear attention (rank-one PSD feature phi(x) = x x^T) and
 the LoLA self-recall-error sparse cache on NVIDIA B200 (sm_100a).
 
-The computation lives in libkata.so (C ABI: include/kata.h); this package is
-its thin Python binding plus the seeded synthetic input generators.
+Beside them the gated delta rule (delta_prefill, delta_decode_step,
+delta_backward) and the gradients of the prefill (prefill_backward).
+
+The computation lives in libkata.so (C ABI: include/kata.h, kata_delta.h,
+kata_backward.h); this package is its thin Python binding plus the seeded
+synthetic input generators.
 """
 from ._binding import (  # noqa: F401
     KATA_BF16,

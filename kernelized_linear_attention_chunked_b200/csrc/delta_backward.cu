@@ -26,6 +26,10 @@
 // have equal work). Products that share an operand go together. What dbeta and dg
 // are made of is in two tf32 parts (mma_tf32.cuh); what only dQ and dK are made of
 // is in one for bf16 inputs, whose results are rounded to 8 bits next.
+//
+// Measured on B200 at B2 H16 T4096 d64 bf16: delta_prep 99 us, delta_walks 153,
+// delta_grad 195 (ncu: issue 52 %, tensor 39 %, shared memory 60 %, 16 warps per SM,
+// their registers and 101 KB of shared memory per CTA in the way of more).
 #include "delta.cuh"
 
 namespace kata {
