@@ -197,19 +197,19 @@ __device__ __forceinline__ void invert(const float *sA, float *sX, int warp, int
         const int r0 = 32 * (warp >> 1), c = r0 + 8 * (warp & 1);
         float acc[1][4];
         clear(acc);
-        gemm<2, 2, 1, false>(
+        gemm<2, 2, 1>(
             acc, 0, 1,
-            [&](int m, int k) { return quad<true, false>(sA + (r0 + 16) * kTS + r0, kTS, m, k); },
-            [&](int n, int k) { return quad<false, false>(sX + r0 * kTS + c, kTS, n, k); });
+            [&](int m, int k) { return quad<true>(sA + (r0 + 16) * kTS + r0, kTS, m, k); },
+            [&](int n, int k) { return quad<false>(sX + r0 * kTS + c, kTS, n, k); });
         float *P = sX + r0 * kTS + c + 16;
         *reinterpret_cast<float2 *>(P + g * kTS + t2) = make_float2(acc[0][0], acc[0][1]);
         *reinterpret_cast<float2 *>(P + (g + 8) * kTS + t2) = make_float2(acc[0][2], acc[0][3]);
         __syncwarp();
         clear(acc);
-        gemm<2, 2, 1, false>(
+        gemm<2, 2, 1>(
             acc, 0, 1,
-            [&](int m, int k) { return quad<true, false>(sX + (r0 + 16) * kTS + r0 + 16, kTS, m, k); },
-            [&](int n, int k) { return quad<false, false>(P, kTS, n, k); });
+            [&](int m, int k) { return quad<true>(sX + (r0 + 16) * kTS + r0 + 16, kTS, m, k); },
+            [&](int n, int k) { return quad<false>(P, kTS, n, k); });
         float *O = sX + (r0 + 16) * kTS + c;
         *reinterpret_cast<float2 *>(O + g * kTS + t2) = make_float2(-acc[0][0], -acc[0][1]);
         *reinterpret_cast<float2 *>(O + (g + 8) * kTS + t2) = make_float2(-acc[0][2], -acc[0][3]);
@@ -224,8 +224,8 @@ __device__ __forceinline__ void invert(const float *sA, float *sX, int warp, int
             FragB<2> b[2][1];
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                a[s].set(quad<true, false>(A, kTS, g, 16 * s + t2), quad<true, false>(A, kTS, g + 8, 16 * s + t2));
-                float4 x = quad<false, false>(B, kTS, g, 16 * s + t2);
+                a[s].set(quad<true>(A, kTS, g, 16 * s + t2), quad<true>(A, kTS, g + 8, 16 * s + t2));
+                float4 x = quad<false>(B, kTS, g, 16 * s + t2);
                 if (!(s ? second : first)) x = make_float4(0.f, 0.f, 0.f, 0.f);
                 b[s][0].set(x);
             }
@@ -246,9 +246,9 @@ __device__ __forceinline__ void invert(const float *sA, float *sX, int warp, int
         for (int mt = 0; mt < 2; ++mt) put(P + 16 * mt * kTS, acc[mt], 1.f);
         __syncwarp();
         clear(acc[0]);  // nor X22, so its first row block takes one sixteen
-        gemm<2, 2, 1, false>(
-            acc[0], 0, 1, [&](int m, int k) { return quad<true, false>(sX + 32 * kTS + 32, kTS, m, k); },
-            [&](int n, int k) { return quad<false, false>(P, kTS, n, k); });
+        gemm<2, 2, 1>(
+            acc[0], 0, 1, [&](int m, int k) { return quad<true>(sX + 32 * kTS + 32, kTS, m, k); },
+            [&](int n, int k) { return quad<false>(P, kTS, n, k); });
         clear(acc[1]);
         product(acc[1], sX + 48 * kTS + 32, P, true, true);
 #pragma unroll
@@ -341,25 +341,24 @@ __global__ void __launch_bounds__(256) delta_prep(Args p, Scratch f, Scratch r) 
     const bool wantQ = BACK || p.o;
     {
         // K K^T and Q K^T together: they share their B operand
-        const int t4 = 4 * (lane & 3);
         float kk[4][4], qk[4][4];
         clear(kk);
         clear(qk);
 #pragma unroll 1
         for (int ks = 0; ks < D / 16; ++ks) {
-            const int k = 16 * ks + t4;
+            const int k = 16 * ks + t2;
             FragA<TI> ak[1], aq[1];
-            ak[0].set(quad<true, true>(sK + m0 * KS, KS, gr, k), quad<true, true>(sK + m0 * KS, KS, gr + 8, k));
+            ak[0].set(quad<true>(sK + m0 * KS, KS, gr, k), quad<true>(sK + m0 * KS, KS, gr + 8, k));
             if (wantQ)
-                aq[0].set(quad<true, true>(sQ + m0 * KS, KS, gr, k),
-                       quad<true, true>(sQ + m0 * KS, KS, gr + 8, k));
+                aq[0].set(quad<true>(sQ + m0 * KS, KS, gr, k),
+                       quad<true>(sQ + m0 * KS, KS, gr + 8, k));
 #pragma unroll
             for (int nt = 0; nt < 4; nt += 2) {
                 if (nt >= nt_end) continue;
                 FragB<TI> b[1][2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e)  // beyond the diagonal block: computed, not used
-                    b[0][e].set(quad<true, true>(sK, KS, 8 * (2 * (nt + e) + hf) + gr, k));
+                    b[0][e].set(quad<true>(sK, KS, 8 * (2 * (nt + e) + hf) + gr, k));
                 mma_step<TI, TI, 2, 1>(*reinterpret_cast<float(*)[2][4]>(&kk[nt]), ak, b);
                 if (wantQ) mma_step<TI, TI, 2, 1>(*reinterpret_cast<float(*)[2][4]>(&qk[nt]), aq, b);
             }
@@ -398,16 +397,16 @@ __global__ void __launch_bounds__(256) delta_prep(Args p, Scratch f, Scratch r) 
     const int d0 = hf * (D / 2), td = hf * ND;
     float acc[ND][4];
     clear(acc);
-    gemm<2, TI, ND, false>(  // X V
-        acc, 0, rb + 1, [&](int m, int k) { return quad<true, false>(sX + m0 * kTS, kTS, m, k); },
-        [&](int n, int k) { return quad<false, false>(sV + d0, KS, n, k); });
+    gemm<2, TI, ND>(  // X V
+        acc, 0, rb + 1, [&](int m, int k) { return quad<true>(sX + m0 * kTS, kTS, m, k); },
+        [&](int n, int k) { return quad<false>(sV + d0, KS, n, k); });
     store_frags<D>(f.Y + ch * (kC * D), acc, rb, td, lane);
-    auto kcols = [&](int n, int k) { return quad<false, false>(sK + d0, KS, n, k); };
+    auto kcols = [&](int n, int k) { return quad<false>(sK + d0, KS, n, k); };
     clear(acc);
-    gemm<2, TI, ND, false>(  // X diag(a) K
+    gemm<2, TI, ND>(  // X diag(a) K
         acc, 0, rb + 1,
         [&](int m, int k) {
-            return scaled<false>(quad<true, false>(sX + m0 * kTS, kTS, m, k), ca, k);
+            return scaled(quad<true>(sX + m0 * kTS, kTS, m, k), ca, k);
         },
         kcols);
     store_frags<D>(f.W + ch * (kC * D), acc, rb, td, lane);
@@ -416,9 +415,9 @@ __global__ void __launch_bounds__(256) delta_prep(Args p, Scratch f, Scratch r) 
     // Z0 = X^T (scale diag(beta) M^T dO), W' = X^T diag(beta c) K: the
     // transposed factors reach from a row's own block to the last one
     clear(acc);
-    gemm<2, TI, ND, false>(
-        acc, rb, 4, [&](int m, int k) { return quad<false, false>(sM + m0, kTS, m, k); },
-        [&](int n, int k) { return quad<false, false>(sO + d0, KS, n, k); });
+    gemm<2, TI, ND>(
+        acc, rb, 4, [&](int m, int k) { return quad<false>(sM + m0, kTS, m, k); },
+        [&](int n, int k) { return quad<false>(sO + d0, KS, n, k); });
     __syncthreads();  // every warp has read V
     {
         const float s0 = p.scale * beta[m0 + gr], s1 = p.scale * beta[m0 + gr + 8];
@@ -431,15 +430,15 @@ __global__ void __launch_bounds__(256) delta_prep(Args p, Scratch f, Scratch r) 
     }
     __syncthreads();
     clear(acc);
-    gemm<2, 2, ND, false>(
-        acc, rb, 4, [&](int m, int k) { return quad<false, false>(sX + m0, kTS, m, k); },
-        [&](int n, int k) { return quad<false, false>(sP + d0, KS, n, k); });
+    gemm<2, 2, ND>(
+        acc, rb, 4, [&](int m, int k) { return quad<false>(sX + m0, kTS, m, k); },
+        [&](int n, int k) { return quad<false>(sP + d0, KS, n, k); });
     store_frags<D>(r.Y + ch * (kC * D), acc, rb, td, lane);
     clear(acc);
-    gemm<2, TI, ND, false>(
+    gemm<2, TI, ND>(
         acc, rb, 4,
         [&](int m, int k) {
-            return scaled<false>(quad<false, false>(sX + m0, kTS, m, k), bc, k);
+            return scaled(quad<false>(sX + m0, kTS, m, k), bc, k);
         },
         kcols);
     store_frags<D>(r.W + ch * (kC * D), acc, rb, td, lane);
@@ -599,7 +598,7 @@ __device__ __forceinline__ void walk_chunks(const Args &p, const Scratch &w, con
             a.set(make_float4(w0.x, w0.y, w1.x, w1.y), make_float4(w0.z, w0.w, w1.z, w1.w));
         };
         // a column's four k of the state or the errors
-        auto column = [&](const float *x, int n, int k) { return quad<false, false>(x, ST, n, k); };
+        auto column = [&](const float *x, int n, int k) { return quad<false>(x, ST, n, k); };
         if (chain) {
             // E = XV - W S0 (REV: Z = Z0 + W' dS)
             float acc[NT][4];
@@ -643,8 +642,8 @@ __device__ __forceinline__ void walk_chunks(const Args &p, const Scratch &w, con
             if (i + 1 < p.nc) load_frags();
         } else if (wantO) {
             clear(o);
-            gemm<TI, TI, NT, false>(
-                o, 0, D / 16, [&](int m, int k) { return quad<true, false>(sQ + m0 * KS, KS, m, k); },
+            gemm<TI, TI, NT>(
+                o, 0, D / 16, [&](int m, int k) { return quad<true>(sQ + m0 * KS, KS, m, k); },
                 [&](int n, int k) { return column(sS, n, k); });
             const float s0 = coef[m0 + gr], s1 = coef[m0 + gr + 8];
 #pragma unroll
@@ -658,11 +657,11 @@ __device__ __forceinline__ void walk_chunks(const Args &p, const Scratch &w, con
             for (int mt = warp & 3; mt < D / 16; mt += 4) {
                 float acc[NT][4];
                 clear(acc);
-                gemm<TI, 2, NT, false>(
+                gemm<TI, 2, NT>(
                     acc, 0, kC / 16,
-                    [&](int m, int k) { return quad<false, false>(sQ + 16 * mt, KS, m, k); },
+                    [&](int m, int k) { return quad<false>(sQ + 16 * mt, KS, m, k); },
                     [&](int n, int k) {
-                        return scaled<false>(quad<false, false>(sO, L::DS, n, k), coef, k);
+                        return scaled(quad<false>(sO, L::DS, n, k), coef, k);
                     });
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
@@ -694,8 +693,8 @@ __device__ __forceinline__ void walk_chunks(const Args &p, const Scratch &w, con
                     const Tin *ka = sK + 16 * (MT * warp + mt);
 #pragma unroll
                     for (int s = 0; s < 2; ++s)
-                        a[s].set(quad<false, false>(ka, KS, gr, 16 * (k0 + s) + t2),
-                                 quad<false, false>(ka, KS, gr + 8, 16 * (k0 + s) + t2));
+                        a[s].set(quad<false>(ka, KS, gr, 16 * (k0 + s) + t2),
+                                 quad<false>(ka, KS, gr + 8, 16 * (k0 + s) + t2));
                     mma_step<TI, 2, NT, 2>(acc[mt], a, b);
                 }
             }

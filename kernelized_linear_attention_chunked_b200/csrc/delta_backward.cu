@@ -131,13 +131,13 @@ __global__ void __launch_bounds__(256, D <= 64 ? 2 : 1) delta_grad(Args p, Grads
         clear(qk);
         // column 8 nt + g of the warp's tiles is column 16 nt + 8 hf + g of the product
         auto kcol = [&](int n, int k) {
-            return quad<true, true>(sK, KS, 2 * (n & ~7) + 8 * hf + (n & 7), k);
+            return quad<true>(sK, KS, 2 * (n & ~7) + 8 * hf + (n & 7), k);
         };
-        gemm<TI, TI, 4, true>(
-            kk, 0, D / 16, [&](int m, int k) { return quad<true, true>(sK + m0 * KS, KS, m, k); }, kcol,
+        gemm<TI, TI, 4>(
+            kk, 0, D / 16, [&](int m, int k) { return quad<true>(sK + m0 * KS, KS, m, k); }, kcol,
             nt_end);
-        gemm<TI, TI, 4, true>(
-            qk, 0, D / 16, [&](int m, int k) { return quad<true, true>(sQ + m0 * KS, KS, m, k); }, kcol,
+        gemm<TI, TI, 4>(
+            qk, 0, D / 16, [&](int m, int k) { return quad<true>(sQ + m0 * KS, KS, m, k); }, kcol,
             nt_end);
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt) {
@@ -179,19 +179,19 @@ __global__ void __launch_bounds__(256, D <= 64 ? 2 : 1) delta_grad(Args p, Grads
             float md[NF][4], kd[NF][4];
             clear(md);
             clear(kd);
-            gemm<2, TI, NF, false>(
-                md, rb, 4, [&](int m, int k) { return quad<false, false>(sM + m0, kTS, m, k); },
-                [&](int n, int k) { return quad<false, false>(sO + f0, SS, n, k); });
+            gemm<2, TI, NF>(
+                md, rb, 4, [&](int m, int k) { return quad<false>(sM + m0, kTS, m, k); },
+                [&](int n, int k) { return quad<false>(sO + f0, SS, n, k); });
 #pragma unroll
             for (int nt = 0; nt < NF; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) md[nt][e] *= -p.scale;
-            gemm<2, 2, NF, false>(
-                md, rb, 4, [&](int m, int k) { return quad<false, false>(sN + m0, kTS, m, k); },
-                [&](int n, int k) { return quad<false, false>(sZ + f0, SS, n, k); });
-            gemm<TI, 2, NF, false>(
-                kd, 0, D / 16, [&](int m, int k) { return quad<true, false>(sK + m0 * KS, KS, m, k); },
-                [&](int n, int k) { return quad<false, false>(sDS + f0, SS, n, k); });
+            gemm<2, 2, NF>(
+                md, rb, 4, [&](int m, int k) { return quad<false>(sN + m0, kTS, m, k); },
+                [&](int n, int k) { return quad<false>(sZ + f0, SS, n, k); });
+            gemm<TI, 2, NF>(
+                kd, 0, D / 16, [&](int m, int k) { return quad<true>(sK + m0 * KS, KS, m, k); },
+                [&](int n, int k) { return quad<false>(sDS + f0, SS, n, k); });
 #pragma unroll
             for (int nt = 0; nt < NF; ++nt)
 #pragma unroll
@@ -207,19 +207,18 @@ __global__ void __launch_bounds__(256, D <= 64 ? 2 : 1) delta_grad(Args p, Grads
             const int at = (i / SL) * SS + i % SL;
             end = fmaf(aC * sS0[at], sDS[at], end);
         }
-        const int t4 = 4 * (lane & 3);
 #pragma unroll 1
         for (int ks = 0; ks < SL / 16; ++ks) {  // dO and Z against U's rows and S0's
-            const int k = 16 * ks + t4;
+            const int k = 16 * ks + t2;
             FragA<TI> ao[1];
             FragA<2> az[1];
-            ao[0].set(quad<true, true>(sO + m0 * SS, SS, gr, k), quad<true, true>(sO + m0 * SS, SS, gr + 8, k));
-            az[0].set(quad<true, true>(sZ + m0 * SS, SS, gr, k), quad<true, true>(sZ + m0 * SS, SS, gr + 8, k));
+            ao[0].set(quad<true>(sO + m0 * SS, SS, gr, k), quad<true>(sO + m0 * SS, SS, gr + 8, k));
+            az[0].set(quad<true>(sZ + m0 * SS, SS, gr, k), quad<true>(sZ + m0 * SS, SS, gr + 8, k));
 #pragma unroll
             for (int nt = 0; nt < 4; ++nt) {
                 if (nt >= nt_end) continue;
                 const int j = 8 * (2 * nt + hf) + gr;
-                const float4 x = quad<true, true>(sE, SS, j, k);
+                const float4 x = quad<true>(sE, SS, j, k);
                 FragB<2> b[1][1];
                 b[0][0].set(make_float4(beta[j] * x.x, beta[j] * x.y, beta[j] * x.z, beta[j] * x.w));
                 mma_step<TI, 2, 1, 1>(*reinterpret_cast<float(*)[1][4]>(&pm[nt]), ao, b);
@@ -228,14 +227,14 @@ __global__ void __launch_bounds__(256, D <= 64 ? 2 : 1) delta_grad(Args p, Grads
 #pragma unroll
             for (int nt = 0; nt < ND; ++nt) {
                 FragB<2> b[1][1];
-                b[0][0].set(quad<true, true>(sS0 + d0 * SS, SS, 8 * nt + gr, k));
+                b[0][0].set(quad<true>(sS0 + d0 * SS, SS, 8 * nt + gr, k));
                 mma_step<TI, 2, 1, 1>(*reinterpret_cast<float(*)[1][4]>(&dq[nt]), ao, b);
                 mma_step<2, 2, 1, 1>(*reinterpret_cast<float(*)[1][4]>(&dr[nt]), az, b);
             }
         }
-        gemm<TI, TI, ND, true>(
-            dl, 0, SL / 16, [&](int m, int k) { return quad<true, true>(sE + m0 * SS, SS, m, k); },
-            [&](int n, int k) { return quad<true, true>(sDS + d0 * SS, SS, n, k); });
+        gemm<TI, TI, ND>(
+            dl, 0, SL / 16, [&](int m, int k) { return quad<true>(sE + m0 * SS, SS, m, k); },
+            [&](int n, int k) { return quad<true>(sDS + d0 * SS, SS, n, k); });
         Tin *dv = static_cast<Tin *>(gr_.dv);
         for (int i = tid; i < kC * SL / 2; i += 256) {
             const int r = i / (SL / 2), c = 2 * (i % (SL / 2));
@@ -315,22 +314,22 @@ __global__ void __launch_bounds__(256, D <= 64 ? 2 : 1) delta_grad(Args p, Grads
     for (int ks = 0; ks < nt_end; ++ks) {  // PM and PN against K
         const int k = 16 * ks + t2;
         FragA<TI> am[1], an[1];
-        am[0].set(quad<true, false>(sM + m0 * kTS, kTS, gr, k), quad<true, false>(sM + m0 * kTS, kTS, gr + 8, k));
-        an[0].set(quad<true, false>(sN + m0 * kTS, kTS, gr, k), quad<true, false>(sN + m0 * kTS, kTS, gr + 8, k));
+        am[0].set(quad<true>(sM + m0 * kTS, kTS, gr, k), quad<true>(sM + m0 * kTS, kTS, gr + 8, k));
+        an[0].set(quad<true>(sN + m0 * kTS, kTS, gr, k), quad<true>(sN + m0 * kTS, kTS, gr + 8, k));
 #pragma unroll
         for (int nt = 0; nt < ND; ++nt) {
             FragB<TI> b[1][1];
-            b[0][0].set(quad<false, false>(sK + d0, KS, 8 * nt + gr, k));
+            b[0][0].set(quad<false>(sK + d0, KS, 8 * nt + gr, k));
             mma_step<TI, TI, 1, 1>(*reinterpret_cast<float(*)[1][4]>(&dq[nt]), am, b);
             mma_step<TI, TI, 1, 1>(*reinterpret_cast<float(*)[1][4]>(&dr[nt]), an, b);
         }
     }
-    gemm<TI, TI, ND, false>(
-        dr, rb, 4, [&](int m, int k) { return quad<false, false>(sM + m0, kTS, m, k); },
-        [&](int n, int k) { return quad<false, false>(sQ + d0, KS, n, k); });
-    gemm<TI, TI, ND, false>(
-        dr, rb, 4, [&](int m, int k) { return quad<false, false>(sN + m0, kTS, m, k); },
-        [&](int n, int k) { return quad<false, false>(sK + d0, KS, n, k); });
+    gemm<TI, TI, ND>(
+        dr, rb, 4, [&](int m, int k) { return quad<false>(sM + m0, kTS, m, k); },
+        [&](int n, int k) { return quad<false>(sQ + d0, KS, n, k); });
+    gemm<TI, TI, ND>(
+        dr, rb, 4, [&](int m, int k) { return quad<false>(sN + m0, kTS, m, k); },
+        [&](int n, int k) { return quad<false>(sK + d0, KS, n, k); });
 #pragma unroll
     for (int nt = 0; nt < ND; ++nt)
 #pragma unroll

@@ -16,14 +16,15 @@
 // tensor cycles (6 x k16 against 3 x 2 x k8) and more instructions to form.
 //
 // A product advances sixteen k at a time, in two steps of eight whose k slots t
-// and t + 4 hold two neighbours. Which neighbours is free as long as both
-// operands agree:
-//   narrow  2t, 2t + 1 and 2t + 8, 2t + 9: an accumulator tile (row g, columns
-//           2t, 2t + 1; row g + 8, the same) is then, register for register, an A
-//           operand whose k runs over its columns, and an operand whose k runs
-//           down the rows of memory meets no bank conflict;
-//   wide    4t .. 4t + 3: a lane's four values are one load where k runs along
-//           the rows of memory in both operands.
+// and t + 4 hold two neighbours: lane (g, t) holds k = 2t, 2t + 1 and 2t + 8, 2t + 9.
+// The order of a sum's terms is free as long as both operands agree, and in this
+// one
+//   - an accumulator tile (row g, columns 2t, 2t + 1; row g + 8, the same) is,
+//     register for register, an A operand whose k runs over its columns,
+//   - neighbours along a row of memory are one load, without bank conflicts where
+//     rows start eight 32-bit banks apart (four for bf16). (One load of four
+//     neighbours, k = 4t .., meets two-way conflicts there and measured 0.5 to 3 %
+//     slower.)
 #pragma once
 
 #include <cuda_bf16.h>
@@ -133,13 +134,11 @@ __device__ __forceinline__ void mma_step(float (&acc)[NT][4], const FragA<TA> (&
         }
 }
 
-// The four k from `k` on (k = 16 step + 4t wide, + 2t narrow) of row or column
-// mn of an operand in shared memory. `K`: k runs along the rows of memory;
-// otherwise it is the row index.
-template <bool K, bool WIDE>
+// k, k + 1, k + 8, k + 9 (k = 16 step + 2t) of row or column mn of an operand in
+// shared memory. `K`: k runs along the rows of memory; otherwise it is the row
+// index.
+template <bool K>
 __device__ __forceinline__ float4 quad(const float *p, int stride, int mn, int k) {
-    static_assert(K || !WIDE, "rows of memory four apart share a bank");
-    if (K && WIDE) return *reinterpret_cast<const float4 *>(p + mn * stride + k);
     if (K) {
         const float2 a = *reinterpret_cast<const float2 *>(p + mn * stride + k);
         const float2 b = *reinterpret_cast<const float2 *>(p + mn * stride + k + 8);
@@ -151,18 +150,11 @@ __device__ __forceinline__ float4 quad(const float *p, int stride, int mn, int k
 __device__ __forceinline__ float2 unpack(uint32_t u) {
     return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
 }
-template <bool K, bool WIDE>
+template <bool K>
 __device__ __forceinline__ float4 quad(const __nv_bfloat16 *p, int stride, int mn, int k) {
-    static_assert(K || !WIDE, "rows of memory four apart share a bank");
     if (K) {
-        uint2 u;
-        if (WIDE) {
-            u = *reinterpret_cast<const uint2 *>(p + mn * stride + k);
-        } else {
-            u.x = *reinterpret_cast<const uint32_t *>(p + mn * stride + k);
-            u.y = *reinterpret_cast<const uint32_t *>(p + mn * stride + k + 8);
-        }
-        const float2 a = unpack(u.x), b = unpack(u.y);
+        const float2 a = unpack(*reinterpret_cast<const uint32_t *>(p + mn * stride + k));
+        const float2 b = unpack(*reinterpret_cast<const uint32_t *>(p + mn * stride + k + 8));
         return make_float4(a.x, a.y, b.x, b.y);
     }
     // a transposed 16 x 8 matrix load: lanes 0 .. 15 name the rows, and lane (g, t)
@@ -180,23 +172,21 @@ __device__ __forceinline__ float4 quad(const __nv_bfloat16 *p, int stride, int m
     return make_float4(a.x, a.y, b.x, b.y);
 }
 // A quad times c[.] of its k.
-template <bool WIDE>
 __device__ __forceinline__ float4 scaled(float4 x, const float *c, int k) {
-    return WIDE ? make_float4(x.x * c[k], x.y * c[k + 1], x.z * c[k + 2], x.w * c[k + 3])
-                : make_float4(x.x * c[k], x.y * c[k + 1], x.z * c[k + 8], x.w * c[k + 9]);
+    return make_float4(x.x * c[k], x.y * c[k + 1], x.z * c[k + 8], x.w * c[k + 9]);
 }
 
 // acc[NT] += A B over the sixteens of k from `s0` to `s1`. fa(m, k) and fb(n, k)
 // give quads of row m of A (0 .. 15) and of column n of B (0 .. 8 NT - 1).
 // Columns from 8 * nt_end on are left alone.
-template <int TA, int TB, int NT, bool WIDE, class FA, class FB>
+template <int TA, int TB, int NT, int UNROLL = 1, class FA, class FB>
 __device__ __forceinline__ void gemm(float (&acc)[NT][4], int s0, int s1, FA fa, FB fb,
                                      int nt_end = NT) {
-    const int g = (threadIdx.x & 31) >> 2, tk = (WIDE ? 4 : 2) * (threadIdx.x & 3);
+    const int g = (threadIdx.x & 31) >> 2, t2 = 2 * (threadIdx.x & 3);
     constexpr int G = NT % 2 == 0 ? 2 : 1;  // tiles at a time: more cost registers
-#pragma unroll 1
+#pragma unroll UNROLL
     for (int st = s0; st < s1; ++st) {
-        const int k = 16 * st + tk;
+        const int k = 16 * st + t2;
         FragA<TA> a[1];
         a[0].set(fa(g, k), fa(g + 8, k));
 #pragma unroll

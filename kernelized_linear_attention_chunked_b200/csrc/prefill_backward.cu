@@ -40,7 +40,6 @@ using delta::load_tile;
 
 constexpr int kB = 64;    // streamed rows per step
 constexpr int kTS = 72;   // row stride of a ROWS x 64 product
-constexpr int kFew = 16;  // queries whose scores are formed in 64 bits
 
 struct Args {
     const void *q, *k, *v, *d_o;
@@ -212,12 +211,12 @@ __global__ void __launch_bounds__(BwdCfg<D, ROWS>::THREADS) bwd_query(Args p) {
         } else {
             clear(s);
             clear(dp);
-            gemm<2, 2, 2, true>(
-                s, 0, D / 16, [&](int m, int kk) { return quad<true, true>(sQ + m0 * RS, RS, m, kk); },
-                [&](int n, int kk) { return quad<true, true>(k + n0 * RS, RS, n, kk); });
-            gemm<2, 2, 2, true>(
-                dp, 0, D / 16, [&](int m, int kk) { return quad<true, true>(sO + m0 * RS, RS, m, kk); },
-                [&](int n, int kk) { return quad<true, true>(v + n0 * RS, RS, n, kk); });
+            gemm<2, 2, 2, 4>(
+                s, 0, D / 16, [&](int m, int kk) { return quad<true>(sQ + m0 * RS, RS, m, kk); },
+                [&](int n, int kk) { return quad<true>(k + n0 * RS, RS, n, kk); });
+            gemm<2, 2, 2, 4>(
+                dp, 0, D / 16, [&](int m, int kk) { return quad<true>(sO + m0 * RS, RS, m, kk); },
+                [&](int n, int kk) { return quad<true>(v + n0 * RS, RS, n, kk); });
             float ds[2] = {0.f, 0.f}, ns[2] = {0.f, 0.f};
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt)
@@ -251,10 +250,10 @@ __global__ void __launch_bounds__(BwdCfg<D, ROWS>::THREADS) bwd_query(Args p) {
                         make_float2(s[nt][2 * h], s[nt][2 * h + 1]);
             __syncthreads();
             if (d0 < D)
-                gemm<2, 2, ND, false>(
+                gemm<2, 2, ND, 4>(
                     dq, 0, kB / 16,
-                    [&](int m, int kk) { return quad<true, false>(sDS + m0 * kTS, kTS, m, kk); },
-                    [&](int n, int kk) { return quad<false, false>(k + d0, RS, n, kk); });
+                    [&](int m, int kk) { return quad<true>(sDS + m0 * kTS, kTS, m, kk); },
+                    [&](int n, int kk) { return quad<false>(k + d0, RS, n, kk); });
         }
         cp_wait_all();
         __syncthreads();
@@ -309,12 +308,12 @@ __global__ void __launch_bounds__(BwdCfg<D, ROWS>::THREADS) bwd_key(Args p) {
         float s[2][4], dp[2][4];
         clear(s);
         clear(dp);
-        gemm<2, 2, 2, true>(
-            s, 0, D / 16, [&](int m, int kk) { return quad<true, true>(sK + m0 * RS, RS, m, kk); },
-            [&](int n, int kk) { return quad<true, true>(q + n0 * RS, RS, n, kk); });
-        gemm<2, 2, 2, true>(
-            dp, 0, D / 16, [&](int m, int kk) { return quad<true, true>(sV + m0 * RS, RS, m, kk); },
-            [&](int n, int kk) { return quad<true, true>(o + n0 * RS, RS, n, kk); });
+        gemm<2, 2, 2, 4>(
+            s, 0, D / 16, [&](int m, int kk) { return quad<true>(sK + m0 * RS, RS, m, kk); },
+            [&](int n, int kk) { return quad<true>(q + n0 * RS, RS, n, kk); });
+        gemm<2, 2, 2, 4>(
+            dp, 0, D / 16, [&](int m, int kk) { return quad<true>(sV + m0 * RS, RS, m, kk); },
+            [&](int n, int kk) { return quad<true>(o + n0 * RS, RS, n, kk); });
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
@@ -351,14 +350,14 @@ __global__ void __launch_bounds__(BwdCfg<D, ROWS>::THREADS) bwd_key(Args p) {
             }
         __syncthreads();
         if (d0 < D) {
-            gemm<2, 2, ND, false>(
+            gemm<2, 2, ND, 4>(
                 dk, 0, kB / 16,
-                [&](int m, int kk) { return quad<true, false>(sDS + m0 * kTS, kTS, m, kk); },
-                [&](int n, int kk) { return quad<false, false>(q + d0, RS, n, kk); });
-            gemm<2, 2, ND, false>(
+                [&](int m, int kk) { return quad<true>(sDS + m0 * kTS, kTS, m, kk); },
+                [&](int n, int kk) { return quad<false>(q + d0, RS, n, kk); });
+            gemm<2, 2, ND, 4>(
                 dv, 0, kB / 16,
-                [&](int m, int kk) { return quad<true, false>(sP + m0 * kTS, kTS, m, kk); },
-                [&](int n, int kk) { return quad<false, false>(o + d0, RS, n, kk); });
+                [&](int m, int kk) { return quad<true>(sP + m0 * kTS, kTS, m, kk); },
+                [&](int n, int kk) { return quad<false>(o + d0, RS, n, kk); });
         }
         cp_wait_all();
         __syncthreads();
