@@ -340,29 +340,11 @@ __global__ void __launch_bounds__(256) delta_prep(Args p, Scratch f, Scratch r) 
     const int nt_end = rb + 1;  // this warp's column tiles up to the diagonal block
     const bool wantQ = BACK || p.o;
     {
-        // K K^T and Q K^T together: they share their B operand
+        // K K^T and Q K^T
         float kk[4][4], qk[4][4];
         clear(kk);
         clear(qk);
-#pragma unroll 1
-        for (int ks = 0; ks < D / 16; ++ks) {
-            const int k = 16 * ks + t2;
-            FragA<TI> ak[1], aq[1];
-            ak[0].set(quad<true>(sK + m0 * KS, KS, gr, k), quad<true>(sK + m0 * KS, KS, gr + 8, k));
-            if (wantQ)
-                aq[0].set(quad<true>(sQ + m0 * KS, KS, gr, k),
-                       quad<true>(sQ + m0 * KS, KS, gr + 8, k));
-#pragma unroll
-            for (int nt = 0; nt < 4; nt += 2) {
-                if (nt >= nt_end) continue;
-                FragB<TI> b[1][2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e)  // beyond the diagonal block: computed, not used
-                    b[0][e].set(quad<true>(sK, KS, 8 * (2 * (nt + e) + hf) + gr, k));
-                mma_step<TI, TI, 2, 1>(*reinterpret_cast<float(*)[2][4]>(&kk[nt]), ak, b);
-                if (wantQ) mma_step<TI, TI, 2, 1>(*reinterpret_cast<float(*)[2][4]>(&qk[nt]), aq, b);
-            }
-        }
+        grams(kk, qk, wantQ, sK + m0 * KS, sQ + m0 * KS, sK, KS, 8 * hf, D / 16, nt_end);
         float4 *d = BACK ? nullptr
                          : reinterpret_cast<float4 *>(f.M + ch * (kC * kC)) + (size_t)rb * 8 * 32 + lane;
         const float gh[2] = {ghi[m0 + gr], ghi[m0 + gr + 8]}, gl[2] = {glo[m0 + gr], glo[m0 + gr + 8]};

@@ -129,16 +129,7 @@ __global__ void __launch_bounds__(256, D <= 64 ? 2 : 1) delta_grad(Args p, Grads
         float kk[4][4], qk[4][4];
         clear(kk);
         clear(qk);
-        // column 8 nt + g of the warp's tiles is column 16 nt + 8 hf + g of the product
-        auto kcol = [&](int n, int k) {
-            return quad<true>(sK, KS, 2 * (n & ~7) + 8 * hf + (n & 7), k);
-        };
-        gemm<TI, TI, 4>(
-            kk, 0, D / 16, [&](int m, int k) { return quad<true>(sK + m0 * KS, KS, m, k); }, kcol,
-            nt_end);
-        gemm<TI, TI, 4>(
-            qk, 0, D / 16, [&](int m, int k) { return quad<true>(sQ + m0 * KS, KS, m, k); }, kcol,
-            nt_end);
+        grams(kk, qk, true, sK + m0 * KS, sQ + m0 * KS, sK, KS, 8 * hf, D / 16, nt_end);
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt) {
             if (nt >= nt_end) continue;

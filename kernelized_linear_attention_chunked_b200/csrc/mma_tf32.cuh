@@ -200,6 +200,78 @@ __device__ __forceinline__ void gemm(float (&acc)[NT][4], int s0, int s1, FA fa,
     }
 }
 
+// Rows of shared memory times rows: kk += A B^T and (two) qk += A2 B^T over `steps`
+// sixteens of k; row block A, A2 of 16, and eight rows of B from 16 nt + b0 on per
+// tile nt < nt_end. Tiles go in pairs: of the last one a second may be computed in
+// vain.
+template <int NT>
+__device__ __forceinline__ void grams(float (&kk)[NT][4], float (&qk)[NT][4], bool two,
+                                      const float *A, const float *A2, const float *B, int stride,
+                                      int b0, int steps, int nt_end) {
+    const int g = (threadIdx.x & 31) >> 2, t2 = 2 * (threadIdx.x & 3);
+#pragma unroll 1
+    for (int st = 0; st < steps; ++st) {
+        const int k = 16 * st + t2;
+        FragA<2> a[1], a2[1];
+        a[0].set(quad<true>(A, stride, g, k), quad<true>(A, stride, g + 8, k));
+        if (two) a2[0].set(quad<true>(A2, stride, g, k), quad<true>(A2, stride, g + 8, k));
+#pragma unroll
+        for (int nt = 0; nt < NT; nt += 2) {
+            if (nt >= nt_end) continue;
+            FragB<2> b[1][2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) b[0][e].set(quad<true>(B, stride, 16 * (nt + e) + b0 + g, k));
+            mma_step<2, 2, 2, 1>(*reinterpret_cast<float(*)[2][4]>(&kk[nt]), a, b);
+            if (two) mma_step<2, 2, 2, 1>(*reinterpret_cast<float(*)[2][4]>(&qk[nt]), a2, b);
+        }
+    }
+}
+// Four 8 x 8 matrices of bf16; lanes 8 i .. 8 i + 7 name the rows of the i-th.
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], const __nv_bfloat16 *row) {
+    const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(row));
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
+}
+// The same of bf16: m16n8k16, whose products are exact as well, takes sixteen k in the
+// cycles of eight tf32 ones, and its operands need no unpacking.
+template <int NT>
+__device__ __forceinline__ void grams(float (&kk)[NT][4], float (&qk)[NT][4], bool two,
+                                      const __nv_bfloat16 *A, const __nv_bfloat16 *A2,
+                                      const __nv_bfloat16 *B, int stride, int b0, int steps,
+                                      int nt_end) {
+    const int lane = threadIdx.x & 31;
+    const int at = (lane & 15) * stride + 8 * (lane >> 4);  // rows, then the second eight k
+    const __nv_bfloat16 *bt = B + (b0 + (lane & 7) + 16 * (lane >> 4)) * stride + (lane & 8);
+    auto mma16 = [](float(&c)[4], const uint32_t(&a)[4], uint32_t y0, uint32_t y1) {
+        float t[4];
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+            "{%8,%9}, {%10,%10,%10,%10};"
+            : "=f"(t[0]), "=f"(t[1]), "=f"(t[2]), "=f"(t[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(y0), "r"(y1), "f"(0.f));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] += t[i];
+    };
+#pragma unroll 1
+    for (int st = 0; st < steps; ++st) {
+        uint32_t a[4], a2[4];
+        ldmatrix4(a, A + at + 16 * st);
+        if (two) ldmatrix4(a2, A2 + at + 16 * st);
+#pragma unroll
+        for (int nt = 0; nt < NT; nt += 2) {
+            if (nt >= nt_end) continue;
+            uint32_t b[4];
+            ldmatrix4(b, bt + 16 * nt * stride + 16 * st);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                mma16(kk[nt + e], a, b[2 * e], b[2 * e + 1]);
+                if (two) mma16(qk[nt + e], a2, b[2 * e], b[2 * e + 1]);
+            }
+        }
+    }
+}
+
 template <int NT>
 __device__ __forceinline__ void clear(float (&acc)[NT][4]) {
 #pragma unroll
