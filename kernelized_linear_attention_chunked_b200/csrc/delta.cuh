@@ -57,6 +57,7 @@ namespace delta {
 
 constexpr int kC = 64;    // tokens per chunk
 constexpr int kTS = 72;   // row stride of a 64 x 64 fp32 tile in shared memory
+constexpr int kAS = 68;   // of the one whose rows are read least
 constexpr int kCoef = 256;  // floats of coefficients per chunk: a' [64], c' [64], a_C
 constexpr float kMinLog = -200.f;
 constexpr int kLoaders = 128;     // threads of delta_chain that copy
@@ -168,8 +169,8 @@ __device__ __forceinline__ float2 decay2(float hi_i, float lo_i, const float *hi
     return make_float2(exp2f((hi_i - h.x) + (lo_i - l.x)), exp2f((hi_i - h.y) + (lo_i - l.y)));
 }
 
-// sX = (1 + A)^-1 for the strictly lower triangular A (64 x 64, both with row
-// stride kTS), by the CTA's first four warps. Diagonal 16 x 16 blocks by forward substitution,
+// sX = (1 + A)^-1 for the strictly lower triangular A (64 x 64, row
+// strides kTS and kAS), by the CTA's first four warps. Diagonal 16 x 16 blocks by forward substitution,
 // one column per lane; then the blocks below them, 16 to 32 to 64 rows, by
 //     X21 = -X22 (A21 X11),
 // where a warp's own columns need no other warp's. The blocks above the
@@ -179,14 +180,14 @@ __device__ __forceinline__ void invert(const float *sA, float *sX, int warp, int
     const int g = lane >> 2, t2 = 2 * (lane & 3);
     if (warp < 4) {
         const int j = lane & 15;
-        const float *A = sA + 16 * warp * kTS + 16 * warp;
+        const float *A = sA + 16 * warp * kAS + 16 * warp;
         float x[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[i] = i == j ? 1.f : 0.f;
 #pragma unroll
         for (int m = 0; m < 15; ++m)  // x[m] is final: take it out of the rows below
 #pragma unroll
-            for (int i = m + 1; i < 16; ++i) x[i] = fmaf(-A[i * kTS + m], x[m], x[i]);
+            for (int i = m + 1; i < 16; ++i) x[i] = fmaf(-A[i * kAS + m], x[m], x[i]);
         if (lane < 16) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) sX[(16 * warp + i) * kTS + 16 * warp + j] = x[i];
@@ -199,7 +200,7 @@ __device__ __forceinline__ void invert(const float *sA, float *sX, int warp, int
         clear(acc);
         gemm<2, 2, 1>(
             acc, 0, 1,
-            [&](int m, int k) { return quad<true>(sA + (r0 + 16) * kTS + r0, kTS, m, k); },
+            [&](int m, int k) { return quad<true>(sA + (r0 + 16) * kAS + r0, kAS, m, k); },
             [&](int n, int k) { return quad<false>(sX + r0 * kTS + c, kTS, n, k); });
         float *P = sX + r0 * kTS + c + 16;
         *reinterpret_cast<float2 *>(P + g * kTS + t2) = make_float2(acc[0][0], acc[0][1]);
@@ -219,12 +220,12 @@ __device__ __forceinline__ void invert(const float *sA, float *sX, int warp, int
         const int c = 8 * warp;
         float *P = sX + 32 + c;
         // rows m0 .. of A (32 columns) times a 32 x 8 B: both sixteens of k at once, or one
-        auto product = [&](float(&acc)[1][4], const float *A, const float *B, bool first, bool second) {
+        auto product = [&](float(&acc)[1][4], const float *A, int as, const float *B, bool first, bool second) {
             FragA<2> a[2];
             FragB<2> b[2][1];
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                a[s].set(quad<true>(A, kTS, g, 16 * s + t2), quad<true>(A, kTS, g + 8, 16 * s + t2));
+                a[s].set(quad<true>(A, as, g, 16 * s + t2), quad<true>(A, as, g + 8, 16 * s + t2));
                 float4 x = quad<false>(B, kTS, g, 16 * s + t2);
                 if (!(s ? second : first)) x = make_float4(0.f, 0.f, 0.f, 0.f);
                 b[s][0].set(x);
@@ -240,7 +241,7 @@ __device__ __forceinline__ void invert(const float *sA, float *sX, int warp, int
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {  // X11 has nothing above its diagonal blocks
             clear(acc[mt]);
-            product(acc[mt], sA + (32 + 16 * mt) * kTS, sX + c, warp < 2, true);
+            product(acc[mt], sA + (32 + 16 * mt) * kAS, kAS, sX + c, warp < 2, true);
         }
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) put(P + 16 * mt * kTS, acc[mt], 1.f);
@@ -250,7 +251,7 @@ __device__ __forceinline__ void invert(const float *sA, float *sX, int warp, int
             acc[0], 0, 1, [&](int m, int k) { return quad<true>(sX + 32 * kTS + 32, kTS, m, k); },
             [&](int n, int k) { return quad<false>(P, kTS, n, k); });
         clear(acc[1]);
-        product(acc[1], sX + 48 * kTS + 32, P, true, true);
+        product(acc[1], sX + 48 * kTS + 32, kTS, P, true, true);
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) put(sX + (32 + 16 * mt) * kTS + c, acc[mt], -1.f);
     }
@@ -262,11 +263,12 @@ struct PrepSmem {
     static constexpr int KS = row_stride<D>();
     static constexpr int IN = kC * KS * (int)sizeof(Tin);
     static constexpr int P = kC * KS * 4;  // BACK: diag(beta) M^T dO, over V
-    static constexpr int K = 0, Q = IN, V = 2 * IN, DO = V + (BACK ? P : IN);
-    static constexpr int A = DO + (BACK ? IN : 0);
-    static constexpr int X = A + kC * kTS * 4, M = X + kC * kTS * 4;
-    static constexpr int COEF = M + (BACK ? kC * kTS * 4 : 0);  // beta, a, beta c, G (hi, lo)
+    static constexpr int T = kC * kTS * 4, X = IN, Q = X;  // X over Q
+    static constexpr int K = 0, V = X + (IN > T ? IN : T), DO = V + (BACK ? P : IN);
+    static constexpr int A = DO + (BACK ? IN : 0), M = A + kC * kAS * 4;
+    static constexpr int COEF = M + (BACK ? T : 0);  // beta, a, beta c, G (hi, lo)
     static constexpr int BYTES = COEF + 5 * kC * 4;
+    static constexpr int CTAS = sizeof(Tin) == 2 && 4 * (BYTES + 1024) <= 228 * 1024 ? 4 : 1;
 };
 
 // Tiles first .. first + N - 1 of row block rb of a [64, D] matrix in fragment order.
@@ -283,7 +285,7 @@ __device__ __forceinline__ void store_frags(float *dst, const float (&acc)[N][4]
 // columns each, of a triangular product every other eight.
 // f: the forward chain's operands; r: the reverse chain's (BACK only).
 template <typename Tin, int D, bool BACK>
-__global__ void __launch_bounds__(256) delta_prep(Args p, Scratch f, Scratch r) {
+__global__ void __launch_bounds__(256, PrepSmem<Tin, D, BACK>::CTAS) delta_prep(Args p, Scratch f, Scratch r) {
     using namespace tf;
     using L = PrepSmem<Tin, D, BACK>;
     constexpr int KS = L::KS, TI = Parts<Tin>::N;
@@ -359,7 +361,7 @@ __global__ void __launch_bounds__(256) delta_prep(Args p, Scratch f, Scratch r) 
                 const int i = m0 + gr + 8 * h;
                 const float2 dec = decay2(gh[h], gl[h], ghi, glo, j);
                 // (above the diagonal a decay may be infinite: chosen away, not multiplied)
-                *reinterpret_cast<float2 *>(sA + i * kTS + j) =
+                *reinterpret_cast<float2 *>(sA + i * kAS + j) =
                     make_float2(i > j ? kk[nt][2 * h] * dec.x * be.x : 0.f,
                                 i > j + 1 ? kk[nt][2 * h + 1] * dec.y * be.y : 0.f);
                 m[2 * h] = i >= j ? qk[nt][2 * h] * dec.x : 0.f;
