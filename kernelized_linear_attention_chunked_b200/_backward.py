@@ -10,8 +10,8 @@ import ctypes as C
 import torch
 
 from . import _binding as kb
-from ._binding import KataError, _check, _dt, _ptr, _workspace
-from ._calls import bind, on_stream, want
+from ._binding import KataError, _check, _dt, _ptr
+from ._calls import bind, on_stream, want, workspace_for
 
 _vp, _i, _f, _sz = C.c_void_p, C.c_int, C.c_float, C.c_size_t
 
@@ -48,7 +48,8 @@ def prefill_backward(q, k, v, do, eps: float = 1e-6, workspace=None, stream=None
     with on_stream(q, stream) as s:
         dq, dk, dv = (torch.empty_like(q) for _ in range(3))
         if workspace is None:
-            workspace = _workspace(L.kata_prefill_backward_workspace_bytes(B, H, T, d, dt), q.device)
+            workspace = workspace_for(L, "kata_prefill_backward_workspace_bytes",
+                                      (B, H, T, d, dt), q)
         _check("kata_prefill_backward", L.kata_prefill_backward(
             _ptr(q), _ptr(k), _ptr(v), dt, B, H, T, d, eps, _ptr(do), _ptr(dq), _ptr(dk), _ptr(dv),
             _ptr(workspace), workspace.numel() * workspace.element_size(), s))

@@ -4,6 +4,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes as C
+import functools
 
 import torch
 
@@ -44,6 +45,18 @@ def want(name: str, t, shape, dtype, like: torch.Tensor) -> None:
                         f"{None if shape is None else tuple(shape)} {dtype} on {like.device}")
 
 
+@functools.lru_cache(maxsize=256)
+def _bytes(lib, query: str, *sizes) -> int:
+    return int(getattr(lib, query)(*sizes))
+
+
+def workspace_for(lib, query: str, sizes, like: torch.Tensor) -> torch.Tensor:
+    """A workspace of lib.query(*sizes) bytes beside the tensor `like` (that
+    gives its device and type: 1 us less than naming them)."""
+    item = like.element_size()
+    return like.new_empty(max(1, -(-_bytes(lib, query, *sizes) // item)))
+
+
 class on_stream:
     """Runs a call on t's device and on `stream` (default: that device's current
     one), and gives the stream's handle. What the call allocates inside belongs
@@ -56,7 +69,7 @@ class on_stream:
         self.inner = None
         if stream is not None and stream.device != t.device:
             raise KataError(f"stream of {stream.device}, tensors on {t.device}")
-        if stream is not None or self.dev != torch.cuda.current_device():
+        if stream is not None or self.dev != torch._C._cuda_getDevice():
             self.inner = contextlib.ExitStack()
             self.inner.enter_context(torch.cuda.device(self.dev))
             if stream is not None:

@@ -11,8 +11,8 @@ import ctypes as C
 import torch
 
 from . import _binding as kb
-from ._binding import KataError, _check, _dt, _ptr, _workspace
-from ._calls import bind, fits, on_stream, want
+from ._binding import KataError, _check, _dt, _ptr
+from ._calls import bind, fits, on_stream, want, workspace_for
 
 _vp, _i, _f, _sz = C.c_void_p, C.c_int, C.c_float, C.c_size_t
 
@@ -33,23 +33,36 @@ def lib() -> C.CDLL:
 
 
 def _inputs(q, k, v, g, beta, ndim):
+    """The tensors' type code and q's shape; raises unless they fit each other.
+    One expression for the ordinary case: a call for single tokens is bound by
+    the host."""
+    f32 = torch.float32
+    try:
+        shape, dtype, dev = q.shape, q.dtype, q.get_device()
+        rows = shape[:-1]
+        if (len(shape) == ndim and dev >= 0 and dtype in kb._DTYPE and q.is_contiguous()
+                and k.shape == shape and k.dtype is dtype and k.get_device() == dev
+                and k.is_contiguous() and v.shape == shape and v.dtype is dtype
+                and v.get_device() == dev and v.is_contiguous() and g.shape == rows
+                and g.dtype is f32 and g.get_device() == dev and g.is_contiguous()
+                and beta.shape == rows and beta.dtype is f32 and beta.get_device() == dev
+                and beta.is_contiguous()):
+            return kb._DTYPE[dtype], shape
+    except AttributeError:
+        pass
     for name, t in (("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta)):
         if t is None:
             raise KataError(f"{name} must not be None")
     if q.dim() != ndim:
         raise KataError(f"q has {q.dim()} dimensions, expected {ndim}")
     dt = _dt(q)
-    shape, dtype, dev = q.shape, q.dtype, q.get_device()
-    rows = shape[:-1]
-    if not (dev >= 0 and fits(q, shape, dtype, dev) and fits(k, shape, dtype, dev)
-            and fits(v, shape, dtype, dev) and fits(g, rows, torch.float32, dev)
-            and fits(beta, rows, torch.float32, dev)):
-        want("q", q, None, None, q)
-        want("k", k, shape, dtype, q)
-        want("v", v, shape, dtype, q)
-        want("g", g, rows, torch.float32, q)
-        want("beta", beta, rows, torch.float32, q)
-    return dt
+    rows = q.shape[:-1]
+    want("q", q, None, None, q)
+    want("k", k, q.shape, q.dtype, q)
+    want("v", v, q.shape, q.dtype, q)
+    want("g", g, rows, f32, q)
+    want("beta", beta, rows, f32, q)
+    return dt, q.shape
 
 
 def delta_prefill_workspace_bytes(B, H, T, d, dtype) -> int:
@@ -63,22 +76,26 @@ def delta_prefill(q, k, v, g, beta, scale: float | None = None, S_in=None, state
     (fp32, None: zero). ``scale`` defaults to d**-0.5. Returns (o, S): o in q's
     dtype, None when ``output`` is False; the last state, None when ``state``
     is False."""
-    dt = _inputs(q, k, v, g, beta, 4)
-    B, H, T, d = q.shape
+    dt, shape = _inputs(q, k, v, g, beta, 4)
+    B, H, T, d = shape
     st = (B, H, d, d)
-    want("S_in", S_in, st, torch.float32, q)
-    want("S_out", S_out, st, torch.float32, q)
-    want("o", o, q.shape, q.dtype, q)
-    want("workspace", workspace, None, None, q)
+    if S_in is not None:
+        want("S_in", S_in, st, torch.float32, q)
+    if S_out is not None:
+        want("S_out", S_out, st, torch.float32, q)
+    if o is not None:
+        want("o", o, shape, q.dtype, q)
+    if workspace is not None:
+        want("workspace", workspace, None, None, q)
     scale = d ** -0.5 if scale is None else scale
     L = lib()
     with on_stream(q, stream) as s:
         if output and o is None:
             o = torch.empty_like(q)
         if state and S_out is None:
-            S_out = torch.empty(st, dtype=torch.float32, device=q.device)
+            S_out = g.new_empty(st)
         if workspace is None:
-            workspace = _workspace(L.kata_delta_prefill_workspace_bytes(B, H, T, d, dt), q.device)
+            workspace = workspace_for(L, "kata_delta_prefill_workspace_bytes", (B, H, T, d, dt), g)
         _check("kata_delta_prefill", L.kata_delta_prefill(
             _ptr(q), _ptr(k), _ptr(v), dt, _ptr(g), _ptr(beta), B, H, T, d, scale, _ptr(S_in),
             _ptr(o), _ptr(S_out), _ptr(workspace), workspace.numel() * workspace.element_size(), s))
@@ -89,13 +106,14 @@ def delta_decode_step(q, k, v, g, beta, S, scale: float | None = None, o=None, s
     """One token of the gated delta rule: q, k, v [B, H, d], g and beta [B, H]
     (fp32), the state S [B, H, d, d] (fp32) updated in place. Returns o in q's
     dtype."""
-    dt = _inputs(q, k, v, g, beta, 3)
-    B, H, d = q.shape
+    dt, shape = _inputs(q, k, v, g, beta, 3)
+    B, H, d = shape
     if S is None:
         raise KataError("S must not be None")
     if not fits(S, (B, H, d, d), torch.float32, q.get_device()):
         want("S", S, (B, H, d, d), torch.float32, q)
-    want("o", o, q.shape, q.dtype, q)
+    if o is not None:
+        want("o", o, shape, q.dtype, q)
     scale = d ** -0.5 if scale is None else scale
     with on_stream(q, stream) as s:
         if o is None:
@@ -116,23 +134,26 @@ def delta_backward(q, k, v, g, beta, do, scale: float | None = None, S_in=None, 
     ``dS`` [B, H, d, d] (fp32, None: zero) of its last state. Returns (dq, dk,
     dv, dg, dbeta, dS_in): the first three in q's dtype, the rest fp32; dS_in,
     the gradient of the first state, is None unless ``state_grad``."""
-    dt = _inputs(q, k, v, g, beta, 4)
-    B, H, T, d = q.shape
+    dt, shape = _inputs(q, k, v, g, beta, 4)
+    B, H, T, d = shape
     st = (B, H, d, d)
     if do is None:
         raise KataError("do must not be None")
-    want("do", do, q.shape, q.dtype, q)
-    want("S_in", S_in, st, torch.float32, q)
-    want("dS", dS, st, torch.float32, q)
-    want("workspace", workspace, None, None, q)
+    want("do", do, shape, q.dtype, q)
+    if S_in is not None:
+        want("S_in", S_in, st, torch.float32, q)
+    if dS is not None:
+        want("dS", dS, st, torch.float32, q)
+    if workspace is not None:
+        want("workspace", workspace, None, None, q)
     scale = d ** -0.5 if scale is None else scale
     L = lib()
     with on_stream(q, stream) as s:
         dq, dk, dv = (torch.empty_like(q) for _ in range(3))
         dg, db = torch.empty_like(g), torch.empty_like(beta)
-        dS_in = torch.empty(st, dtype=torch.float32, device=q.device) if state_grad else None
+        dS_in = g.new_empty(st) if state_grad else None
         if workspace is None:
-            workspace = _workspace(L.kata_delta_backward_workspace_bytes(B, H, T, d, dt), q.device)
+            workspace = workspace_for(L, "kata_delta_backward_workspace_bytes", (B, H, T, d, dt), g)
         _check("kata_delta_backward", L.kata_delta_backward(
             _ptr(q), _ptr(k), _ptr(v), dt, _ptr(g), _ptr(beta), B, H, T, d, scale, _ptr(S_in),
             _ptr(do), _ptr(dS), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), _ptr(db), _ptr(dS_in),
