@@ -281,6 +281,19 @@ __device__ __forceinline__ void store_frags(float *dst, const float (&acc)[N][4]
         d[nt * 32] = make_float4(acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]);
 }
 
+// The same, each 16 x 8 tile transposed: a lane's four values are rows 2t, 2t + 1, 2t + 8,
+// 2t + 9 of column g.
+template <int D, int N>
+__device__ __forceinline__ void store_frags_t(float *dst, const float (&acc)[N][4], int rb, int first,
+                                              int lane) {
+    float4 *d = reinterpret_cast<float4 *>(dst) + (size_t)(rb * (D / 8) + first) * 32 + lane;
+#pragma unroll
+    for (int nt = 0; nt < N; ++nt) {
+        const float2 a = tf::transpose8(acc[nt][0], acc[nt][1]), b = tf::transpose8(acc[nt][2], acc[nt][3]);
+        d[nt * 32] = make_float4(a.x, a.y, b.x, b.y);
+    }
+}
+
 // What each chunk needs of itself alone. 8 warps: 16 rows (warp % 4) and half the
 // columns each, of a triangular product every other eight.
 // f: the forward chain's operands; r: the reverse chain's (BACK only).
@@ -384,7 +397,7 @@ __global__ void __launch_bounds__(256, PrepSmem<Tin, D, BACK>::CTAS) delta_prep(
     gemm<2, TI, ND>(  // X V
         acc, 0, rb + 1, [&](int m, int k) { return quad<true>(sX + m0 * kTS, kTS, m, k); },
         [&](int n, int k) { return quad<false>(sV + d0, KS, n, k); });
-    store_frags<D>(f.Y + ch * (kC * D), acc, rb, td, lane);
+    store_frags_t<D>(f.Y + ch * (kC * D), acc, rb, td, lane);
     auto kcols = [&](int n, int k) { return quad<false>(sK + d0, KS, n, k); };
     clear(acc);
     gemm<2, TI, ND>(  // X diag(a) K
@@ -417,7 +430,7 @@ __global__ void __launch_bounds__(256, PrepSmem<Tin, D, BACK>::CTAS) delta_prep(
     gemm<2, 2, ND>(
         acc, rb, 4, [&](int m, int k) { return quad<false>(sX + m0, kTS, m, k); },
         [&](int n, int k) { return quad<false>(sP + d0, KS, n, k); });
-    store_frags<D>(r.Y + ch * (kC * D), acc, rb, td, lane);
+    store_frags_t<D>(r.Y + ch * (kC * D), acc, rb, td, lane);
     clear(acc);
     gemm<2, TI, ND>(
         acc, rb, 4,
@@ -428,15 +441,18 @@ __global__ void __launch_bounds__(256, PrepSmem<Tin, D, BACK>::CTAS) delta_prep(
     store_frags<D>(r.W + ch * (kC * D), acc, rb, td, lane);
 }
 
-template <typename Tin, int D, int NS, bool REV>
+constexpr int kSlice = 16;  // value columns per CTA: the rows of one operand tile
+
+template <typename Tin, int D, bool REV>
 struct ChainSmem {
     static constexpr int KS = row_stride<D>();
-    static constexpr int ST = NS + 4;  // row stride of B operands: rows 2t start 8t banks on
-    static constexpr int DS = NS + 8;  // row stride of the dO slice
+    static constexpr int DS = kSlice + 8;  // row stride of the dO slice
     static constexpr int IN = kC * KS * (int)sizeof(Tin);
-    static constexpr int S = 0, YC = S + D * ST * 4, Y = YC + kC * ST * 4;
-    static constexpr int GQ = Y + kC * ST * 4;  // REV: Q^T diag(scale a) dO
-    static constexpr int STAGE = GQ + (REV ? D * ST * 4 : 0);
+    static constexpr int FRAG = 1024;      // one part of a 16 x 16 A operand
+    static constexpr int S = 0, YC = S + D / 16 * 2 * FRAG, SIDE = YC + kC / 16 * 2 * FRAG;
+    // what passes between the chain and the side warps: E or (REV) Q^T diag(scale a) dO
+    static constexpr int STAGE =
+        SIDE + (REV ? D / 16 * FRAG : kC / 16 * tf::Parts<Tin>::N * FRAG);
     // one stage: K, Q, coefficients, (REV) the dO slice
     static constexpr int K = 0, Q = IN, COEF = 2 * IN, DO = COEF + kCoef * 4;
     static constexpr int STAGE_BYTES = DO + (REV ? kC * DS * (int)sizeof(Tin) : 0);
@@ -447,33 +463,38 @@ struct ChainSmem {
     static constexpr int BYTES = STAGE + STAGES * STAGE_BYTES;
 };
 
-// The walk over the chunks, one CTA per (head, NS value columns): `cta` of them. Warps 0-3
-// carry the chain: they hold the state in registers (fp32, D / 4 rows each)
-// and take two dependent products per chunk. Warps 4-7 take the products that
+// The walk over the chunks, one CTA per (head, 16 value columns): `cta` of them. Everything
+// is transposed, so that the 16 value columns are the rows of the products,
+//     E^T = XV^T - S0^T W^T,  S_C^T = a_C S0^T + (c beta E)^T K,
+//     O^T = scale S0^T Q^T diag(a) + E^T M^T,
+// and an accumulator is, register for register, the A operand of the product that
+// follows. The warp that makes one cuts it into tf32 parts and leaves it in that order
+// for the others: eight 128-bit reads where the plain form took 32 scalar ones and cut
+// them four times over (341 -> REPLACE1 us at B2 H16 T16384 d64, 33 -> REPLACE2 us at
+// B4 H8 T2048 d32).
+// Warps 0-3 carry the chain: they hold the state in registers (fp32, D / 4 of its rows
+// each) and take two dependent products per chunk. Warps 4-7 take the products that
 // hang off it: the outputs (forward) or Q^T dO (REV). Warps 8-11 bring K, Q and
-// the coefficients by asynchronous copies up to three chunks ahead, and calls
+// the coefficients by asynchronous copies up to three chunks ahead, and call
 // the next chunks' W, XV and M into L2; those come straight from there into
-// the fragments that use them, one chunk ahead. The state and the errors pass
-// between the warps as fp32 and are cut into tf32 parts by each reader: shared
-// memory's bandwidth is what the walk runs out of, not its instructions (cut by
-// the writer, as pairs, the walk took 348 us instead of 339 us at B2 H16 T16384
-// d64).
-template <typename Tin, int D, int NS, bool REV, bool KEEP>
+// the fragments that use them, one chunk ahead.
+template <typename Tin, int D, bool REV, bool KEEP>
 __device__ __forceinline__ void walk_chunks(const Args &p, const Scratch &w, const unsigned cta) {
     using namespace tf;
-    using L = ChainSmem<Tin, D, NS, REV>;
-    constexpr int KS = L::KS, ST = L::ST, NT = NS / 8, TI = Parts<Tin>::N;
-    constexpr int MT = D >= 64 ? D / 64 : 1;  // 16-row tiles of the state per chain warp
+    using L = ChainSmem<Tin, D, REV>;
+    constexpr int KS = L::KS, TI = Parts<Tin>::N;
+    constexpr int MT = D >= 64 ? D / 64 : 1;  // sixteens of the state's rows per chain warp
     constexpr int KP = D >= 32 ? 2 : 1;       // sixteens of k at a time
     extern __shared__ __align__(16) uint8_t sm[];
-    float *sS = reinterpret_cast<float *>(sm + L::S), *sYc = reinterpret_cast<float *>(sm + L::YC);
-    float *sY = reinterpret_cast<float *>(sm + L::Y), *sG = reinterpret_cast<float *>(sm + L::GQ);
+    uint4 *sS = reinterpret_cast<uint4 *>(sm + L::S), *sYc = reinterpret_cast<uint4 *>(sm + L::YC);
+    uint4 *sE = reinterpret_cast<uint4 *>(sm + L::SIDE);
+    float4 *sG = reinterpret_cast<float4 *>(sm + L::SIDE);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int gr = lane >> 2, t2 = 2 * (lane & 3);
-    const size_t head = cta / (D / NS);
-    const int slice = cta % (D / NS), c0 = slice * NS;
+    const int gr = lane >> 2, t2 = 2 * (lane & 3), rw = warp & 3;
+    const size_t head = cta / (D / kSlice);
+    const int slice = cta % (D / kSlice), c0 = slice * kSlice;
     const size_t row0 = head * (size_t)p.T;
-    const int m0 = 16 * (warp & 3);
+    const int m0 = 16 * rw;
     const bool wantO = !REV && p.o != nullptr;
     const size_t ch0 = head * p.nc;
     auto chunk_of = [&](int i) { return REV ? p.nc - 1 - i : i; };
@@ -492,9 +513,9 @@ __device__ __forceinline__ void walk_chunks(const Args &p, const Scratch &w, con
                                                 static_cast<const Tin *>(p.q), row0, c * kC, p.T, D, 0,
                                                 lt);
                 if (REV)
-                    load_tile<Tin, NS, kLoaders>(reinterpret_cast<Tin *>(s + L::DO), L::DS,
-                                                 static_cast<const Tin *>(p.d_o), row0, c * kC, p.T, D,
-                                                 c0, lt);
+                    load_tile<Tin, kSlice, kLoaders>(reinterpret_cast<Tin *>(s + L::DO), L::DS,
+                                                     static_cast<const Tin *>(p.d_o), row0, c * kC, p.T,
+                                                     D, c0, lt);
                 const float *cf = w.coef + (ch0 + c) * kCoef;
                 if (lt < kCoef / 4) cp16(s + L::COEF + lt * 16, cf + lt * 4, true);
                 if (slice == 0 && lt == kLoaders - 1) {
@@ -518,44 +539,50 @@ __device__ __forceinline__ void walk_chunks(const Args &p, const Scratch &w, con
     }
 
     const bool chain = warp < 4;
-    // the state in accumulator layout: rows 16 (MT warp + mt) + gr (+ 8), columns 8 nt + t2 (+ 1)
-    float S[MT][NT][4];
+    // The state, transposed, in accumulator layout: value columns c0 + gr (+ 8 for e = 2, 3),
+    // rows srow(mt, nt) (+ 1 for e = 1, 3). An accumulator pair as quads: rows gr, gr + 8.
+    float S[MT][2][4];
     const bool owns = chain && (D >= 64 || warp < D / 16);
-    auto srow = [&](int mt) { return 16 * (MT * warp + mt) + gr; };
+    auto srow = [&](int mt, int nt) { return 16 * (MT * warp + mt) + 8 * nt + t2; };
+    auto top = [](const float(&x)[2][4]) { return make_float4(x[0][0], x[0][1], x[1][0], x[1][1]); };
+    auto bottom = [](const float(&x)[2][4]) { return make_float4(x[0][2], x[0][3], x[1][2], x[1][3]); };
+    auto put_state = [&]() {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            FragA<2> f;
+            f.set(top(S[mt]), bottom(S[mt]));
+            put_frag(sS + (MT * warp + mt) * 128 + lane, f);
+        }
+    };
     if (owns) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float2 x = make_float2(0.f, 0.f);
-                    const int r = srow(mt) + 8 * h;
-                    if (p.S_in)
-                        x = *reinterpret_cast<const float2 *>(p.S_in + (head * D + r) * D + c0 +
-                                                              8 * nt + t2);
-                    S[mt][nt][2 * h] = x.x;
-                    S[mt][nt][2 * h + 1] = x.y;
-                    *reinterpret_cast<float2 *>(sS + r * ST + 8 * nt + t2) = x;
-                }
+                for (int e = 0; e < 4; ++e)
+                    S[mt][nt][e] = p.S_in ? p.S_in[(head * D + srow(mt, nt) + (e & 1)) * D + c0 + gr +
+                                                   8 * (e >> 1)]
+                                          : 0.f;
+        put_state();
     }
     // the next chunk's W and XV (chain) or M (outputs), as fragments
     constexpr int NW = D / 8 > 8 ? D / 8 : 8;
-    float4 W[NW], Y0[NT];
+    float4 W[NW], Y0[2];
     const ptrdiff_t dir = REV ? -1 : 1;
     const float4 *wp = reinterpret_cast<const float4 *>(w.W + (ch0 + chunk_of(0)) * (kC * D)) +
-                       (size_t)(warp & 3) * (D / 8) * 32 + lane;
+                       (size_t)rw * (D / 8) * 32 + lane;
     const float4 *yp = reinterpret_cast<const float4 *>(w.Y + (ch0 + chunk_of(0)) * (kC * D)) +
-                       (size_t)((warp & 3) * (D / 8) + slice * NT) * 32 + lane;
+                       (size_t)(rw * (D / 8) + slice * 2) * 32 + lane;
     const float4 *mp = reinterpret_cast<const float4 *>(w.M + (ch0 + chunk_of(0)) * (kC * kC)) +
-                       (size_t)(warp & 3) * 8 * 32 + lane;
-    const int kts = 2 * ((warp & 3) + 1);  // eights of M's columns up to the diagonal block
+                       (size_t)rw * 8 * 32 + lane;
+    const int kts = 2 * (rw + 1);  // eights of M's columns up to the diagonal block
     auto load_frags = [&]() {
         if (chain) {
 #pragma unroll
             for (int kt = 0; kt < D / 8; ++kt) W[kt] = wp[kt * 32];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) Y0[nt] = yp[nt * 32];
+            for (int h = 0; h < 2; ++h) Y0[h] = yp[h * 32];
             wp += dir * (kC * D / 4);
             yp += dir * (kC * D / 4);
         } else if (wantO) {
@@ -575,84 +602,96 @@ __device__ __forceinline__ void walk_chunks(const Args &p, const Scratch &w, con
         const Tin *sQ = reinterpret_cast<const Tin *>(st + L::Q);
         const Tin *sO = reinterpret_cast<const Tin *>(st + L::DO);
         const float *coef = reinterpret_cast<const float *>(st + L::COEF);
-        float o[NT][4];
-        // W's or M's columns 16 ks .. as an A operand
-        auto frag_a = [&](auto &a, int ks) {
+        float o[2][4];
+        // sixteen of k of W's or M's 16 rows as B operands
+        auto frag_w = [&](auto &b, int ks) {
             const float4 w0 = W[2 * ks], w1 = W[2 * ks + 1];
-            a.set(make_float4(w0.x, w0.y, w1.x, w1.y), make_float4(w0.z, w0.w, w1.z, w1.w));
+            b[0].set(make_float4(w0.x, w0.y, w1.x, w1.y));
+            b[1].set(make_float4(w0.z, w0.w, w1.z, w1.w));
         };
-        // a column's four k of the state or the errors
-        auto column = [&](const float *x, int n, int k) { return quad<false>(x, ST, n, k); };
         if (chain) {
             // E = XV - W S0 (REV: Z = Z0 + W' dS)
-            float acc[NT][4];
+            float acc[2][4];
             clear(acc);
 #pragma unroll
             for (int k0 = 0; k0 < D / 16; k0 += KP) {
                 FragA<2> a[KP];
-                FragB<2> b[KP][NT];
+                FragB<2> b[KP][2];
 #pragma unroll
                 for (int s = 0; s < KP; ++s) {
-                    frag_a(a[s], k0 + s);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        b[s][nt].set(column(sS, 8 * nt + gr, 16 * (k0 + s) + t2));
+                    get_frag(a[s], sS + (k0 + s) * 128 + lane);
+                    frag_w(b[s], k0 + s);
                 }
-                mma_step<2, 2, NT, KP>(acc, a, b);
+                mma_step<2, 2, 2, KP>(acc, a, b);
             }
-            const float k0 = coef[kC + m0 + gr], k1 = coef[kC + m0 + gr + 8];
+            const float2 c0_ = *reinterpret_cast<const float2 *>(coef + kC + m0 + t2);
+            const float2 c1_ = *reinterpret_cast<const float2 *>(coef + kC + m0 + t2 + 8);
+            float4 y[2] = {top(acc), bottom(acc)};
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
+            for (int h = 0; h < 2; ++h) {
                 const float sg = REV ? 1.f : -1.f;
-                const float2 y0 = make_float2(fmaf(sg, acc[nt][0], Y0[nt].x),
-                                              fmaf(sg, acc[nt][1], Y0[nt].y));
-                const float2 y1 = make_float2(fmaf(sg, acc[nt][2], Y0[nt].z),
-                                              fmaf(sg, acc[nt][3], Y0[nt].w));
-                const int n = 8 * nt + t2;
-                *reinterpret_cast<float2 *>(sYc + (m0 + gr) * ST + n) =
-                    make_float2(k0 * y0.x, k0 * y0.y);
-                *reinterpret_cast<float2 *>(sYc + (m0 + gr + 8) * ST + n) =
-                    make_float2(k1 * y1.x, k1 * y1.y);
-                if (wantO) {
-                    *reinterpret_cast<float2 *>(sY + (m0 + gr) * ST + n) = y0;
-                    *reinterpret_cast<float2 *>(sY + (m0 + gr + 8) * ST + n) = y1;
-                }
-                if (KEEP) {
-                    float *d = p.keepY + ((ch0 + c) * kC + m0 + gr) * D + c0 + n;
-                    *reinterpret_cast<float2 *>(d) = y0;
-                    *reinterpret_cast<float2 *>(d + 8 * D) = y1;
+                y[h] = make_float4(fmaf(sg, y[h].x, Y0[h].x), fmaf(sg, y[h].y, Y0[h].y),
+                                   fmaf(sg, y[h].z, Y0[h].z), fmaf(sg, y[h].w, Y0[h].w));
+            }
+            auto times = [&](float4 x) {
+                return make_float4(c0_.x * x.x, c0_.y * x.y, c1_.x * x.z, c1_.y * x.w);
+            };
+            FragA<2> f;
+            f.set(times(y[0]), times(y[1]));
+            put_frag(sYc + rw * 128 + lane, f);
+            if (wantO) {
+                FragA<TI> e;
+                e.set(y[0], y[1]);
+                put_frag(sE + rw * (64 * TI) + lane, e);
+            }
+            if (KEEP) {
+                float *d = p.keepY + ((ch0 + c) * kC + m0 + t2) * D + c0 + gr;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    d[8 * h] = y[h].x;
+                    d[D + 8 * h] = y[h].y;
+                    d[8 * D + 8 * h] = y[h].z;
+                    d[9 * D + 8 * h] = y[h].w;
                 }
             }
             if (i + 1 < p.nc) load_frags();
         } else if (wantO) {
             clear(o);
-            gemm<TI, TI, NT>(
-                o, 0, D / 16, [&](int m, int k) { return quad<true>(sQ + m0 * KS, KS, m, k); },
-                [&](int n, int k) { return column(sS, n, k); });
-            const float s0 = coef[m0 + gr], s1 = coef[m0 + gr + 8];
+#pragma unroll 1
+            for (int ks = 0; ks < D / 16; ++ks) {
+                FragA<TI> a[1];
+                FragB<TI> b[1][2];
+                get_frag(a[0], sS + ks * 128 + lane);
+                const Quads x = quads<true>(sQ + m0 * KS, KS, 16 * ks);
+                b[0][0].set(x.a);
+                b[0][1].set(x.b);
+                mma_step<TI, TI, 2, 1>(o, a, b);
+            }
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                o[nt][0] *= s0;
-                o[nt][1] *= s0;
-                o[nt][2] *= s1;
-                o[nt][3] *= s1;
+            for (int nt = 0; nt < 2; ++nt) {
+                const float2 s = *reinterpret_cast<const float2 *>(coef + m0 + 8 * nt + t2);
+                o[nt][0] *= s.x;
+                o[nt][1] *= s.y;
+                o[nt][2] *= s.x;
+                o[nt][3] *= s.y;
             }
         } else if (REV) {
-            for (int mt = warp & 3; mt < D / 16; mt += 4) {
-                float acc[NT][4];
+            for (int ms = rw; ms < D / 16; ms += 4) {
+                float acc[2][4];
                 clear(acc);
-                gemm<TI, 2, NT>(
-                    acc, 0, kC / 16,
-                    [&](int m, int k) { return quad<false>(sQ + 16 * mt, KS, m, k); },
-                    [&](int n, int k) {
-                        return scaled(quad<false>(sO, L::DS, n, k), coef, k);
-                    });
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float *d = sG + (16 * mt + gr) * ST + 8 * nt + t2;
-                    *reinterpret_cast<float2 *>(d) = make_float2(acc[nt][0], acc[nt][1]);
-                    *reinterpret_cast<float2 *>(d + 8 * ST) = make_float2(acc[nt][2], acc[nt][3]);
+#pragma unroll 1
+                for (int ks = 0; ks < kC / 16; ++ks) {
+                    FragA<2> a[1];
+                    FragB<TI> b[1][2];
+                    const Quads x = quads<false>(sO, L::DS, 16 * ks);
+                    a[0].set(scaled(x.a, coef, 16 * ks + t2), scaled(x.b, coef, 16 * ks + t2));
+                    const Quads y = quads<false>(sQ + 16 * ms, KS, 16 * ks);
+                    b[0][0].set(y.a);
+                    b[0][1].set(y.b);
+                    mma_step<2, TI, 2, 1>(acc, a, b);
                 }
+                sG[ms * 64 + lane] = top(acc);
+                sG[ms * 64 + 32 + lane] = bottom(acc);
             }
         }
         __syncthreads();
@@ -660,77 +699,74 @@ __device__ __forceinline__ void walk_chunks(const Args &p, const Scratch &w, con
             // S = a_C S + K^T (c' Y) (REV: + Q^T dO): the chunk's share is summed
             // by itself, then added, so that rounding does not grow with the chunks
             const float aC = coef[2 * kC];
-            float acc[MT][NT][4];
+            float acc[MT][2][4];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) clear(acc[mt]);
 #pragma unroll
             for (int k0 = 0; k0 < kC / 16; k0 += 2) {
-                FragB<2> b[2][NT];
+                FragA<2> a[2];
 #pragma unroll
-                for (int s = 0; s < 2; ++s)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        b[s][nt].set(column(sYc, 8 * nt + gr, 16 * (k0 + s) + t2));
+                for (int s = 0; s < 2; ++s) get_frag(a[s], sYc + (k0 + s) * 128 + lane);
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
-                    FragA<TI> a[2];
-                    const Tin *ka = sK + 16 * (MT * warp + mt);
+                    FragB<TI> b[2][2];
 #pragma unroll
-                    for (int s = 0; s < 2; ++s)
-                        a[s].set(quad<false>(ka, KS, gr, 16 * (k0 + s) + t2),
-                                 quad<false>(ka, KS, gr + 8, 16 * (k0 + s) + t2));
-                    mma_step<TI, 2, NT, 2>(acc[mt], a, b);
+                    for (int s = 0; s < 2; ++s) {
+                        const Quads x = quads<false>(sK + 16 * (MT * warp + mt), KS, 16 * (k0 + s));
+                        b[s][0].set(x.a);
+                        b[s][1].set(x.b);
+                    }
+                    mma_step<2, TI, 2, 2>(acc[mt], a, b);
                 }
             }
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int mt = 0; mt < MT; ++mt) {
+                if (KEEP) {  // the state before this chunk
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const int n = 8 * nt + t2;
-                    if (KEEP) {  // the state before this chunk
-                        float *d = p.keepS + ((ch0 + c) * D + srow(mt)) * D + c0 + n;
-                        *reinterpret_cast<float2 *>(d) = make_float2(S[mt][nt][0], S[mt][nt][1]);
-                        *reinterpret_cast<float2 *>(d + 8 * D) =
-                            make_float2(S[mt][nt][2], S[mt][nt][3]);
-                    }
+                    for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float x = fmaf(aC, S[mt][nt][e], acc[mt][nt][e]);
-                        if (REV) x += sG[(srow(mt) + (e & 2 ? 8 : 0)) * ST + n + (e & 1)];
-                        S[mt][nt][e] = x;
-                    }
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        *reinterpret_cast<float2 *>(sS + (srow(mt) + 8 * h) * ST + n) =
-                            make_float2(S[mt][nt][2 * h], S[mt][nt][2 * h + 1]);
+                        for (int e = 0; e < 4; ++e)
+                            p.keepS[((ch0 + c) * D + srow(mt, nt) + (e & 1)) * D + c0 + gr +
+                                    8 * (e >> 1)] = S[mt][nt][e];
                 }
-        } else if (!chain && wantO) {
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) S[mt][nt][e] = fmaf(aC, S[mt][nt][e], acc[mt][nt][e]);
+                if (REV) {
+                    const float4 *d = sG + (MT * warp + mt) * 64 + lane;
+                    const float4 g0 = d[0], g1 = d[32];
+                    S[mt][0][0] += g0.x, S[mt][0][1] += g0.y, S[mt][1][0] += g0.z, S[mt][1][1] += g0.w;
+                    S[mt][0][2] += g1.x, S[mt][0][3] += g1.y, S[mt][1][2] += g1.z, S[mt][1][3] += g1.w;
+                }
+            }
+            put_state();
+        } else if (wantO && !chain) {
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
-                if (ks > (warp & 3)) continue;
+                if (ks > rw) continue;
                 FragA<TI> a[1];
-                frag_a(a[0], ks);
-                FragB<TI> b[1][NT];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    b[0][nt].set(column(sY, 8 * nt + gr, 16 * ks + t2));
-                mma_step<TI, TI, NT, 1>(o, a, b);
+                FragB<TI> b[1][2];
+                get_frag(a[0], sE + ks * (64 * TI) + lane);
+                frag_w(b[0], ks);
+                mma_step<TI, TI, 2, 1>(o, a, b);
             }
             if (i + 1 < p.nc) load_frags();
             Tin *od = static_cast<Tin *>(p.o);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int t = c * kC + m0 + gr + 8 * h;
-                if (t >= p.T) continue;
+            for (int nt = 0; nt < 2; ++nt) {
+                const int t = c * kC + m0 + 8 * nt + gr;
                 Tin *d = od + (row0 + t) * (size_t)D + c0 + t2;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    if constexpr (sizeof(Tin) == 2)
-                        *reinterpret_cast<__nv_bfloat162 *>(d + 8 * nt) =
-                            __floats2bfloat162_rn(o[nt][2 * h], o[nt][2 * h + 1]);
-                    else
-                        *reinterpret_cast<float2 *>(d + 8 * nt) =
-                            make_float2(o[nt][2 * h], o[nt][2 * h + 1]);
+                for (int h = 0; h < 2; ++h) {
+                    if constexpr (sizeof(Tin) == 2) {
+                        const __nv_bfloat162 x = __floats2bfloat162_rn(o[nt][2 * h], o[nt][2 * h + 1]);
+                        const uint32_t y = transpose8(*reinterpret_cast<const uint32_t *>(&x));
+                        if (t < p.T) *reinterpret_cast<uint32_t *>(d + 8 * h) = y;
+                    } else {
+                        const float2 y = transpose8(o[nt][2 * h], o[nt][2 * h + 1]);
+                        if (t < p.T) *reinterpret_cast<float2 *>(d + 8 * h) = y;
+                    }
                 }
             }
         }
@@ -740,20 +776,18 @@ __device__ __forceinline__ void walk_chunks(const Args &p, const Scratch &w, con
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float *d = p.S_out + (head * D + srow(mt)) * D + c0 + 8 * nt + t2;
-                *reinterpret_cast<float2 *>(d) = make_float2(S[mt][nt][0], S[mt][nt][1]);
-                *reinterpret_cast<float2 *>(d + 8 * D) = make_float2(S[mt][nt][2], S[mt][nt][3]);
-            }
+            for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    p.S_out[(head * D + srow(mt, nt) + (e & 1)) * D + c0 + gr + 8 * (e >> 1)] =
+                        S[mt][nt][e];
     }
 }
-
-constexpr int kSlice = 16;  // value columns per CTA
 
 template <typename Tin, int D>
 __global__ void __launch_bounds__(kChainThreads, 1) delta_chain(Args p, Scratch w) {
     sm100::grid_dependency_wait();  // delta_prep
-    walk_chunks<Tin, D, kSlice, false, false>(p, w, blockIdx.x);
+    walk_chunks<Tin, D, false, false>(p, w, blockIdx.x);
 }
 
 // The gradients' two walks in one launch, the longer one's CTAs first: neither
@@ -766,9 +800,9 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     sm100::grid_dependency_wait();  // delta_prep
     if (threadIdx.x == 0) sm100::launch_dependents();
     if (blockIdx.x < half)
-        walk_chunks<Tin, D, kSlice, true, true>(back, wb, blockIdx.x);
+        walk_chunks<Tin, D, true, true>(back, wb, blockIdx.x);
     else
-        walk_chunks<Tin, D, kSlice, false, true>(forth, wf, blockIdx.x - half);
+        walk_chunks<Tin, D, false, true>(forth, wf, blockIdx.x - half);
 }
 
 template <typename Tin, int D, bool BACK>
@@ -784,7 +818,7 @@ cudaError_t launch_prep(const Args &p, const Scratch &f, const Scratch &r, long 
 
 template <typename Tin, int D>
 cudaError_t launch_chain(const Args &p, const Scratch &w, long heads, cudaStream_t stream) {
-    constexpr int bytes = ChainSmem<Tin, D, kSlice, false>::BYTES;
+    constexpr int bytes = ChainSmem<Tin, D, false>::BYTES;
     static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
     cudaError_t e = tc::set_smem_once<delta_chain<Tin, D>>(bytes);
     if (e != cudaSuccess) return e;
@@ -796,8 +830,8 @@ cudaError_t launch_chain(const Args &p, const Scratch &w, long heads, cudaStream
 template <typename Tin, int D>
 cudaError_t launch_walks(const Args &back, const Scratch &wb, const Args &forth, const Scratch &wf,
                          long heads, cudaStream_t stream) {
-    constexpr int b0 = ChainSmem<Tin, D, kSlice, true>::BYTES;
-    constexpr int b1 = ChainSmem<Tin, D, kSlice, false>::BYTES, bytes = b0 > b1 ? b0 : b1;
+    constexpr int b0 = ChainSmem<Tin, D, true>::BYTES;
+    constexpr int b1 = ChainSmem<Tin, D, false>::BYTES, bytes = b0 > b1 ? b0 : b1;
     static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
     cudaError_t e = tc::set_smem_once<delta_walks<Tin, D>>(bytes);
     if (e != cudaSuccess) return e;

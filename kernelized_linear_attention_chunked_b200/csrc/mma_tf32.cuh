@@ -77,6 +77,29 @@ struct FragA {
     }
 };
 
+// An A operand that is kept cut, in the order of its registers: 2 TA rows of 32 lanes x
+// uint4 (conflict-free, and its readers do not cut it again).
+template <int TA>
+__device__ __forceinline__ void put_frag(uint4 *p, const FragA<TA> &f) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        p[32 * h] = make_uint4(f.hi[h][0], f.hi[h][1], f.hi[h][2], f.hi[h][3]);
+        if (TA == 2) p[64 + 32 * h] = make_uint4(f.lo[h][0], f.lo[h][1], f.lo[h][2], f.lo[h][3]);
+    }
+}
+template <int TA>
+__device__ __forceinline__ void get_frag(FragA<TA> &f, const uint4 *p) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint4 u = p[32 * h];
+        f.hi[h][0] = u.x, f.hi[h][1] = u.y, f.hi[h][2] = u.z, f.hi[h][3] = u.w;
+        if (TA == 2) {
+            const uint4 l = p[64 + 32 * h];
+            f.lo[h][0] = l.x, f.lo[h][1] = l.y, f.lo[h][2] = l.z, f.lo[h][3] = l.w;
+        }
+    }
+}
+
 // A 16 x 8 B operand: four k of column g.
 template <int TB>
 struct FragB {
@@ -171,6 +194,51 @@ __device__ __forceinline__ float4 quad(const __nv_bfloat16 *p, int stride, int m
     const float2 a = unpack(u), b = unpack(v);
     return make_float4(a.x, a.y, b.x, b.y);
 }
+// The quads of rows or columns g and g + 8 at once; p and k: the sixteen's start.
+struct Quads {
+    float4 a, b;
+};
+template <bool K>
+__device__ __forceinline__ Quads quads(const float *p, int stride, int k) {
+    const int g = (threadIdx.x & 31) >> 2, t2 = 2 * (threadIdx.x & 3);
+    return {quad<K>(p, stride, g, k + t2), quad<K>(p, stride, g + 8, k + t2)};
+}
+template <bool K>
+__device__ __forceinline__ Quads quads(const __nv_bfloat16 *p, int stride, int k) {
+    // four 8 x 8 matrices: k's halves of the first eight, then of the second; eight
+    // lanes name each one's rows
+    const int lane = threadIdx.x & 31;
+    const __nv_bfloat16 *row = K ? p + ((lane & 7) + 8 * (lane >> 4)) * stride + k + (lane & 8)
+                                 : p + (k + (lane & 15)) * stride + 8 * (lane >> 4);
+    const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(row));
+    uint32_t r0, r1, r2, r3;
+    if (K)
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+                     : "r"(at)
+                     : "memory");
+    else
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+                     : "r"(at)
+                     : "memory");
+    const float2 a = unpack(r0), b = unpack(r1), c = unpack(r2), d = unpack(r3);
+    return {make_float4(a.x, a.y, b.x, b.y), make_float4(c.x, c.y, d.x, d.y)};
+}
+
+// Lane (g, t) holds columns 2t, 2t + 1 of row g of an 8 x 8 tile (bf16: in one
+// register) and gets those of its transpose.
+__device__ __forceinline__ uint32_t transpose8(uint32_t u) {
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %0;" : "+r"(u));
+    return u;
+}
+__device__ __forceinline__ float2 transpose8(float x, float y) {
+    const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
+    const uint32_t lo = transpose8(__byte_perm(a, b, 0x5410)), hi = transpose8(__byte_perm(a, b, 0x7632));
+    return make_float2(__uint_as_float(__byte_perm(lo, hi, 0x5410)),
+                       __uint_as_float(__byte_perm(lo, hi, 0x7632)));
+}
+
 // A quad times c[.] of its k.
 __device__ __forceinline__ float4 scaled(float4 x, const float *c, int k) {
     return make_float4(x.x * c[k], x.y * c[k + 1], x.z * c[k + 8], x.w * c[k + 9]);
