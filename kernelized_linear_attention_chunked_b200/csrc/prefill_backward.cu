@@ -62,22 +62,26 @@ struct BwdCfg {
     static constexpr int DS = B0 + 4 * IN;     // ROWS x 64 products
     static constexpr int P = DS + ROWS * kTS * 4;
     static constexpr int STAT = P + ROWS * kTS * 4;  // bwd_key: two stages of 64 float4
-    static constexpr int RED = STAT + 2 * kB * 16;   // bwd_query: row sums of four column quarters
-    static constexpr int BYTES = RED + 8 * ROWS * 8;
+    static constexpr int RED = STAT + 2 * kB * 16;   // bwd_query: row sums of four column quarters, and theirs
+    static constexpr int BYTES = RED + 10 * ROWS * 8;
 };
 
-// s and dP in 64 bits for two rows (0, 8 on) of q, o against four columns (0, 1,
-// 8, 9 on) of k, v, in the layout of two accumulator tiles.
+// The first sixteen queries' scores and dP in 64 bits, in the layout of two accumulator
+// tiles: rows (0, 8 on) of q, o against columns (0, 1, 8, 9 on) of k, v. Each of four
+// warps (`quarter`) sums a quarter of the d terms into its 512 doubles of `buf`; after a
+// barrier one of them joins those. (By one warp alone, in every pass, this was two thirds
+// of a call of 64 tokens at d = 64.)
 template <int D>
-__device__ __forceinline__ void dots64(const float *q, const float *o, const float *k, const float *v,
-                                       double (&s)[2][4], double (&dp)[2][4]) {
+__device__ __forceinline__ void dots64(double *buf, int quarter, int lane, const float *q,
+                                       const float *o, const float *k, const float *v) {
     constexpr int RS = D + 8;
+    double s[2][4], dp[2][4];
 #pragma unroll
     for (int n = 0; n < 2; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[n][e] = dp[n][e] = 0.0;
 #pragma unroll 2
-    for (int c = 0; c < D; ++c) {
+    for (int c = quarter * (D / 4); c < (quarter + 1) * (D / 4); ++c) {
         double a[2], b[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -96,6 +100,52 @@ __device__ __forceinline__ void dots64(const float *q, const float *o, const flo
                 }
             }
     }
+    double *d = buf + 512 * quarter + lane;
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            d[32 * (4 * n + e)] = s[n][e];
+            d[32 * (8 + 4 * n + e)] = dp[n][e];
+        }
+}
+// value x (0 .. 7 the scores, then dP) of this lane, joined
+__device__ __forceinline__ double joined64(const double *buf, int lane, int x) {
+    const double *d = buf + 32 * x + lane;
+    return (d[0] + d[512]) + (d[1024] + d[1536]);
+}
+
+// The CTAs of a cluster share a tile of rows: each takes every n-th step of its walk.
+struct Split {
+    int rank, n;
+    __device__ __forceinline__ Split() {
+        asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+        asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+    }
+    __device__ __forceinline__ int steps(int all) const { return all > rank ? (all - rank + n - 1) / n : 0; }
+    __device__ __forceinline__ void sync() const {
+        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                         : "memory");
+    }
+    // CTA `r`'s address of shared memory at `p`
+    __device__ __forceinline__ uint32_t at(const void *p, int r) const {
+        uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p));
+        asm("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(a) : "r"(r));
+        return a;
+    }
+};
+__device__ __forceinline__ double peer_f64(uint32_t a) {
+    double x;
+    asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(x) : "r"(a) : "memory");
+    return x;
+}
+__device__ __forceinline__ float4 peer_f32x4(uint32_t a) {
+    float4 x;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                 : "r"(a)
+                 : "memory");
+    return x;
 }
 
 // Columns d0 .. of rows m0 .. of a tile that starts at row t0 of a [T, D] matrix
@@ -114,7 +164,41 @@ __device__ __forceinline__ void store_rows(void *dst, size_t row0, int t0, int T
     }
 }
 
-// One CTA per (head, ROWS queries). Two walks over the key tiles up to the
+// The same of `part`, the sum over the cluster's CTAs (in their order: the same bits on
+// every run), through `tile` (ROWS x D in shared memory that nobody else uses). Each CTA
+// joins and writes its share of the rows. Ends with the reads done everywhere.
+template <int D, int ROWS, int N, int M>
+__device__ __forceinline__ void join_rows(void *const (&dst)[M], size_t row0, int t0, int T,
+                                          const float (*const (&part)[M])[4], float *tile,
+                                          const Split &cl, int m0, int d0, int gr, int t2) {
+    constexpr int RS = D + 8;
+#pragma unroll
+    for (int x = 0; x < M; ++x)
+        if (d0 < D) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int nt = 0; nt < N; ++nt)
+                    *reinterpret_cast<float2 *>(tile + (x * ROWS + m0 + gr + 8 * h) * RS + d0 + 8 * nt +
+                                                t2) =
+                        make_float2(part[x][nt][2 * h], part[x][nt][2 * h + 1]);
+        }
+    cl.sync();
+    for (int i = cl.rank * blockDim.x + threadIdx.x; i < M * ROWS * (D / 4); i += cl.n * blockDim.x) {
+        const int r = i / (D / 4), c = 4 * (i % (D / 4)), t = t0 + r % ROWS;
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int p = 0; p < cl.n; ++p) {
+            const float4 v = peer_f32x4(cl.at(tile + r * RS + c, p));
+            sum = make_float4(sum.x + v.x, sum.y + v.y, sum.z + v.z, sum.w + v.w);
+        }
+        if (t < T)
+            *reinterpret_cast<float4 *>(static_cast<float *>(dst[M == 1 ? 0 : r / ROWS]) +
+                                        (row0 + t) * (size_t)D + c) = sum;
+    }
+    cl.sync();
+}
+
+// One cluster per (head, ROWS queries). Two walks over the key tiles up to the
 // diagonal: den and delta, then dQ.
 template <int D, int ROWS>
 __global__ void __launch_bounds__(BwdCfg<D, ROWS>::THREADS) bwd_query(Args p) {
@@ -127,16 +211,21 @@ __global__ void __launch_bounds__(BwdCfg<D, ROWS>::THREADS) bwd_query(Args p) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int gr = lane >> 2, t2 = 2 * (lane & 3);
     const int quarter = warp & 3, m0 = 16 * (warp >> 2), n0 = 16 * quarter, d0 = 8 * ND * quarter;
-    const size_t head = blockIdx.x / p.tiles;
-    const int q0 = (p.tiles - 1 - (int)(blockIdx.x % p.tiles)) * ROWS;  // the longest rows first
+    const Split cl;
+    const unsigned id = blockIdx.x / cl.n;
+    const size_t head = id / p.tiles;
+    const int q0 = (p.tiles - 1 - (int)(id % p.tiles)) * ROWS;  // the longest rows first
     const size_t row0 = head * (size_t)p.T;
-    const int walk = (min(q0 + ROWS, p.T) + kB - 1) / kB;  // key tiles with a key that a query sees
-    const bool few = q0 == 0 && m0 == 0;  // this warp's rows are the first sixteen queries
+    // this CTA's key tiles with a key that a query sees
+    const int walk = cl.steps((min(q0 + ROWS, p.T) + kB - 1) / kB);
+    // step 0 holds the first sixteen queries' tile; it is one warp's
+    const bool few = q0 == 0 && cl.rank == 0, mine = few && m0 == 0 && n0 == 0;
+    double *buf = reinterpret_cast<double *>(sm + L::DS);
 
     auto tileK = [&](int u) { return reinterpret_cast<float *>(sm + L::B0 + (u & 1) * 2 * L::IN); };
     auto tileV = [&](int u) { return tileK(u) + kB * RS; };
     auto prefetch = [&](int u) {
-        const int t = (u < walk ? u : u - walk) * kB;
+        const int t = ((u < walk ? u : u - walk) * cl.n + cl.rank) * kB;
         load_tile<float, D, TH>(tileK(u), RS, static_cast<const float *>(p.k), row0, t, p.T, D, 0, tid);
         load_tile<float, D, TH>(tileV(u), RS, static_cast<const float *>(p.v), row0, t, p.T, D, 0, tid);
         cp_commit();
@@ -144,7 +233,7 @@ __global__ void __launch_bounds__(BwdCfg<D, ROWS>::THREADS) bwd_query(Args p) {
     if (tid == 0) sm100::launch_dependents();  // bwd_key: it waits for this grid's end
     load_tile<float, D, TH, ROWS>(sQ, RS, static_cast<const float *>(p.q), row0, q0, p.T, D, 0, tid);
     load_tile<float, D, TH, ROWS>(sO, RS, static_cast<const float *>(p.d_o), row0, q0, p.T, D, 0, tid);
-    prefetch(0);
+    if (walk > 0) prefetch(0);
     cp_wait_all();
     __syncthreads();
 
@@ -152,113 +241,153 @@ __global__ void __launch_bounds__(BwdCfg<D, ROWS>::THREADS) bwd_query(Args p) {
     float inv2[2], dhi[2], dlo[2];
     float dq[ND][4];
     clear(dq);
-    for (int u = 0; u < 2 * walk; ++u) {
-        if (u + 1 < 2 * walk) prefetch(u + 1);
-        const bool second = u >= walk;
-        const int k0 = (second ? u - walk : u) * kB;
+    auto scores = [&](const float *k, const float *v, float(&s)[2][4], float(&dp)[2][4]) {
+        clear(s);
+        clear(dp);
+        gemm<2, 2, 2, 4>(
+            s, 0, D / 16, [&](int m, int kk) { return quad<true>(sQ + m0 * RS, RS, m, kk); },
+            [&](int n, int kk) { return quad<true>(k + n0 * RS, RS, n, kk); });
+        gemm<2, 2, 2, 4>(
+            dp, 0, D / 16, [&](int m, int kk) { return quad<true>(sO + m0 * RS, RS, m, kk); },
+            [&](int n, int kk) { return quad<true>(v + n0 * RS, RS, n, kk); });
+    };
+    // whether row gr + 8 h sees column 8 nt + t2 + (e & 1) of step u
+    auto seen = [&](int u, int nt, int e) {
+        return (u * cl.n + cl.rank) * kB + n0 + 8 * nt + t2 + (e & 1) <= q0 + m0 + gr + 8 * (e >> 1);
+    };
+    for (int u = 0; u < walk; ++u) {  // den and delta den
+        prefetch(u + 1);
         const float *k = tileK(u), *v = tileV(u);
-        if (u == walk) {  // the rows' sums are complete: join the lanes, then the column quarters
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                for (int off = 1; off < 4; off <<= 1) {
-                    den[h] += __shfl_xor_sync(0xffffffffu, den[h], off);
-                    num[h] += __shfl_xor_sync(0xffffffffu, num[h], off);
-                }
-                if ((lane & 3) == 0) {
-                    red[2 * quarter * ROWS + m0 + gr + 8 * h] = den[h];
-                    red[(2 * quarter + 1) * ROWS + m0 + gr + 8 * h] = num[h];
-                }
-            }
+        if (few && u == 0) {
+            if (m0 == 0)
+                dots64<D>(buf, quarter, lane, sQ + gr * RS, sO + gr * RS, k + t2 * RS, v + t2 * RS);
             __syncthreads();
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int i = m0 + gr + 8 * h;
-                den[h] = (double)p.eps;
-                num[h] = 0.0;
-                for (int c = 0; c < 4; ++c) {
-                    den[h] += red[2 * c * ROWS + i];
-                    num[h] += red[(2 * c + 1) * ROWS + i];
-                }
-                const double delta = den[h] == 0.0 ? 0.0 : num[h] / den[h];
-                inv2[h] = den[h] == 0.0 ? 0.f : (float)(2.0 / den[h]);
-                dhi[h] = (float)delta;
-                dlo[h] = (float)(delta - (double)dhi[h]);
-                if (quarter == 0 && (lane & 3) == 0 && q0 + i < p.T)
-                    p.stat[row0 + q0 + i] = make_float4(0.5f * inv2[h], inv2[h], dhi[h], dlo[h]);
-            }
         }
-        float s[2][4], dp[2][4];
-        if (few && k0 == 0 && n0 == 0) {
-            double s64[2][4], dp64[2][4];
-            dots64<D>(sQ + gr * RS, sO + gr * RS, k + t2 * RS, v + t2 * RS, s64, dp64);
+        if (mine && u == 0) {
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int h = e >> 1;
-                    const bool seen = 8 * nt + t2 + (e & 1) <= gr + 8 * h;
-                    const double x = seen ? s64[nt][e] : 0.0;
-                    if (!second) {
-                        den[h] = fma(x, x, den[h]);
-                        if (seen) num[h] = fma(x * x, dp64[nt][e], num[h]);
-                    } else {
-                        s[nt][e] = seen ? (float)((double)inv2[h] * x *
-                                                  ((dp64[nt][e] - (double)dhi[h]) - (double)dlo[h]))
-                                        : 0.f;
+                for (int e = 0; e < 4; ++e)
+                    if (seen(0, nt, e)) {
+                        const double x = joined64(buf, lane, 4 * nt + e);
+                        den[e >> 1] = fma(x, x, den[e >> 1]);
+                        num[e >> 1] = fma(x * x, joined64(buf, lane, 8 + 4 * nt + e), num[e >> 1]);
                     }
-                }
         } else {
-            clear(s);
-            clear(dp);
-            gemm<2, 2, 2, 4>(
-                s, 0, D / 16, [&](int m, int kk) { return quad<true>(sQ + m0 * RS, RS, m, kk); },
-                [&](int n, int kk) { return quad<true>(k + n0 * RS, RS, n, kk); });
-            gemm<2, 2, 2, 4>(
-                dp, 0, D / 16, [&](int m, int kk) { return quad<true>(sO + m0 * RS, RS, m, kk); },
-                [&](int n, int kk) { return quad<true>(v + n0 * RS, RS, n, kk); });
-            float ds[2] = {0.f, 0.f}, ns[2] = {0.f, 0.f};
+            float s[2][4], dp[2][4], ds[2] = {0.f, 0.f}, ns[2] = {0.f, 0.f};
+            scores(k, v, s, dp);
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int h = e >> 1;
-                    const bool seen = k0 + n0 + 8 * nt + t2 + (e & 1) <= q0 + m0 + gr + 8 * h;
-                    if (!second) {
-                        const float w = seen ? s[nt][e] * s[nt][e] : 0.f;
-                        ds[h] += w;
-                        ns[h] = fmaf(w, seen ? dp[nt][e] : 0.f, ns[h]);
-                    } else {
-                        s[nt][e] =
-                            seen ? inv2[h] * s[nt][e] * ((dp[nt][e] - dhi[h]) - dlo[h]) : 0.f;
-                    }
+                    const bool on = seen(u, nt, e);
+                    const float w = on ? s[nt][e] * s[nt][e] : 0.f;
+                    ds[e >> 1] += w;
+                    ns[e >> 1] = fmaf(w, on ? dp[nt][e] : 0.f, ns[e >> 1]);
                 }
-            if (!second) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    den[h] += (double)ds[h];
-                    num[h] += (double)ns[h];
-                }
+            for (int h = 0; h < 2; ++h) {
+                den[h] += (double)ds[h];
+                num[h] += (double)ns[h];
             }
-        }
-        if (second) {
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    *reinterpret_cast<float2 *>(sDS + (m0 + gr + 8 * h) * kTS + n0 + 8 * nt + t2) =
-                        make_float2(s[nt][2 * h], s[nt][2 * h + 1]);
-            __syncthreads();
-            if (d0 < D)
-                gemm<2, 2, ND, 4>(
-                    dq, 0, kB / 16,
-                    [&](int m, int kk) { return quad<true>(sDS + m0 * kTS, kTS, m, kk); },
-                    [&](int n, int kk) { return quad<false>(k + d0, RS, n, kk); });
         }
         cp_wait_all();
         __syncthreads();
     }
-    if (d0 < D) store_rows<D>(p.dq, row0, q0, p.T, dq, m0, d0, gr, t2);
+    // the rows' sums are complete: join the lanes, the column quarters, the CTAs
+    {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int off = 1; off < 4; off <<= 1) {
+                den[h] += __shfl_xor_sync(0xffffffffu, den[h], off);
+                num[h] += __shfl_xor_sync(0xffffffffu, num[h], off);
+            }
+            if ((lane & 3) == 0) {
+                red[2 * quarter * ROWS + m0 + gr + 8 * h] = den[h];
+                red[(2 * quarter + 1) * ROWS + m0 + gr + 8 * h] = num[h];
+            }
+        }
+        __syncthreads();
+        double *sum = red + 8 * ROWS;
+        if (tid < 2 * ROWS) {
+            double x = 0.0;
+            for (int c = 0; c < 4; ++c) x += red[2 * c * ROWS + tid];
+            sum[tid] = x;
+        }
+        cl.sync();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int i = m0 + gr + 8 * h;
+            double d = (double)p.eps, n = 0.0;
+            for (int r = 0; r < cl.n; ++r) {
+                d += peer_f64(cl.at(sum + i, r));
+                n += peer_f64(cl.at(sum + ROWS + i, r));
+            }
+            const double delta = d == 0.0 ? 0.0 : n / d;
+            inv2[h] = d == 0.0 ? 0.f : (float)(2.0 / d);
+            dhi[h] = (float)delta;
+            dlo[h] = (float)(delta - (double)dhi[h]);
+            if (cl.rank == 0 && quarter == 0 && (lane & 3) == 0 && q0 + i < p.T)
+                p.stat[row0 + q0 + i] = make_float4(0.5f * inv2[h], inv2[h], dhi[h], dlo[h]);
+        }
+    }
+    if (mine) {  // sDS takes the partial sums' place: keep the joined ones behind it
+        double x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = joined64(buf, lane, i);
+        __syncwarp();
+        buf = reinterpret_cast<double *>(sm + L::P);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) buf[32 * i + lane] = x[i];
+    }
+    if (few) __syncthreads();
+    for (int u = 0; u < walk; ++u) {  // dQ
+        if (u + 1 < walk) prefetch(walk + u + 1);
+        const float *k = tileK(walk + u), *v = tileV(walk + u);
+        float s[2][4];
+        if (mine && u == 0) {
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int h = e >> 1;
+                    const double x = buf[32 * (4 * nt + e) + lane], y = buf[32 * (8 + 4 * nt + e) + lane];
+                    s[nt][e] = seen(0, nt, e) ? (float)((double)inv2[h] * x *
+                                                        ((y - (double)dhi[h]) - (double)dlo[h]))
+                                              : 0.f;
+                }
+        } else {
+            float dp[2][4];
+            scores(k, v, s, dp);
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int h = e >> 1;
+                    s[nt][e] =
+                        seen(u, nt, e) ? inv2[h] * s[nt][e] * ((dp[nt][e] - dhi[h]) - dlo[h]) : 0.f;
+                }
+        }
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                *reinterpret_cast<float2 *>(sDS + (m0 + gr + 8 * h) * kTS + n0 + 8 * nt + t2) =
+                    make_float2(s[nt][2 * h], s[nt][2 * h + 1]);
+        __syncthreads();
+        if (d0 < D)
+            gemm<2, 2, ND, 4>(
+                dq, 0, kB / 16, [&](int m, int kk) { return quad<true>(sDS + m0 * kTS, kTS, m, kk); },
+                [&](int n, int kk) { return quad<false>(k + d0, RS, n, kk); });
+        cp_wait_all();
+        __syncthreads();
+    }
+    if (cl.n > 1)
+        join_rows<D, ROWS, ND, 1>({p.dq}, row0, q0, p.T, {dq}, reinterpret_cast<float *>(sm + L::B0), cl,
+                                  m0, d0, gr, t2);
+    else if (d0 < D)
+        store_rows<D>(p.dq, row0, q0, p.T, dq, m0, d0, gr, t2);
 }
 
 // One CTA per (head, ROWS keys): the query steps from the diagonal on. Rows of
@@ -273,38 +402,42 @@ __global__ void __launch_bounds__(BwdCfg<D, ROWS>::THREADS) bwd_key(Args p) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int gr = lane >> 2, t2 = 2 * (lane & 3);
     const int quarter = warp & 3, m0 = 16 * (warp >> 2), n0 = 16 * quarter, d0 = 8 * ND * quarter;
-    const size_t head = blockIdx.x / p.tiles;
-    const int k0 = (int)(blockIdx.x % p.tiles) * ROWS;  // the keys that most queries see first
+    const Split cl;
+    const unsigned id = blockIdx.x / cl.n;
+    const size_t head = id / p.tiles;
+    const int k0 = (int)(id % p.tiles) * ROWS;  // the keys that most queries see first
     const size_t row0 = head * (size_t)p.T;
 
-    auto tileQ = [&](int u) { return reinterpret_cast<float *>(sm + L::B0 + (u & 1) * 2 * L::IN); };
-    auto tileO = [&](int u) { return tileQ(u) + kB * RS; };
-    auto stats = [&](int u) { return reinterpret_cast<float4 *>(sm + L::STAT) + (u & 1) * kB; };
-    auto prefetch = [&](int u) {
-        load_tile<float, D, TH>(tileQ(u), RS, static_cast<const float *>(p.q), row0, u * kB, p.T, D, 0, tid);
-        load_tile<float, D, TH>(tileO(u), RS, static_cast<const float *>(p.d_o), row0, u * kB, p.T, D, 0,
-                              tid);
+    const int first = k0 / kB + cl.rank, walk = cl.steps(p.steps - k0 / kB);  // this CTA's steps
+
+    auto tileQ = [&](int j) { return reinterpret_cast<float *>(sm + L::B0 + (j & 1) * 2 * L::IN); };
+    auto tileO = [&](int j) { return tileQ(j) + kB * RS; };
+    auto stats = [&](int j) { return reinterpret_cast<float4 *>(sm + L::STAT) + (j & 1) * kB; };
+    auto prefetch = [&](int j) {
+        const int t = (first + j * cl.n) * kB;
+        load_tile<float, D, TH>(tileQ(j), RS, static_cast<const float *>(p.q), row0, t, p.T, D, 0, tid);
+        load_tile<float, D, TH>(tileO(j), RS, static_cast<const float *>(p.d_o), row0, t, p.T, D, 0, tid);
         if (tid < kB) {
-            const bool have = u * kB + tid < p.T;
-            delta::cp16(stats(u) + tid, p.stat + row0 + (have ? u * kB + tid : 0), have);
+            const bool have = t + tid < p.T;
+            delta::cp16(stats(j) + tid, p.stat + row0 + (have ? t + tid : 0), have);
         }
         cp_commit();
     };
     load_tile<float, D, TH, ROWS>(sK, RS, static_cast<const float *>(p.k), row0, k0, p.T, D, 0, tid);
     load_tile<float, D, TH, ROWS>(sV, RS, static_cast<const float *>(p.v), row0, k0, p.T, D, 0, tid);
-    const int first = k0 / kB;
     sm100::grid_dependency_wait();  // bwd_query's statistics
-    prefetch(first);
+    if (walk > 0) prefetch(0);
     cp_wait_all();
     __syncthreads();
 
     float dk[ND][4], dv[ND][4];
     clear(dk);
     clear(dv);
-    for (int u = first; u < p.steps; ++u) {
-        if (u + 1 < p.steps) prefetch(u + 1);
-        const float *q = tileQ(u), *o = tileO(u);
-        const float4 *st = stats(u);
+    for (int j = 0; j < walk; ++j) {
+        if (j + 1 < walk) prefetch(j + 1);
+        const int u = first + j * cl.n;
+        const float *q = tileQ(j), *o = tileO(j);
+        const float4 *st = stats(j);
         float s[2][4], dp[2][4];
         clear(s);
         clear(dp);
@@ -325,20 +458,25 @@ __global__ void __launch_bounds__(BwdCfg<D, ROWS>::THREADS) bwd_key(Args p) {
                 s[nt][e] = seen ? t.y * x * ((dp[nt][e] - t.z) - t.w) : 0.f;
                 dp[nt][e] = seen ? x * x * t.x : 0.f;
             }
-        if (u == 0 && n0 == 0 && k0 + m0 == 0) {  // the first sixteen queries (and keys) in 64 bits
-            double s64[2][4], dp64[2][4];
-            dots64<D>(sK + gr * RS, sV + gr * RS, q + t2 * RS, o + t2 * RS, s64, dp64);
+        if (u == 0 && k0 == 0) {  // the first sixteen queries (and keys) in 64 bits
+            double *buf = reinterpret_cast<double *>(sm + L::DS);
+            if (m0 == 0) dots64<D>(buf, quarter, lane, sK + gr * RS, sV + gr * RS, q + t2 * RS, o + t2 * RS);
+            __syncthreads();
+            if (m0 == 0 && n0 == 0) {
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
+                for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int j = gr + (e & 2 ? 8 : 0), i = 8 * nt + t2 + (e & 1);
-                    const float4 t = st[i];
-                    const double x = s64[nt][e];
-                    if (j > i) continue;
-                    s[nt][e] = (float)((double)t.y * x * ((dp64[nt][e] - (double)t.z) - (double)t.w));
-                    dp[nt][e] = (float)(x * x * (double)t.x);
-                }
+                    for (int e = 0; e < 4; ++e) {
+                        const int j = gr + (e & 2 ? 8 : 0), i = 8 * nt + t2 + (e & 1);
+                        const float4 t = st[i];
+                        const double x = joined64(buf, lane, 4 * nt + e);
+                        const double y = joined64(buf, lane, 8 + 4 * nt + e);
+                        if (j > i) continue;
+                        s[nt][e] = (float)((double)t.y * x * ((y - (double)t.z) - (double)t.w));
+                        dp[nt][e] = (float)(x * x * (double)t.x);
+                    }
+            }
+            __syncthreads();  // sDS and sP take the partial sums' place
         }
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt)
@@ -362,32 +500,65 @@ __global__ void __launch_bounds__(BwdCfg<D, ROWS>::THREADS) bwd_key(Args p) {
         cp_wait_all();
         __syncthreads();
     }
-    if (d0 < D) {
+    if (cl.n > 1) {
+        join_rows<D, ROWS, ND, 2>({p.dk, p.dv}, row0, k0, p.T, {dk, dv},
+                                  reinterpret_cast<float *>(sm + L::B0), cl, m0, d0, gr, t2);
+    } else if (d0 < D) {
         store_rows<D>(p.dk, row0, k0, p.T, dk, m0, d0, gr, t2);
         store_rows<D>(p.dv, row0, k0, p.T, dv, m0, d0, gr, t2);
     }
 }
 
 template <int D, int ROWS>
-cudaError_t run(Args p, long heads, cudaStream_t stream) {
+cudaError_t run(Args p, long heads, int split, cudaStream_t stream) {
     using L = BwdCfg<D, ROWS>;
     static_assert(L::BYTES <= 227 * 1024, "shared memory of one CTA");
     p.tiles = (p.T + ROWS - 1) / ROWS;
     cudaError_t e;
     if ((e = tc::set_smem_once<bwd_query<D, ROWS>>(L::BYTES)) != cudaSuccess) return e;
     if ((e = tc::set_smem_once<bwd_key<D, ROWS>>(L::BYTES)) != cudaSuccess) return e;
-    const unsigned grid = (unsigned)(heads * p.tiles);
-    bwd_query<D, ROWS><<<grid, L::THREADS, L::BYTES, stream>>>(p);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)split;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // bwd_key waits itself
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(heads * p.tiles * split), 1, 1);
+    cfg.blockDim = dim3(L::THREADS, 1, 1);
+    cfg.dynamicSmemBytes = L::BYTES;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if ((e = cudaLaunchKernelEx(&cfg, bwd_query<D, ROWS>, p)) != cudaSuccess) return e;
     if ((e = after_launch()) != cudaSuccess) return e;
-    e = tc::launch_overlapped(bwd_key<D, ROWS>, grid, L::THREADS, L::BYTES, stream, p);
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, bwd_key<D, ROWS>, p);
     return e != cudaSuccess ? e : after_launch();
+}
+
+// CTAs per tile of rows, for `tiles` of them whose longest walk has `steps`: doubled as
+// long as all fit the SMs at once, or the longest walk keeps two steps (up to 512 CTAs)
+// or four (up to 1024). Measured, for 1, 2, 4, 8 (us; fp32 d64, heads x T): 4 x 643: 95, 75,
+// 55, 73; 1 x 2048: 257, 137, 104, 91; 4 x 2048: 405, 307, 267, 319; 16 x 1024: 315, 282,
+// 307, 430; 48 x 300: 115, 127, 163, 299; 16 x 2048: 1080, 998, 1146, 1594; 64 x 1024:
+// 1009, 1072, 1420, 2243.
+int split_of(long tiles, int steps) {
+    int n = 1;
+    while (n < 8 && 2 * n <= steps) {
+        const long ctas = 2 * n * tiles;
+        if (!(ctas <= 148 || (ctas <= 512 && steps >= 4 * n) || (ctas <= 1024 && steps >= 8 * n))) break;
+        n *= 2;
+    }
+    return n;
 }
 
 // 32 rows per CTA where 64 would not give every SM two
 template <int D>
 cudaError_t run_rows(const Args &p, long heads, cudaStream_t stream) {
-    const bool small = heads * ((p.T + 63) / 64) < 2 * 148;
-    return small ? run<D, 32>(p, heads, stream) : run<D, 64>(p, heads, stream);
+    const long t64 = heads * ((p.T + 63) / 64), t32 = heads * ((p.T + 31) / 32);
+    return t64 < 2 * 148 ? run<D, 32>(p, heads, split_of(t32, p.steps), stream)
+                         : run<D, 64>(p, heads, split_of(t64, p.steps), stream);
 }
 
 }  // namespace
