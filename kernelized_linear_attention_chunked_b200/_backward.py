@@ -32,21 +32,40 @@ def prefill_backward_workspace_bytes(B, H, T, d, dtype) -> int:
     return int(lib().kata_prefill_backward_workspace_bytes(B, H, T, d, kb._DTYPE[dtype]))
 
 
-def prefill_backward(q, k, v, do, eps: float = 1e-6, workspace=None, stream=None):
-    """Gradients (dq, dk, dv) of prefill's output from a zero state, for the
-    output's gradient ``do``. All [B, H, T, d] in q's dtype; any T."""
+def _inputs(q, k, v, do):
+    """The tensors' type code and shape; raises unless they fit each other. One
+    expression for the ordinary case: a short call is bound by the host."""
+    try:
+        shape, dtype, dev = q.shape, q.dtype, q.get_device()
+        if (len(shape) == 4 and dev >= 0 and dtype in kb._DTYPE and q.is_contiguous()
+                and k.shape == shape and k.dtype is dtype and k.get_device() == dev
+                and k.is_contiguous() and v.shape == shape and v.dtype is dtype
+                and v.get_device() == dev and v.is_contiguous() and do.shape == shape
+                and do.dtype is dtype and do.get_device() == dev and do.is_contiguous()):
+            return kb._DTYPE[dtype], shape
+    except AttributeError:
+        pass
+    for name, t in (("q", q), ("k", k), ("v", v), ("do", do)):
+        if t is None:
+            raise KataError(f"{name} must not be None")
     if q.dim() != 4:
         raise KataError(f"q has {q.dim()} dimensions, expected 4")
     dt = _dt(q)
     for name, t in (("q", q), ("k", k), ("v", v), ("do", do)):
-        if t is None:
-            raise KataError(f"{name} must not be None")
         want(name, t, q.shape, q.dtype, q)
-    want("workspace", workspace, None, None, q)
-    B, H, T, d = q.shape
+    return dt, q.shape
+
+
+def prefill_backward(q, k, v, do, eps: float = 1e-6, workspace=None, stream=None):
+    """Gradients (dq, dk, dv) of prefill's output from a zero state, for the
+    output's gradient ``do``. All [B, H, T, d] in q's dtype; any T."""
+    dt, shape = _inputs(q, k, v, do)
+    B, H, T, d = shape
+    if workspace is not None:
+        want("workspace", workspace, None, None, q)
     L = lib()
     with on_stream(q, stream) as s:
-        dq, dk, dv = (torch.empty_like(q) for _ in range(3))
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(q), torch.empty_like(q)
         if workspace is None:
             workspace = workspace_for(L, "kata_prefill_backward_workspace_bytes",
                                       (B, H, T, d, dt), q)

@@ -149,7 +149,7 @@ def delta_backward(q, k, v, g, beta, do, scale: float | None = None, S_in=None, 
     scale = d ** -0.5 if scale is None else scale
     L = lib()
     with on_stream(q, stream) as s:
-        dq, dk, dv = (torch.empty_like(q) for _ in range(3))
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(q), torch.empty_like(q)
         dg, db = torch.empty_like(g), torch.empty_like(beta)
         dS_in = g.new_empty(st) if state_grad else None
         if workspace is None:
