@@ -470,8 +470,13 @@ struct ChainSmem {
 // and an accumulator is, register for register, the A operand of the product that
 // follows. The warp that makes one cuts it into tf32 parts and leaves it in that order
 // for the others: eight 128-bit reads where the plain form took 32 scalar ones and cut
-// them four times over (341 -> REPLACE1 us at B2 H16 T16384 d64, 33 -> REPLACE2 us at
-// B4 H8 T2048 d32).
+// them four times over (341 -> 315 us at B2 H16 T16384 d64, 33 -> 31 us at B4 H8 T2048
+// d32). A chunk of d = 64 takes 2220 cycles: 1120 for E, 1010 for the state and the outputs'
+// end. Bound by the length of these steps and by shared memory (1370 of those cycles move
+// data). Measured without gain: the outputs a chunk behind the chain with barriers of their
+// own (d64 the same, d32 33 -> 36 us), their products two sixteens at a time (d32 31 -> 34),
+// operands cut by each reader (d64 315 -> 321, d128 66 -> 64), M by the copying warps
+// (d32 31 -> 34).
 // Warps 0-3 carry the chain: they hold the state in registers (fp32, D / 4 of its rows
 // each) and take two dependent products per chunk. Warps 4-7 take the products that
 // hang off it: the outputs (forward) or Q^T dO (REV). Warps 8-11 bring K, Q and
@@ -485,6 +490,10 @@ __device__ __forceinline__ void walk_chunks(const Args &p, const Scratch &w, con
     constexpr int KS = L::KS, TI = Parts<Tin>::N;
     constexpr int MT = D >= 64 ? D / 64 : 1;  // sixteens of the state's rows per chain warp
     constexpr int KP = D >= 32 ? 2 : 1;       // sixteens of k at a time
+    // (c beta E)^T in three bf16 parts, for bf16 K: cutting takes longer on the critical
+    // path, which pays where a warp uses a part twice (d128 68 -> 63 us at B3 H5 T1531; d64
+    // 315 -> 324 us at B2 H16 T16384)
+    constexpr bool CUT3 = TI == 1 && MT > 1;
     extern __shared__ __align__(16) uint8_t sm[];
     uint4 *sS = reinterpret_cast<uint4 *>(sm + L::S), *sYc = reinterpret_cast<uint4 *>(sm + L::YC);
     uint4 *sE = reinterpret_cast<uint4 *>(sm + L::SIDE);
@@ -636,9 +645,13 @@ __device__ __forceinline__ void walk_chunks(const Args &p, const Scratch &w, con
             auto times = [&](float4 x) {
                 return make_float4(c0_.x * x.x, c0_.y * x.y, c1_.x * x.z, c1_.y * x.w);
             };
-            FragA<2> f;
-            f.set(times(y[0]), times(y[1]));
-            put_frag(sYc + rw * 128 + lane, f);
+            if constexpr (CUT3) {
+                put_cut3(sYc + rw * 96 + lane, times(y[0]), times(y[1]));
+            } else {
+                FragA<2> f;
+                f.set(times(y[0]), times(y[1]));
+                put_frag(sYc + rw * 128 + lane, f);
+            }
             if (wantO) {
                 FragA<TI> e;
                 e.set(y[0], y[1]);
@@ -704,19 +717,53 @@ __device__ __forceinline__ void walk_chunks(const Args &p, const Scratch &w, con
             for (int mt = 0; mt < MT; ++mt) clear(acc[mt]);
 #pragma unroll
             for (int k0 = 0; k0 < kC / 16; k0 += 2) {
-                FragA<2> a[2];
+                if constexpr (CUT3) {
+                    uint4 a[2][3];
 #pragma unroll
-                for (int s = 0; s < 2; ++s) get_frag(a[s], sYc + (k0 + s) * 128 + lane);
+                    for (int s = 0; s < 2; ++s)
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    FragB<TI> b[2][2];
+                        for (int j = 0; j < 3; ++j) a[s][j] = sYc[(k0 + s) * 96 + 32 * j + lane];
 #pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        const Quads x = quads<false>(sK + 16 * (MT * warp + mt), KS, 16 * (k0 + s));
-                        b[s][0].set(x.a);
-                        b[s][1].set(x.b);
+                    for (int mt = 0; mt < MT; ++mt) {
+                        uint4 b[2];
+                        float t[2][2][4];
+#pragma unroll
+                        for (int s = 0; s < 2; ++s)
+                            b[s] = pairs<false>(sK + 16 * (MT * warp + mt), KS, 16 * (k0 + s));
+#pragma unroll
+                        for (int j = 2; j >= 0; --j)  // the small parts first
+#pragma unroll
+                            for (int s = 0; s < 2; ++s) {
+                                if (j == 2) {
+                                    mma16_0(t[s][0], a[s][j], b[s].x, b[s].y);
+                                    mma16_0(t[s][1], a[s][j], b[s].z, b[s].w);
+                                } else {
+                                    mma16(t[s][0], a[s][j], b[s].x, b[s].y);
+                                    mma16(t[s][1], a[s][j], b[s].z, b[s].w);
+                                }
+                            }
+#pragma unroll
+                        for (int s = 0; s < 2; ++s)
+#pragma unroll
+                            for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) acc[mt][nt][e] += t[s][nt][e];
                     }
-                    mma_step<2, TI, 2, 2>(acc[mt], a, b);
+                } else {
+                    FragA<2> a[2];
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) get_frag(a[s], sYc + (k0 + s) * 128 + lane);
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        FragB<TI> b[2][2];
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) {
+                            const Quads x = quads<false>(sK + 16 * (MT * warp + mt), KS, 16 * (k0 + s));
+                            b[s][0].set(x.a);
+                            b[s][1].set(x.b);
+                        }
+                        mma_step<2, TI, 2, 2>(acc[mt], a, b);
+                    }
                 }
             }
 #pragma unroll

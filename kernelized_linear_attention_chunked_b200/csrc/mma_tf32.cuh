@@ -52,6 +52,22 @@ __device__ __forceinline__ void mma0(float (&c)[4], const uint32_t (&a)[4], uint
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
+// m16n8k16 on bf16 pairs: c += A B, and c = A B.
+__device__ __forceinline__ void mma16(float (&c)[4], const uint4 &a, uint32_t b0, uint32_t b1) {
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma16_0(float (&c)[4], const uint4 &a, uint32_t b0, uint32_t b1) {
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // x's tf32 part (nearest) and what is left of it. A NaN stays one in `lo`.
 __device__ __forceinline__ void split(float x, uint32_t &hi, uint32_t &lo) {
     hi = (__float_as_uint(x) + 0x1000u) & 0xFFFFE000u;
@@ -203,27 +219,58 @@ __device__ __forceinline__ Quads quads(const float *p, int stride, int k) {
     const int g = (threadIdx.x & 31) >> 2, t2 = 2 * (threadIdx.x & 3);
     return {quad<K>(p, stride, g, k + t2), quad<K>(p, stride, g + 8, k + t2)};
 }
-template <bool K>
-__device__ __forceinline__ Quads quads(const __nv_bfloat16 *p, int stride, int k) {
-    // four 8 x 8 matrices: k's halves of the first eight, then of the second; eight
-    // lanes name each one's rows
-    const int lane = threadIdx.x & 31;
-    const __nv_bfloat16 *row = K ? p + ((lane & 7) + 8 * (lane >> 4)) * stride + k + (lane & 8)
-                                 : p + (k + (lane & 15)) * stride + 8 * (lane >> 4);
+// Four 8 x 8 matrices of bf16; lanes 8 i .. 8 i + 7 name the rows of the i-th.
+template <bool TRANS>
+__device__ __forceinline__ uint4 ldmatrix4(const __nv_bfloat16 *row) {
     const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(row));
-    uint32_t r0, r1, r2, r3;
-    if (K)
-        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+    uint4 r;
+    if (TRANS)
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
                      : "r"(at)
                      : "memory");
     else
-        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
                      : "r"(at)
                      : "memory");
-    const float2 a = unpack(r0), b = unpack(r1), c = unpack(r2), d = unpack(r3);
+    return r;
+}
+// Rows or columns g (x, y: k's halves) and g + 8 (z, w) as bf16 pairs.
+template <bool K>
+__device__ __forceinline__ uint4 pairs(const __nv_bfloat16 *p, int stride, int k) {
+    const int lane = threadIdx.x & 31;
+    return ldmatrix4<!K>(K ? p + ((lane & 7) + 8 * (lane >> 4)) * stride + k + (lane & 8)
+                           : p + (k + (lane & 15)) * stride + 8 * (lane >> 4));
+}
+template <bool K>
+__device__ __forceinline__ Quads quads(const __nv_bfloat16 *p, int stride, int k) {
+    const uint4 r = pairs<K>(p, stride, k);
+    const float2 a = unpack(r.x), b = unpack(r.y), c = unpack(r.z), d = unpack(r.w);
     return {make_float4(a.x, a.y, b.x, b.y), make_float4(c.x, c.y, d.x, d.y)};
+}
+
+// An A operand cut into three bf16 parts (24 bits and more), for products with bf16
+// values: three m16n8k16 instead of four m16n8k8 of two tf32 parts, three quarters of the
+// bytes, and the bf16 side needs no unpacking.
+__device__ __forceinline__ void cut3(float x, float y, uint32_t (&part)[3]) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+        part[i] = *reinterpret_cast<const uint32_t *>(&h);
+        const float2 f = unpack(part[i]);
+        x -= f.x;
+        y -= f.y;
+    }
+}
+__device__ __forceinline__ void put_cut3(uint4 *p, float4 top, float4 bottom) {
+    uint32_t a[4][3];
+    cut3(top.x, top.y, a[0]);
+    cut3(bottom.x, bottom.y, a[1]);
+    cut3(top.z, top.w, a[2]);
+    cut3(bottom.z, bottom.w, a[3]);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) p[32 * i] = make_uint4(a[0][i], a[1][i], a[2][i], a[3][i]);
 }
 
 // Lane (g, t) holds columns 2t, 2t + 1 of row g of an 8 x 8 tile (bf16: in one
@@ -294,14 +341,6 @@ __device__ __forceinline__ void grams(float (&kk)[NT][4], float (&qk)[NT][4], bo
         }
     }
 }
-// Four 8 x 8 matrices of bf16; lanes 8 i .. 8 i + 7 name the rows of the i-th.
-__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], const __nv_bfloat16 *row) {
-    const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(row));
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(at)
-                 : "memory");
-}
 // The same of bf16: m16n8k16, whose products are exact as well, takes sixteen k in the
 // cycles of eight tf32 ones, and its operands need no unpacking.
 template <int NT>
@@ -312,29 +351,24 @@ __device__ __forceinline__ void grams(float (&kk)[NT][4], float (&qk)[NT][4], bo
     const int lane = threadIdx.x & 31;
     const int at = (lane & 15) * stride + 8 * (lane >> 4);  // rows, then the second eight k
     const __nv_bfloat16 *bt = B + (b0 + (lane & 7) + 16 * (lane >> 4)) * stride + (lane & 8);
-    auto mma16 = [](float(&c)[4], const uint32_t(&a)[4], uint32_t y0, uint32_t y1) {
-        float t[4];
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-            "{%8,%9}, {%10,%10,%10,%10};"
-            : "=f"(t[0]), "=f"(t[1]), "=f"(t[2]), "=f"(t[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(y0), "r"(y1), "f"(0.f));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) c[i] += t[i];
-    };
 #pragma unroll 1
     for (int st = 0; st < steps; ++st) {
-        uint32_t a[4], a2[4];
-        ldmatrix4(a, A + at + 16 * st);
-        if (two) ldmatrix4(a2, A2 + at + 16 * st);
+        const uint4 a = ldmatrix4<false>(A + at + 16 * st);
+        const uint4 a2 = two ? ldmatrix4<false>(A2 + at + 16 * st) : a;
 #pragma unroll
         for (int nt = 0; nt < NT; nt += 2) {
             if (nt >= nt_end) continue;
-            uint32_t b[4];
-            ldmatrix4(b, bt + 16 * nt * stride + 16 * st);
+            const uint4 b = ldmatrix4<false>(bt + 16 * nt * stride + 16 * st);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                mma16(kk[nt + e], a, b[2 * e], b[2 * e + 1]);
-                if (two) mma16(qk[nt + e], a2, b[2 * e], b[2 * e + 1]);
+                float x[4], y[4];
+                mma16_0(x, a, e ? b.z : b.x, e ? b.w : b.y);
+                if (two) mma16_0(y, a2, e ? b.z : b.x, e ? b.w : b.y);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    kk[nt + e][i] += x[i];
+                    if (two) qk[nt + e][i] += y[i];
+                }
             }
         }
     }
