@@ -35,12 +35,12 @@
 // which has the same shape: Z = Z0 + W' dS with W' = X^T diag(beta c) K and
 // Z0 = scale X^T diag(beta) M^T dO.
 //
-// Measured on B200 (bf16; both launches): B2 H16 T16384 d64 197 + 333 us, B4 H8 T2048
-// d32 20 + 29, B3 H5 T1531 d128 22 + 62. Neither is near a hardware limit. ncu at B2
-// H16 T4096 d64: delta_prep 52 % of issue slots, tensor pipe 38 %, shared memory 50 %,
-// its CTAs a sequence of short dependent steps (24 warps per SM); delta_chain 128 CTAs
-// of 148 SMs, 2500 cycles per chunk, of which its critical products take 640: issue
-// 44 %, tensor 35 %, shared memory 52 %, the rest waiting at its two barriers.
+// Measured on B200 (bf16; both launches): B2 H16 T16384 d64 174 + 315 us, B4 H8 T2048
+// d32 19 + 31, B3 H5 T1531 d128 20 + 63. ncu at B2 H16 T4096 d64: delta_prep 59 % of
+// issue slots, tensor pipe 37 %, shared memory 63 %, its CTAs a sequence of short
+// dependent steps (32 warps per SM); delta_chain 128 CTAs of 148 SMs, 2220 cycles per
+// chunk, of which its critical products take 640: issue 35 %, tensor 38 %, shared
+// memory 68 %.
 //
 // All products keep fp32 accuracy by split tf32 operands (mma_tf32.cuh): the
 // state, its gradient, dg and dbeta are fp32 results. Only o of bf16 inputs,
@@ -220,7 +220,8 @@ __device__ __forceinline__ void invert(const float *sA, float *sX, int warp, int
         const int c = 8 * warp;
         float *P = sX + 32 + c;
         // rows m0 .. of A (32 columns) times a 32 x 8 B: both sixteens of k at once, or one
-        auto product = [&](float(&acc)[1][4], const float *A, int as, const float *B, bool first, bool second) {
+        auto product = [&](float(&acc)[1][4], const float *A, int as, const float *B, bool first,
+                           bool second) {
             FragA<2> a[2];
             FragB<2> b[2][1];
 #pragma unroll
@@ -268,6 +269,9 @@ struct PrepSmem {
     static constexpr int A = DO + (BACK ? IN : 0), M = A + kC * kAS * 4;
     static constexpr int COEF = M + (BACK ? T : 0);  // beta, a, beta c, G (hi, lo)
     static constexpr int BYTES = COEF + 5 * kC * 4;
+    // four CTAs per SM where their shared memory allows it, at 64 registers (d64 184 -> 174
+    // us at B2 H16 T16384); otherwise the registers are the compiler's choice (with as few
+    // d128 took 21.8 us instead of 20.2 at B3 H5 T1531)
     static constexpr int CTAS = sizeof(Tin) == 2 && 4 * (BYTES + 1024) <= 228 * 1024 ? 4 : 1;
 };
 
@@ -298,7 +302,8 @@ __device__ __forceinline__ void store_frags_t(float *dst, const float (&acc)[N][
 // columns each, of a triangular product every other eight.
 // f: the forward chain's operands; r: the reverse chain's (BACK only).
 template <typename Tin, int D, bool BACK>
-__global__ void __launch_bounds__(256, PrepSmem<Tin, D, BACK>::CTAS) delta_prep(Args p, Scratch f, Scratch r) {
+__global__ void __launch_bounds__(256, PrepSmem<Tin, D, BACK>::CTAS)
+    delta_prep(Args p, Scratch f, Scratch r) {
     using namespace tf;
     using L = PrepSmem<Tin, D, BACK>;
     constexpr int KS = L::KS, TI = Parts<Tin>::N;
@@ -469,11 +474,11 @@ struct ChainSmem {
 //     O^T = scale S0^T Q^T diag(a) + E^T M^T,
 // and an accumulator is, register for register, the A operand of the product that
 // follows. The warp that makes one cuts it into tf32 parts and leaves it in that order
-// for the others: eight 128-bit reads where the plain form took 32 scalar ones and cut
-// them four times over (341 -> 315 us at B2 H16 T16384 d64, 33 -> 31 us at B4 H8 T2048
-// d32). A chunk of d = 64 takes 2220 cycles: 1120 for E, 1010 for the state and the outputs'
-// end. Bound by the length of these steps and by shared memory (1370 of those cycles move
-// data). Measured without gain: the outputs a chunk behind the chain with barriers of their
+// for the others: sixteen 128-bit reads where the plain form took 32 scalar ones and cut
+// them four times over (d = 64; 341 -> 315 us at B2 H16 T16384, d = 32 33 -> 31 us
+// at B4 H8 T2048). A chunk of d = 64 takes 2220 cycles: 1120 for E, 1010 for the state and
+// the outputs' end. Bound by the length of these steps and by shared memory (1370 of those
+// cycles move data). Measured without gain: the outputs a chunk behind the chain with barriers of their
 // own (d64 the same, d32 33 -> 36 us), their products two sixteens at a time (d32 31 -> 34),
 // operands cut by each reader (d64 315 -> 321, d128 66 -> 64), M by the copying warps
 // (d32 31 -> 34).

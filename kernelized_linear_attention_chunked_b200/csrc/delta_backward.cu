@@ -16,8 +16,9 @@
 //     dg_t = sum_{i >= t in the chunk} dG_i + (a_C <S0, dS> + sum_j w_j).
 //
 // Three launches: delta_prep (the operands of both walks), delta_walks (the
-// states and errors forwards, their gradients backwards), and delta_grad, one CTA per (chunk, head), for everything above. The
-// states and errors of every chunk are kept in the workspace in fp32.
+// states and errors forwards, their gradients backwards), and delta_grad, one CTA
+// per (chunk, head), for everything above. The states and errors of every chunk are
+// kept in the workspace in fp32.
 //
 // delta_grad takes the value columns in slices of 32, so that d = 128 fits a
 // CTA's shared memory, and sums the products over the columns in registers.
@@ -27,9 +28,11 @@
 // are made of is in two tf32 parts (mma_tf32.cuh); what only dQ and dK are made of
 // is in one for bf16 inputs, whose results are rounded to 8 bits next.
 //
-// Measured on B200 at B2 H16 T4096 d64 bf16: delta_prep 99 us, delta_walks 153,
-// delta_grad 195 (ncu: issue 52 %, tensor 39 %, shared memory 60 %, 16 warps per SM,
-// their registers and 101 KB of shared memory per CTA in the way of more).
+// Measured on B200 at B2 H16 T4096 d64 bf16: delta_prep 91 us, delta_walks 153,
+// delta_grad 185 (ncu: issue 52 %, tensor 38 %, shared memory 51 %, 16 warps per SM,
+// their registers and 101 KB of shared memory per CTA in the way of more). Its two-way
+// bank conflicts (transposed reads of fp32 tiles, a third of its wavefronts) cost
+// nothing: without them it took as long.
 #include "delta.cuh"
 
 namespace kata {

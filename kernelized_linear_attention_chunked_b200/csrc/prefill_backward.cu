@@ -12,10 +12,12 @@
 // every run.
 //
 // This file: fp32 inputs, in split-tf32 products (mma_tf32.cuh), which keep fp32
-// accuracy; bf16 inputs are prefill_backward_tc.cu's. Two launches: bwd_query (one CTA
-// per ROWS queries: den and delta over the keys, then dQ) and bwd_key (one CTA
-// per ROWS keys: dK, dV). bwd_query leaves den and delta of every row for
-// bwd_key. ROWS is 64, or 32 where 64 would leave SMs idle.
+// accuracy; bf16 inputs are prefill_backward_tc.cu's. Two launches: bwd_query (den and
+// delta over the keys of ROWS queries, then their dQ) and bwd_key (dK, dV of ROWS
+// keys). bwd_query leaves den and delta of every row for bwd_key. ROWS is 64, or 32
+// where 64 would leave SMs idle. A tile of rows is one CTA's or, where tiles are few
+// and walks are long, a cluster's: its CTAs take every n-th step, and their sums are
+// joined through each other's shared memory in the CTAs' order.
 //
 // Rows with few keys need care: there delta_i is nearly dP_ij (row 0 has
 // dP - delta = dP eps / den), and a score near zero enters as 1 / s^3. So delta
@@ -24,10 +26,11 @@
 // queries' scores and dP are formed in 64 bits, the same in both kernels. From
 // row 16 on a row's den is a sum over more than 16 keys.
 //
-// Measured on B200 at B1 H4 T643 d64: 67 + 50 us (84 CTAs; the longest walks 22
-// steps); at B2 H8 T2048 d64 1.15 ms, 18.7 TFLOP/s of the five products per causal pair, of
-// which nine are run in three tf32 parts (101 TFLOP/s of 288 in tf32). Bound by issue (50 %)
-// and shared memory (61 to 67 %).
+// Measured on B200 at B1 H4 T643 d64: 54 us (four CTAs per tile; 103 with one each: 84
+// CTAs, the longest walking 22 steps); at B1 H16 T2048 d64 1.00 ms, 21.5 TFLOP/s of the
+// five products per causal pair, of which nine are run in three tf32 parts (116 TFLOP/s of
+// 288 in tf32). Bound by issue (49 %), the tensor pipe (47 %) and the steps' dependent
+// parts (8 warps per SM).
 #include "delta.cuh"
 
 namespace kata {

@@ -50,6 +50,17 @@ def test_larger(dtype, B, H, T, d):
     check(*inputs(B, H, T, d, dtype, seed=T))
 
 
+@pytest.mark.parametrize("B,H,T,d", [(2, 8, 300, 16), (1, 4, 643, 64), (1, 5, 643, 32),
+                                     (1, 1, 1025, 16), (1, 37, 512, 32)])
+def test_shared_walks(B, H, T, d):
+    # few rows: two, four, eight CTAs share a tile's walk, some of them without a
+    # step of their own (the first rows); tiles of 32 and, in the last case, 64 rows
+    x = inputs(B, H, T, d, torch.float32, seed=H + T)
+    got = kata.prefill_backward(*x)
+    check(*x, got=got)
+    assert all(torch.equal(a, b) for a, b in zip(got, kata.prefill_backward(*x)))
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("eps", [0.0, 1e-6, 1e-2, 10.0])
 def test_eps(dtype, eps):
