@@ -84,6 +84,8 @@ __global__ void __launch_bounds__(StepCfg<Tin, D>::THREADS)
     const size_t head = blockIdx.x / PARTS;
     const int c0 = (int)(blockIdx.x % PARTS) * L::CW + 4 * cg;
     float *Sh = S + head * (size_t)(D * D) + c0;
+    if (tid == 0) sm100::launch_dependents();
+    sm100::grid_dependency_wait();  // whatever the stream ran before
     float4 s[L::ROWS];
 #pragma unroll
     for (int i = 0; i < L::ROWS; ++i)
@@ -149,10 +151,11 @@ template <typename Tin, int D>
 cudaError_t step_d(const void *q, const void *k, const void *v, const float *g, const float *beta,
                    long heads, float scale, float *S, void *o, cudaStream_t stream) {
     using L = StepCfg<Tin, D>;
-    delta_step<Tin, D><<<(unsigned)(heads * (D / L::CW)), L::THREADS, 0, stream>>>(
-        static_cast<const Tin *>(q), static_cast<const Tin *>(k), static_cast<const Tin *>(v), g,
-        beta, scale, S, static_cast<Tin *>(o));
-    return after_launch();
+    const cudaError_t e = tc::launch_overlapped(
+        delta_step<Tin, D>, (unsigned)(heads * (D / L::CW)), L::THREADS, 0, stream,
+        static_cast<const Tin *>(q), static_cast<const Tin *>(k), static_cast<const Tin *>(v), g, beta,
+        scale, S, static_cast<Tin *>(o));
+    return e != cudaSuccess ? e : after_launch();
 }
 
 template <typename Tin>

@@ -322,6 +322,7 @@ __global__ void __launch_bounds__(256, PrepSmem<Tin, D, BACK>::CTAS)
     const size_t row0 = head * (size_t)p.T;
 
     if (tid == 0) sm100::launch_dependents();  // the walks: they wait for this grid's end
+    sm100::grid_dependency_wait();             // whatever the stream ran before
     float2 v2 = make_float2(0.f, 0.f);
     if (warp == 0) v2 = load_decays(p.g, row0, t0, p.T);
     load_tile<Tin, D, 256>(sK, KS, static_cast<const Tin *>(p.k), row0, t0, p.T, D, 0, tid);
@@ -864,8 +865,9 @@ cudaError_t launch_prep(const Args &p, const Scratch &f, const Scratch &r, long 
     static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
     cudaError_t e = tc::set_smem_once<delta_prep<Tin, D, BACK>>(bytes);
     if (e != cudaSuccess) return e;
-    delta_prep<Tin, D, BACK><<<(unsigned)(heads * p.nc), 256, bytes, stream>>>(p, f, r);
-    return after_launch();
+    e = tc::launch_overlapped(delta_prep<Tin, D, BACK>, (unsigned)(heads * p.nc), 256, bytes, stream, p,
+                              f, r);
+    return e != cudaSuccess ? e : after_launch();
 }
 
 template <typename Tin, int D>

@@ -233,7 +233,10 @@ __global__ void __launch_bounds__(BwdCfg<D, ROWS>::THREADS) bwd_query(Args p) {
         load_tile<float, D, TH>(tileV(u), RS, static_cast<const float *>(p.v), row0, t, p.T, D, 0, tid);
         cp_commit();
     };
-    if (tid == 0) sm100::launch_dependents();  // bwd_key: it waits for this grid's end
+    // After the wait for whatever the stream ran before: bwd_key reads inputs at once, and
+    // only for the statistics waits for this grid's end.
+    sm100::grid_dependency_wait();
+    if (tid == 0) sm100::launch_dependents();
     load_tile<float, D, TH, ROWS>(sQ, RS, static_cast<const float *>(p.q), row0, q0, p.T, D, 0, tid);
     load_tile<float, D, TH, ROWS>(sO, RS, static_cast<const float *>(p.d_o), row0, q0, p.T, D, 0, tid);
     if (walk > 0) prefetch(0);
@@ -524,7 +527,7 @@ cudaError_t run(Args p, long heads, int split, cudaStream_t stream) {
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = (unsigned)split;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // bwd_key waits itself
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // the kernels wait themselves
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(heads * p.tiles * split), 1, 1);
@@ -532,10 +535,9 @@ cudaError_t run(Args p, long heads, int split, cudaStream_t stream) {
     cfg.dynamicSmemBytes = L::BYTES;
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     if ((e = cudaLaunchKernelEx(&cfg, bwd_query<D, ROWS>, p)) != cudaSuccess) return e;
     if ((e = after_launch()) != cudaSuccess) return e;
-    cfg.numAttrs = 2;
     e = cudaLaunchKernelEx(&cfg, bwd_key<D, ROWS>, p);
     return e != cudaSuccess ? e : after_launch();
 }

@@ -184,6 +184,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         cta_abort_clear();
         fence_barrier_init();
     }
+    // Whatever the stream ran before, ahead of taking tensor memory that it may still want.
+    // (The keys' kernel starts once every CTA of this one has its own and is past this.)
+    if (!KEYS) grid_dependency_wait();
     if (warp == L::S_WARP) {
         tmem_alloc(slot, 512);
         tmem_relinquish();
@@ -540,8 +543,8 @@ cudaError_t launch(const PrefillBackwardArgs &a, cudaStream_t stream) {
     if ((e = set_smem_once<backward_kernel<DH, true>>(K::BYTES)) != cudaSuccess) return e;
     p.out0 = static_cast<__nv_bfloat16 *>(a.dq);
     p.out1 = nullptr;
-    backward_kernel<DH, false><<<grid, kThreads, Q::BYTES, stream>>>(mq, mo, mk, mv, p);
-    if ((e = after_launch()) != cudaSuccess) return e;
+    e = launch_overlapped(backward_kernel<DH, false>, grid, kThreads, Q::BYTES, stream, mq, mo, mk, mv, p);
+    if (e != cudaSuccess || (e = after_launch()) != cudaSuccess) return e;
     p.out0 = static_cast<__nv_bfloat16 *>(a.dk);
     p.out1 = static_cast<__nv_bfloat16 *>(a.dv);
     e = launch_overlapped(backward_kernel<DH, true>, grid, kThreads, K::BYTES, stream, mk, mv, mq, mo, p);
