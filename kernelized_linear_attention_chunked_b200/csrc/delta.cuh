@@ -35,10 +35,10 @@
 // which has the same shape: Z = Z0 + W' dS with W' = X^T diag(beta c) K and
 // Z0 = scale X^T diag(beta) M^T dO.
 //
-// Measured on B200 (bf16; both launches): B2 H16 T16384 d64 174 + 315 us, B4 H8 T2048
+// Measured on B200 (bf16; both launches): B2 H16 T16384 d64 174 + 310 us, B4 H8 T2048
 // d32 19 + 31, B3 H5 T1531 d128 20 + 63. ncu at B2 H16 T4096 d64: delta_prep 59 % of
 // issue slots, tensor pipe 37 %, shared memory 63 %, its CTAs a sequence of short
-// dependent steps (32 warps per SM); delta_chain 128 CTAs of 148 SMs, 2220 cycles per
+// dependent steps (32 warps per SM); delta_chain 128 CTAs of 148 SMs, 2200 cycles per
 // chunk, of which its critical products take 640: issue 35 %, tensor 38 %, shared
 // memory 68 %.
 //
@@ -454,8 +454,9 @@ struct ChainSmem {
     static constexpr int KS = row_stride<D>();
     static constexpr int DS = kSlice + 8;  // row stride of the dO slice
     static constexpr int IN = kC * KS * (int)sizeof(Tin);
-    static constexpr int FRAG = 1024;      // one part of a 16 x 16 A operand
-    static constexpr int S = 0, YC = S + D / 16 * 2 * FRAG, SIDE = YC + kC / 16 * 2 * FRAG;
+    static constexpr int FRAG = 1024;      // a 16 x 16 A operand, or one tf32 part of it
+    // the state in two parts; the chunk's errors whole, or in three bf16 parts
+    static constexpr int S = 0, YC = S + D / 16 * 2 * FRAG, SIDE = YC + kC / 16 * 3 * FRAG / 2;
     // what passes between the chain and the side warps: E or (REV) Q^T diag(scale a) dO
     static constexpr int STAGE =
         SIDE + (REV ? D / 16 * FRAG : kC / 16 * tf::Parts<Tin>::N * FRAG);
@@ -474,15 +475,15 @@ struct ChainSmem {
 //     E^T = XV^T - S0^T W^T,  S_C^T = a_C S0^T + (c beta E)^T K,
 //     O^T = scale S0^T Q^T diag(a) + E^T M^T,
 // and an accumulator is, register for register, the A operand of the product that
-// follows. The warp that makes one cuts it into tf32 parts and leaves it in that order
-// for the others: sixteen 128-bit reads where the plain form took 32 scalar ones and cut
-// them four times over (d = 64; 341 -> 315 us at B2 H16 T16384, d = 32 33 -> 31 us
-// at B4 H8 T2048). A chunk of d = 64 takes 2220 cycles: 1120 for E, 1010 for the state and
-// the outputs' end. Bound by the length of these steps and by shared memory (1370 of those
-// cycles move data). Measured without gain: the outputs a chunk behind the chain with barriers of their
+// follows: 128-bit reads where the plain form took four times as many scalar ones (d = 64
+// 341 -> 310 us at B2 H16 T16384, d = 32 33 -> 31 us at B4 H8 T2048). The state is
+// cut into tf32 parts by the warp that makes it, the errors by their readers (the other
+// ways round: errors cut by their maker 316 us, the state by its readers too 321). A chunk
+// of d = 64 takes 2200 cycles: 1100 for E, 1000 for the state and the outputs' end. Bound by
+// the length of these steps and by shared memory (1250 of those cycles move data).
+// Measured without gain: the outputs a chunk behind the chain with barriers of their
 // own (d64 the same, d32 33 -> 36 us), their products two sixteens at a time (d32 31 -> 34),
-// operands cut by each reader (d64 315 -> 321, d128 66 -> 64), M by the copying warps
-// (d32 31 -> 34).
+// M by the copying warps (d32 31 -> 34).
 // Warps 0-3 carry the chain: they hold the state in registers (fp32, D / 4 of its rows
 // each) and take two dependent products per chunk. Warps 4-7 take the products that
 // hang off it: the outputs (forward) or Q^T dO (REV). Warps 8-11 bring K, Q and
@@ -498,10 +499,11 @@ __device__ __forceinline__ void walk_chunks(const Args &p, const Scratch &w, con
     constexpr int KP = D >= 32 ? 2 : 1;       // sixteens of k at a time
     // (c beta E)^T in three bf16 parts, for bf16 K: cutting takes longer on the critical
     // path, which pays where a warp uses a part twice (d128 68 -> 63 us at B3 H5 T1531; d64
-    // 315 -> 324 us at B2 H16 T16384)
+    // 315 -> 324 us at B2 H16 T16384; d128 with whole ones 68)
     constexpr bool CUT3 = TI == 1 && MT > 1;
     extern __shared__ __align__(16) uint8_t sm[];
-    uint4 *sS = reinterpret_cast<uint4 *>(sm + L::S), *sYc = reinterpret_cast<uint4 *>(sm + L::YC);
+    uint4 *sS = reinterpret_cast<uint4 *>(sm + L::S), *sCut = reinterpret_cast<uint4 *>(sm + L::YC);
+    float4 *sYc = reinterpret_cast<float4 *>(sm + L::YC);
     uint4 *sE = reinterpret_cast<uint4 *>(sm + L::SIDE);
     float4 *sG = reinterpret_cast<float4 *>(sm + L::SIDE);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -652,11 +654,10 @@ __device__ __forceinline__ void walk_chunks(const Args &p, const Scratch &w, con
                 return make_float4(c0_.x * x.x, c0_.y * x.y, c1_.x * x.z, c1_.y * x.w);
             };
             if constexpr (CUT3) {
-                put_cut3(sYc + rw * 96 + lane, times(y[0]), times(y[1]));
+                put_cut3(sCut + rw * 96 + lane, times(y[0]), times(y[1]));
             } else {
-                FragA<2> f;
-                f.set(times(y[0]), times(y[1]));
-                put_frag(sYc + rw * 128 + lane, f);
+                sYc[rw * 64 + lane] = times(y[0]);
+                sYc[rw * 64 + 32 + lane] = times(y[1]);
             }
             if (wantO) {
                 FragA<TI> e;
@@ -728,7 +729,7 @@ __device__ __forceinline__ void walk_chunks(const Args &p, const Scratch &w, con
 #pragma unroll
                     for (int s = 0; s < 2; ++s)
 #pragma unroll
-                        for (int j = 0; j < 3; ++j) a[s][j] = sYc[(k0 + s) * 96 + 32 * j + lane];
+                        for (int j = 0; j < 3; ++j) a[s][j] = sCut[(k0 + s) * 96 + 32 * j + lane];
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {
                         uint4 b[2];
@@ -758,7 +759,8 @@ __device__ __forceinline__ void walk_chunks(const Args &p, const Scratch &w, con
                 } else {
                     FragA<2> a[2];
 #pragma unroll
-                    for (int s = 0; s < 2; ++s) get_frag(a[s], sYc + (k0 + s) * 128 + lane);
+                    for (int s = 0; s < 2; ++s)
+                        a[s].set(sYc[(k0 + s) * 64 + lane], sYc[(k0 + s) * 64 + 32 + lane]);
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {
                         FragB<TI> b[2][2];
