@@ -10,7 +10,7 @@ import ctypes as C
 import torch
 
 from . import _binding as kb
-from ._binding import KataError, _check, _dt, _ptr
+from ._binding import KataError, _check, _dt
 from ._calls import bind, on_stream, want, workspace_for
 
 _vp, _i, _f, _sz = C.c_void_p, C.c_int, C.c_float, C.c_size_t
@@ -70,6 +70,6 @@ def prefill_backward(q, k, v, do, eps: float = 1e-6, workspace=None, stream=None
             workspace = workspace_for(L, "kata_prefill_backward_workspace_bytes",
                                       (B, H, T, d, dt), q)
         _check("kata_prefill_backward", L.kata_prefill_backward(
-            _ptr(q), _ptr(k), _ptr(v), dt, B, H, T, d, eps, _ptr(do), _ptr(dq), _ptr(dk), _ptr(dv),
-            _ptr(workspace), workspace.numel() * workspace.element_size(), s))
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), dt, B, H, T, d, eps, do.data_ptr(),
+            dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(), workspace.nbytes, s))
     return dq, dk, dv

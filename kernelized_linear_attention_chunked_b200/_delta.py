@@ -97,8 +97,8 @@ def delta_prefill(q, k, v, g, beta, scale: float | None = None, S_in=None, state
         if workspace is None:
             workspace = workspace_for(L, "kata_delta_prefill_workspace_bytes", (B, H, T, d, dt), g)
         _check("kata_delta_prefill", L.kata_delta_prefill(
-            _ptr(q), _ptr(k), _ptr(v), dt, _ptr(g), _ptr(beta), B, H, T, d, scale, _ptr(S_in),
-            _ptr(o), _ptr(S_out), _ptr(workspace), workspace.numel() * workspace.element_size(), s))
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), dt, g.data_ptr(), beta.data_ptr(), B, H, T,
+            d, scale, _ptr(S_in), _ptr(o), _ptr(S_out), workspace.data_ptr(), workspace.nbytes, s))
     return o, S_out
 
 
@@ -119,8 +119,8 @@ def delta_decode_step(q, k, v, g, beta, S, scale: float | None = None, o=None, s
         if o is None:
             o = torch.empty_like(q)
         _check("kata_delta_decode_step", lib().kata_delta_decode_step(
-            _ptr(q), _ptr(k), _ptr(v), dt, _ptr(g), _ptr(beta), B, H, d, scale, _ptr(S), _ptr(o),
-            s))
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), dt, g.data_ptr(), beta.data_ptr(), B, H, d,
+            scale, S.data_ptr(), o.data_ptr(), s))
     return o
 
 
@@ -155,7 +155,8 @@ def delta_backward(q, k, v, g, beta, do, scale: float | None = None, S_in=None, 
         if workspace is None:
             workspace = workspace_for(L, "kata_delta_backward_workspace_bytes", (B, H, T, d, dt), g)
         _check("kata_delta_backward", L.kata_delta_backward(
-            _ptr(q), _ptr(k), _ptr(v), dt, _ptr(g), _ptr(beta), B, H, T, d, scale, _ptr(S_in),
-            _ptr(do), _ptr(dS), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), _ptr(db), _ptr(dS_in),
-            _ptr(workspace), workspace.numel() * workspace.element_size(), s))
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), dt, g.data_ptr(), beta.data_ptr(), B, H, T,
+            d, scale, _ptr(S_in), do.data_ptr(), _ptr(dS), dq.data_ptr(), dk.data_ptr(),
+            dv.data_ptr(), dg.data_ptr(), db.data_ptr(), _ptr(dS_in), workspace.data_ptr(),
+            workspace.nbytes, s))
     return dq, dk, dv, dg, db, dS_in
