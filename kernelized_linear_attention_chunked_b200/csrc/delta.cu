@@ -47,7 +47,7 @@ cudaError_t prefill_t(const Args &p, const Scratch &w, long heads, int d, cudaSt
 // so one pass reads it into registers, one exchange joins the row sums, and the
 // same registers are updated and written back. Measured: B64 H16 d128 bf16 (134 MB of
 // state traffic) 19.9 us, 6.7 TB/s (the copy bandwidth); B64 H16 d64 the call's host
-// time, 11 us. A CTA takes CW columns of one
+// time, 10 us. A CTA takes CW columns of one
 // head, a thread float4s of one column group, RPP rows apart.
 template <typename Tin, int D>
 struct StepCfg {
