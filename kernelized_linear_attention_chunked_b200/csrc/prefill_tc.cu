@@ -645,6 +645,12 @@ __global__ void __launch_bounds__(ReadCfg<DH, NIR>::THREADS, 2)
             for (int s = 0; ok && s < first_p; ++s) ok = load_p(s);
             for (int u = 1; ok && u < n_half / 2; ++u) ok = load_kv(u);
             for (int s = first_p; ok && s < n_inter; ++s) ok = load_p(s);
+            // Where no CTA has a snapshot to read, or one gave up before its own, the grid
+            // waits all the same: a kernel that is launched to start early behind it waits
+            // for this grid alone, and takes its end for the end of the state kernel too,
+            // which reads k and v and writes the last state. (One CTA's wait keeps a grid
+            // from ending, so CTAs without snapshots beside some with them go on.)
+            if (p.nint == 1 || !ok) grid_dependency_wait();
             // no copy may still be in flight when the CTA exits. A copy is only
             // issued once the previous phase of its barrier completed, so the
             // last copy issued on each barrier is the only one to wait for.

@@ -105,7 +105,10 @@ inline cudaError_t set_smem_once(int bytes) {
 
 // Launch a kernel that may start while the one before it in the stream still runs;
 // it waits for it itself (grid_dependency_wait), and does so before it lets a kernel
-// start that reads its inputs without waiting. This hides the launch, and costs the
+// start that reads its inputs without waiting. That wait covers the one grid before it,
+// so every grid launched in this way has to wait on every path that it can take, at least
+// in one CTA and before that one ends: only then is its own end the end of all that the
+// stream ran before. This hides the launch, and costs the
 // host 0.5 us less than <<<>>> (a decode step of 58 MB 12.4 -> 10.9 us a call).
 template <class... P, class... A>
 inline cudaError_t launch_overlapped(void (*kern)(P...), unsigned grid, int threads, int bytes,
