@@ -72,9 +72,8 @@ __device__ __forceinline__ float4 shfl4(float4 x, int off) {
 
 template <typename Tin, int D>
 __global__ void __launch_bounds__(StepCfg<Tin, D>::THREADS)
-    delta_step(const Tin *__restrict__ q, const Tin *__restrict__ k, const Tin *__restrict__ v,
-               const float *__restrict__ g, const float *__restrict__ beta, float scale,
-               float *__restrict__ S, Tin *__restrict__ o) {
+    delta_step(const Tin *q, const Tin *k, const Tin *v, const float *g, const float *beta, float scale,
+               float *S, Tin *o) {
     using L = StepCfg<Tin, D>;
     constexpr int PARTS = D / L::CW;
     __shared__ float4 redr[L::NW][L::CG], redp[L::NW][L::CG];
@@ -84,8 +83,11 @@ __global__ void __launch_bounds__(StepCfg<Tin, D>::THREADS)
     const size_t head = blockIdx.x / PARTS;
     const int c0 = (int)(blockIdx.x % PARTS) * L::CW + 4 * cg;
     float *Sh = S + head * (size_t)(D * D) + c0;
+    // Whatever the stream ran before may still be writing any of these tensors (q may be the
+    // o of the step before): no __restrict__, which would allow loads ahead of the wait or
+    // through the read-only cache.
     if (tid == 0) sm100::launch_dependents();
-    sm100::grid_dependency_wait();  // whatever the stream ran before
+    sm100::grid_dependency_wait();
     float4 s[L::ROWS];
 #pragma unroll
     for (int i = 0; i < L::ROWS; ++i)

@@ -13,6 +13,7 @@ from _delta_ref import delta_inputs
 
 pytestmark = pytest.mark.gpu
 
+DTYPES = [torch.float32, torch.bfloat16]
 NAMES = ("q", "k", "v", "g", "beta")
 
 
@@ -27,6 +28,72 @@ def same(run, repeats=3):
         got = run(lambda: None)
         kata.sync_status()
         assert len(got) == len(want) and all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("B,H,d", [(64, 16, 128), (40, 7, 64), (1, 1, 16)])
+def test_steps_in_a_row(dtype, B, H, d):
+    # many steps on one state, several waves of blocks each, and each one's q and v are
+    # what the two before it have just written
+    x = delta_inputs(B, H, 10, d, dtype, seed=d)
+    tokens = [token(x, t) for t in range(10)]
+    S = torch.empty_like(x["S"])
+
+    def run(pause):
+        S.copy_(x["S"])
+        outs = [torch.empty_like(tokens[0]["q"]) for _ in tokens]
+        pause()
+        for i, t in enumerate(tokens):
+            q = outs[i - 1] if i > 0 else t["q"]
+            v = outs[i - 2] if i > 1 else t["v"]
+            kata.delta_decode_step(q, t["k"], v, t["g"], t["beta"], S, o=outs[i])
+            pause()
+        return [S.clone(), *outs]
+
+    same(run)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_step_then_everything(dtype):
+    # what reads a step's output or state, or overwrites its inputs, right behind it
+    B, H, T, d = 16, 8, 130, 64
+    x = delta_inputs(B, H, T, d, dtype, seed=3)
+    tokens = [token(x, t) for t in range(6)]
+    seq = [x[n] for n in NAMES]
+    S = torch.empty_like(x["S"])
+
+    def run(pause):
+        S.copy_(x["S"])
+        outs = [torch.empty_like(tokens[0]["q"]) for _ in tokens]
+        o = torch.empty_like(x["q"])
+        pause()
+
+        def step(i):
+            t = tokens[i]
+            kata.delta_decode_step(*t.values(), S, o=outs[i])
+            pause()
+
+        one = lambda t: t.unsqueeze(2)  # a sequence of one token
+        step(0)
+        kata.delta_prefill(*seq, S_in=S, S_out=S, o=o)
+        pause()
+        step(1)
+        g1 = kata.delta_backward(one(outs[1]), *(one(tokens[1][n]) for n in NAMES[1:]), one(outs[0]),
+                                 S_in=S, dS=S, state_grad=True)
+        pause()
+        step(2)
+        g2 = kata.prefill_backward(one(outs[2]), one(tokens[2]["k"]), one(outs[1]), one(outs[0]))
+        pause()
+        step(3)
+        g3 = kata.delta_backward(*seq, o, S_in=S)
+        pause()
+        step(4)
+        g4 = kata.prefill_backward(x["q"], x["k"], x["v"], o)
+        pause()
+        step(5)
+        return [S.clone(), o, *outs, *g1, *g2, *g3[:5], *g4]
+
+    same(run)
 
 
 @pytest.mark.parametrize("form", ["chunked", "auto"])
