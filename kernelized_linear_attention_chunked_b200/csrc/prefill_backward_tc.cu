@@ -14,8 +14,8 @@
 //
 // Tensor memory (512 columns, one CTA per SM): three buffers of S (64 fp32
 // columns) and dP (64), then the accumulators. The workers overwrite S with P
-// and dP with dS as bf16 pairs, in place, and the output products take them
-// from there as A operands. A streamed tile serves both products it is needed
+// and dP with dS as bf16 pairs, in place, sixteen columns with eight of upper parts and
+// eight of lower ones, and the output products take them from there as A operands. A streamed tile serves both products it is needed
 // in: [64 rows, d] in rows of 2 d bytes, swizzled by that width, is a K-major
 // operand for the scores and an MN-major one for the outputs.
 //
@@ -24,18 +24,18 @@
 // thread needs longer for a step's waits and MMAs than the tensor pipe), one of the
 // output products, a TMA producer. Every wait is bounded.
 //
-// Rounding: scores, dP, den and delta are fp32 or wider. P is rounded to bf16 as
-// an operand (its terms add up without cancelling: dV's error is 1.4 times its own
-// last rounding). dS is a difference whose terms do cancel in dQ and dK, so it goes
-// in as two bf16 parts (16 bits): with one, dQ and dK were off by up to 3.1e-3 of
-// their norm, with two by 1.7e-3, the last rounding alone (12 % more time). The
+// Rounding: scores, dP, den and delta are fp32 or wider. P and dS go in as two bf16
+// parts each (16 bits), so that the gradients are off by little more than their last
+// rounding, 1.66e-3 of their norm. With one part dV was off by 2.3e-3, and dQ and dK, whose
+// terms cancel, by up to 3.1e-3 (the second part of P costs 6 % of the time, that of dS
+// 12 %). The
 // rows of the first 128 queries sum den and delta in 64 bits, and delta is two
 // floats: with few keys dP - delta is a small difference. It stays exact because
 // S and dP come out of the same products with the same bits in both modes and
 // both walks.
 //
 // Measured on B200 at B2 H8 T8192 d64 (344 GFLOP as five products per causal
-// pair; nine and a half are run): queries 482 us, keys 415 us, 383 TFLOP/s of the
+// pair; twelve are run: six in either mode, P and dS counting twice): queries 482 us, keys 415 us, 383 TFLOP/s of the
 // five. What bounds it: the keys' workers, which read two statistics per column
 // from shared memory (1700 of the 4000 cycles that a buffer is in use), and for the
 // queries the single threads that issue the products (66 cycles per MMA against 48
@@ -56,6 +56,8 @@ constexpr int kGroups = 2 * kSets;  // a set is two groups of four warps, half t
 constexpr int kWorkerWarps = 4 * kGroups;
 static_assert(kStages == 2 * kBufs && kStages % kSets == 0, "slots of a step");
 constexpr int kThreads = 32 * (kWorkerWarps + 4);
+// Sixteen columns of S (dP) become the upper parts of P (dS) and, eight columns on, the lower.
+constexpr uint32_t kLower = 8;
 
 constexpr uint32_t kSwizzle32 = 6;  // rows of 32 bytes, 16-byte chunks swapped every four rows
 
@@ -97,9 +99,6 @@ struct BwdCfg {
     // over half an SM's shared memory: a second CTA could not have tensor memory
     static constexpr int BYTES = NEED > 118 * 1024 ? NEED : 118 * 1024;
     static constexpr uint32_t ACC = 128 * kBufs;             // first accumulator column
-    // columns of a group's parts in its half of a buffer: dS's upper part at 64 ..
-    // 79, P (keys) at 0 .. 15, dS's lower part where neither is
-    static constexpr uint32_t DS_LO = KEYS ? 64 + 16 : 0;
     static_assert(ACC + 2 * DH <= 512, "tensor-memory budget");
     static_assert(SLOT % 8 == 0 && BAR % 8 == 0, "barriers");
     static constexpr int S_WARP = kWorkerWarps, O_WARP = S_WARP + kSets, TMA_WARP = O_WARP + 1;
@@ -145,6 +144,13 @@ __device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
     F2 r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
     return r;
+}
+
+// Two values as bf16 pairs: rounded, and what the rounding left.
+__device__ __forceinline__ void cut2(F2 x, uint32_t &up, uint32_t &low) {
+    const float2 v = un(x);
+    up = pack_bf16x2(v.x, v.y);
+    low = pack_bf16x2(v.x - __uint_as_float(up << 16), v.y - __uint_as_float(up & 0xFFFF0000u));
 }
 
 template <int DH, bool KEYS>
@@ -280,17 +286,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 const uint64_t t0 = db + (uint32_t)(st * (L::STAGE >> 4)), t1 = t0 + (L::TILE >> 4);
                 const uint32_t buf = tmem + 128 * (st >= kBufs ? st - kBufs : st);
-                // 16 rows on; a group's columns lie in its own half
-                auto a = [&](int kk) { return buf + 8 * kk + (kk < 2 ? 0 : 16); };
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                    mma_ts(tmem + L::ACC, a(kk) + L::DS_LO, t0 + kk * L::ROW, id, s > n1 || kk > 0);
-                    mma_ts(tmem + L::ACC, a(kk) + 64, t0 + kk * L::ROW, id, 1);
+                for (int kk = 0; kk < 4; ++kk) {  // 16 rows on; the lower parts first
+                    const uint32_t a = buf + 16 * kk + 64;
+                    mma_ts(tmem + L::ACC, a + kLower, t0 + kk * L::ROW, id, s > n1 || kk > 0);
+                    mma_ts(tmem + L::ACC, a, t0 + kk * L::ROW, id, 1);
                 }
                 if (KEYS) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_ts(tmem + L::ACC + DH, a(kk), t1 + kk * L::ROW, id, s > n1 || kk > 0);
+                    for (int kk = 0; kk < 4; ++kk) {
+                        const uint32_t a = buf + 16 * kk;
+                        mma_ts(tmem + L::ACC + DH, a + kLower, t1 + kk * L::ROW, id, s > n1 || kk > 0);
+                        mma_ts(tmem + L::ACC + DH, a, t1 + kk * L::ROW, id, 1);
+                    }
                 }
                 mma_commit(&bar[kOver + st]);
                 if (++st == kStages) st = 0;
@@ -407,7 +415,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float *stats = reinterpret_cast<const float *>(sm + L::STREAM + st * L::STAGE + L::STATS);
             const bool few = KEYS ? step < 2 : tile == 0;  // rows that may see few keys
             uint32_t sv[2][16], dv[2][16];
-            uint32_t low[KEYS ? 2 : 1][8];
             load(b, half, sv[0], dv[0]);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
@@ -416,8 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 arrived(x, y);
                 if (c == 0) load(b, half + 16, sv[1], dv[1]);
                 if (on_diagonal(step)) mask(step * kStep + half + 16 * c, x);
-                uint32_t pk[8], dk[8];
-                uint32_t(&dl_)[8] = low[KEYS ? c : 0];
+                uint32_t pu[8], pl[8], du[8], dl_[8];  // upper and lower parts of P and dS
 #pragma unroll
                 for (int e = 0; e < 16; e += 4) {
                     float4 iv = make_float4(inv, inv, inv, inv), dh = make_float4(dhi, dhi, dhi, dhi);
@@ -435,26 +441,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                         F2 t = add(f2(y[e + 2 * h], y[e + 2 * h + 1]),
                                    h ? f2(dh.z, dh.w) : f2(dh.x, dh.y));
                         if (few) t = add(t, h ? f2(dl.z, dl.w) : f2(dl.x, dl.y));
-                        const float2 ds = un(mul(w, t));
-                        const uint32_t up = pack_bf16x2(ds.x, ds.y);
-                        dk[e / 2 + h] = up;
-                        dl_[e / 2 + h] = pack_bf16x2(ds.x - __uint_as_float(up << 16),
-                                                     ds.y - __uint_as_float(up & 0xFFFF0000u));
-                        if (KEYS) {
-                            const float2 pp = un(mul(v, w));
-                            pk[e / 2 + h] = pack_bf16x2(pp.x, pp.y);
-                        }
+                        cut2(mul(w, t), du[e / 2 + h], dl_[e / 2 + h]);
+                        if (KEYS) cut2(mul(v, w), pu[e / 2 + h], pl[e / 2 + h]);
                     }
                 }
-                // over columns of this group's half that have been read by now
-                if (KEYS) tmem_st8(lanes + 128 * b + half + 8 * c, pk);
-                tmem_st8(lanes + 128 * b + 64 + half + 8 * c, dk);
-                if (!KEYS) {
-                    tmem_st8(lanes + 128 * b + L::DS_LO + half + 8 * c, low[0]);
-                } else if (c == 1) {  // over the second sixteen columns of dP
-                    tmem_st8(lanes + 128 * b + L::DS_LO + half, low[0]);
-                    tmem_st8(lanes + 128 * b + L::DS_LO + half + 8, low[KEYS ? 1 : 0]);
+                // over the sixteen columns of S and of dP that these come from
+                const uint32_t at = lanes + 128 * b + half + 16 * c;
+                if (KEYS) {
+                    tmem_st8(at, pu);
+                    tmem_st8(at + kLower, pl);
                 }
+                tmem_st8(at + 64, du);
+                tmem_st8(at + 64 + kLower, dl_);
             }
             tmem_st_wait();
             tc_fence_before();
