@@ -43,8 +43,10 @@
 // memory 68 %.
 //
 // All products keep fp32 accuracy by split tf32 operands (mma_tf32.cuh): the
-// state, its gradient, dg and dbeta are fp32 results. Only o of bf16 inputs,
-// rounded to bf16 at the end, takes the one-part form.
+// state, its gradient, dg and dbeta are fp32 results. Only Q S0 and M E of bf16 inputs,
+// which go into an o that is rounded to 8 bits next, take operands of 16 bits (two bf16
+// parts): o is then off by its own rounding, 1.66e-3 of its norm. (With one tf32 part of
+// each, 11 bits, it was 1.75e-3 to 1.81e-3.)
 #pragma once
 
 #include "kata_common.cuh"
@@ -76,7 +78,8 @@ constexpr int row_stride() {
 struct Scratch {
     float *W;     // [chunks][64 D], fragment order
     float *Y;     // [chunks][64 D], fragment order: XV, or Z0
-    float *M;     // [chunks][64 * 64], fragment order: scale M diag(beta)
+    float *M;     // [chunks][64 * 64], fragment order: scale M diag(beta); bf16 inputs: each
+                  // two neighbours as two pairs of bf16 parts
     float *coef;  // [chunks][kCoef]
 };
 
@@ -389,7 +392,15 @@ __global__ void __launch_bounds__(256, PrepSmem<Tin, D, BACK>::CTAS)
             }
             if (!BACK && wantQ) {
                 const float s0 = p.scale * be.x, s1 = p.scale * be.y;
-                d[(2 * nt + hf) * 32] = make_float4(s0 * m[0], s1 * m[1], s0 * m[2], s1 * m[3]);
+                float4 x = make_float4(s0 * m[0], s1 * m[1], s0 * m[2], s1 * m[3]);
+                if constexpr (TI == 1) {
+                    uint32_t u[2], v[2];
+                    cut(x.x, x.y, u);
+                    cut(x.z, x.w, v);
+                    x = make_float4(__uint_as_float(u[0]), __uint_as_float(u[1]), __uint_as_float(v[0]),
+                                    __uint_as_float(v[1]));
+                }
+                d[(2 * nt + hf) * 32] = x;
             }
         }
     }
@@ -458,8 +469,8 @@ struct ChainSmem {
     // the state in two parts; the chunk's errors whole, or in three bf16 parts
     static constexpr int S = 0, YC = S + D / 16 * 2 * FRAG, SIDE = YC + kC / 16 * 3 * FRAG / 2;
     // what passes between the chain and the side warps: E or (REV) Q^T diag(scale a) dO
-    static constexpr int STAGE =
-        SIDE + (REV ? D / 16 * FRAG : kC / 16 * tf::Parts<Tin>::N * FRAG);
+    static constexpr int SB = SIDE + (REV ? D / 16 * FRAG : kC / 16 * tf::Parts<Tin>::N * FRAG);
+    static constexpr int STAGE = SB + (REV || sizeof(Tin) == 4 ? 0 : D / 16 * FRAG);
     // one stage: K, Q, coefficients, (REV) the dO slice
     static constexpr int K = 0, Q = IN, COEF = 2 * IN, DO = COEF + kCoef * 4;
     static constexpr int STAGE_BYTES = DO + (REV ? kC * DS * (int)sizeof(Tin) : 0);
@@ -478,7 +489,10 @@ struct ChainSmem {
 // follows: 128-bit reads where the plain form took four times as many scalar ones (d = 64
 // 341 -> 310 us at B2 H16 T16384, d = 32 33 -> 31 us at B4 H8 T2048). The state is
 // cut into tf32 parts by the warp that makes it, the errors by their readers (the other
-// ways round: errors cut by their maker 316 us, the state by its readers too 321). A chunk
+// ways round: errors cut by their maker 316 us, the state by its readers too 321). For the
+// outputs of bf16 inputs that warp cuts state and errors into bf16 parts as well, and
+// delta_prep cuts M (B2 H16 T16384 d64, both launches: 486 us; the state's tf32 parts read for
+// them instead 535, M cut by its readers 530 to 544). A chunk
 // of d = 64 takes 2200 cycles: 1100 for E, 1000 for the state and the outputs' end. Bound by
 // the length of these steps and by shared memory (1250 of those cycles move data).
 // Measured without gain: the outputs a chunk behind the chain with barriers of their
@@ -505,6 +519,7 @@ __device__ __forceinline__ void walk_chunks(const Args &p, const Scratch &w, con
     uint4 *sS = reinterpret_cast<uint4 *>(sm + L::S), *sCut = reinterpret_cast<uint4 *>(sm + L::YC);
     float4 *sYc = reinterpret_cast<float4 *>(sm + L::YC);
     uint4 *sE = reinterpret_cast<uint4 *>(sm + L::SIDE);
+    uint4 *sSb = reinterpret_cast<uint4 *>(sm + L::SB);
     float4 *sG = reinterpret_cast<float4 *>(sm + L::SIDE);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int gr = lane >> 2, t2 = 2 * (lane & 3), rw = warp & 3;
@@ -569,6 +584,11 @@ __device__ __forceinline__ void walk_chunks(const Args &p, const Scratch &w, con
             FragA<2> f;
             f.set(top(S[mt]), bottom(S[mt]));
             put_frag(sS + (MT * warp + mt) * 128 + lane, f);
+            if (TI == 1 && wantO) {
+                PartsA<2> h;
+                h.set(top(S[mt]), bottom(S[mt]));
+                h.put(sSb + (MT * warp + mt) * 64 + lane);
+            }
         }
     };
     if (owns) {
@@ -654,15 +674,23 @@ __device__ __forceinline__ void walk_chunks(const Args &p, const Scratch &w, con
                 return make_float4(c0_.x * x.x, c0_.y * x.y, c1_.x * x.z, c1_.y * x.w);
             };
             if constexpr (CUT3) {
-                put_cut3(sCut + rw * 96 + lane, times(y[0]), times(y[1]));
+                PartsA<3> f;
+                f.set(times(y[0]), times(y[1]));
+                f.put(sCut + rw * 96 + lane);
             } else {
                 sYc[rw * 64 + lane] = times(y[0]);
                 sYc[rw * 64 + 32 + lane] = times(y[1]);
             }
             if (wantO) {
-                FragA<TI> e;
-                e.set(y[0], y[1]);
-                put_frag(sE + rw * (64 * TI) + lane, e);
+                if constexpr (TI == 1) {
+                    PartsA<2> e;
+                    e.set(y[0], y[1]);
+                    e.put(sE + rw * 64 + lane);
+                } else {
+                    FragA<2> e;
+                    e.set(y[0], y[1]);
+                    put_frag(sE + rw * 128 + lane, e);
+                }
             }
             if (KEEP) {
                 float *d = p.keepY + ((ch0 + c) * kC + m0 + t2) * D + c0 + gr;
@@ -679,13 +707,23 @@ __device__ __forceinline__ void walk_chunks(const Args &p, const Scratch &w, con
             clear(o);
 #pragma unroll 1
             for (int ks = 0; ks < D / 16; ++ks) {
-                FragA<TI> a[1];
-                FragB<TI> b[1][2];
-                get_frag(a[0], sS + ks * 128 + lane);
-                const Quads x = quads<true>(sQ + m0 * KS, KS, 16 * ks);
-                b[0][0].set(x.a);
-                b[0][1].set(x.b);
-                mma_step<TI, TI, 2, 1>(o, a, b);
+                if constexpr (TI == 1) {
+                    PartsA<2> a;
+                    PartsB<1> b[2];
+                    a.get(sSb + ks * 64 + lane);
+                    const uint4 x = pairs<true>(sQ + m0 * KS, KS, 16 * ks);
+                    b[0].set(make_uint2(x.x, x.y));
+                    b[1].set(make_uint2(x.z, x.w));
+                    mma_parts<1, 2>(o, a, b);
+                } else {
+                    FragA<2> a[1];
+                    FragB<2> b[1][2];
+                    get_frag(a[0], sS + ks * 128 + lane);
+                    const Quads x = quads<true>(sQ + m0 * KS, KS, 16 * ks);
+                    b[0][0].set(x.a);
+                    b[0][1].set(x.b);
+                    mma_step<2, 2, 2, 1>(o, a, b);
+                }
             }
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt) {
@@ -800,11 +838,23 @@ __device__ __forceinline__ void walk_chunks(const Args &p, const Scratch &w, con
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
                 if (ks > rw) continue;
-                FragA<TI> a[1];
-                FragB<TI> b[1][2];
-                get_frag(a[0], sE + ks * (64 * TI) + lane);
-                frag_w(b[0], ks);
-                mma_step<TI, TI, 2, 1>(o, a, b);
+                if constexpr (TI == 1) {
+                    PartsA<2> a;
+                    PartsB<2> b[2];
+                    a.get(sE + ks * 64 + lane);
+                    const float4 w0 = W[2 * ks], w1 = W[2 * ks + 1];
+                    b[0].p[0] = make_uint2(__float_as_uint(w0.x), __float_as_uint(w1.x));
+                    b[0].p[1] = make_uint2(__float_as_uint(w0.y), __float_as_uint(w1.y));
+                    b[1].p[0] = make_uint2(__float_as_uint(w0.z), __float_as_uint(w1.z));
+                    b[1].p[1] = make_uint2(__float_as_uint(w0.w), __float_as_uint(w1.w));
+                    mma_parts<2, 2>(o, a, b);
+                } else {
+                    FragA<2> a[1];
+                    FragB<2> b[1][2];
+                    get_frag(a[0], sE + ks * 128 + lane);
+                    frag_w(b[0], ks);
+                    mma_step<2, 2, 2, 1>(o, a, b);
+                }
             }
             if (i + 1 < p.nc) load_frags();
             Tin *od = static_cast<Tin *>(p.o);

@@ -7,9 +7,9 @@
 // which leaves out lo_a lo_b (2^-22 of the product) and lo's own rounding
 // (2^-21): the products are as good as fp32 ones. A value that came from bf16
 // is its own hi (8 bits), so that operand needs no lo: TA / TB below say how
-// many parts (1 or 2) an operand is cut into. One part of a general fp32
-// operand is a rounding to 11 bits (toward zero, at most 2^-10), used only
-// where the result is rounded to bf16 (2^-8) next.
+// many parts (1 or 2) an operand is cut into; an operand with values of its own
+// fp32 bits always takes two. What goes into a result that is rounded to bf16 next may
+// be cut into two bf16 parts instead (mma_parts below).
 //
 // Measured on B200: one m16n8k8 tf32 (or m16n8k16 bf16) mma.sync per 8 cycles
 // and SM quadrant, latency 20.6 cycles; three bf16 parts would need as many
@@ -189,13 +189,12 @@ __device__ __forceinline__ float4 quad(const float *p, int stride, int mn, int k
 __device__ __forceinline__ float2 unpack(uint32_t u) {
     return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
 }
+// bf16: as pairs (k, k + 1 and k + 8, k + 9), or unpacked.
 template <bool K>
-__device__ __forceinline__ float4 quad(const __nv_bfloat16 *p, int stride, int mn, int k) {
-    if (K) {
-        const float2 a = unpack(*reinterpret_cast<const uint32_t *>(p + mn * stride + k));
-        const float2 b = unpack(*reinterpret_cast<const uint32_t *>(p + mn * stride + k + 8));
-        return make_float4(a.x, a.y, b.x, b.y);
-    }
+__device__ __forceinline__ uint2 pair(const __nv_bfloat16 *p, int stride, int mn, int k) {
+    if (K)
+        return make_uint2(*reinterpret_cast<const uint32_t *>(p + mn * stride + k),
+                          *reinterpret_cast<const uint32_t *>(p + mn * stride + k + 8));
     // a transposed 16 x 8 matrix load: lanes 0 .. 15 name the rows, and lane (g, t)
     // gets rows 2t, 2t + 1 and 2t + 8, 2t + 9 of column g. Every lane of the warp
     // asks for the same mn - g and k - 2t; rows are 16-byte aligned.
@@ -207,7 +206,12 @@ __device__ __forceinline__ float4 quad(const __nv_bfloat16 *p, int stride, int m
                  : "=r"(u), "=r"(v)
                  : "r"(at)
                  : "memory");
-    const float2 a = unpack(u), b = unpack(v);
+    return make_uint2(u, v);
+}
+template <bool K>
+__device__ __forceinline__ float4 quad(const __nv_bfloat16 *p, int stride, int mn, int k) {
+    const uint2 u = pair<K>(p, stride, mn, k);
+    const float2 a = unpack(u.x), b = unpack(u.y);
     return make_float4(a.x, a.y, b.x, b.y);
 }
 // The quads of rows or columns g and g + 8 at once; p and k: the sixteen's start.
@@ -250,12 +254,16 @@ __device__ __forceinline__ Quads quads(const __nv_bfloat16 *p, int stride, int k
     return {make_float4(a.x, a.y, b.x, b.y), make_float4(c.x, c.y, d.x, d.y)};
 }
 
-// An A operand cut into three bf16 parts (24 bits and more), for products with bf16
-// values: three m16n8k16 instead of four m16n8k8 of two tf32 parts, three quarters of the
-// bytes, and the bf16 side needs no unpacking.
-__device__ __forceinline__ void cut3(float x, float y, uint32_t (&part)[3]) {
+// Operands cut into bf16 parts, for m16n8k16 products: three parts (24 bits and more) of an
+// fp32 value against bf16 values take three of those instead of four m16n8k8 of two tf32
+// parts, with three quarters of the bytes, and the bf16 side needs no unpacking. Two parts
+// (16 bits) are for what goes into a result that is rounded to bf16 next: against bf16
+// values two products, against two parts three, where one tf32 part each (11 bits, off by
+// up to 2^-10) takes two.
+template <int P>
+__device__ __forceinline__ void cut(float x, float y, uint32_t (&part)[P]) {
 #pragma unroll
-    for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < P; ++i) {
         const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
         part[i] = *reinterpret_cast<const uint32_t *>(&h);
         const float2 f = unpack(part[i]);
@@ -263,14 +271,60 @@ __device__ __forceinline__ void cut3(float x, float y, uint32_t (&part)[3]) {
         y -= f.y;
     }
 }
-__device__ __forceinline__ void put_cut3(uint4 *p, float4 top, float4 bottom) {
-    uint32_t a[4][3];
-    cut3(top.x, top.y, a[0]);
-    cut3(bottom.x, bottom.y, a[1]);
-    cut3(top.z, top.w, a[2]);
-    cut3(bottom.z, bottom.w, a[3]);
+// A 16 x 16 A operand: four k of row g and of row g + 8
+template <int P>
+struct PartsA {
+    uint4 p[P];
+    __device__ __forceinline__ void set(float4 top, float4 bottom) {
+        uint32_t a[4][P];
+        cut(top.x, top.y, a[0]);
+        cut(bottom.x, bottom.y, a[1]);
+        cut(top.z, top.w, a[2]);
+        cut(bottom.z, bottom.w, a[3]);
 #pragma unroll
-    for (int i = 0; i < 3; ++i) p[32 * i] = make_uint4(a[0][i], a[1][i], a[2][i], a[3][i]);
+        for (int i = 0; i < P; ++i) p[i] = make_uint4(a[0][i], a[1][i], a[2][i], a[3][i]);
+    }
+    // one row of 32 lanes per part
+    __device__ __forceinline__ void put(uint4 *d) const {
+#pragma unroll
+        for (int i = 0; i < P; ++i) d[32 * i] = p[i];
+    }
+    __device__ __forceinline__ void get(const uint4 *d) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) p[i] = d[32 * i];
+    }
+};
+// A 16 x 8 B operand: four k of column g; P = 1: bf16 pairs as they are
+template <int P>
+struct PartsB {
+    uint2 p[P];
+    __device__ __forceinline__ void set(float4 v) {
+        uint32_t a[2][P];
+        cut(v.x, v.y, a[0]);
+        cut(v.z, v.w, a[1]);
+#pragma unroll
+        for (int i = 0; i < P; ++i) p[i] = make_uint2(a[0][i], a[1][i]);
+    }
+    __device__ __forceinline__ void set(uint2 v) { p[0] = v; }
+};
+// acc += A B over sixteen k, A in two parts: summed from zero, the small parts first, as in
+// mma_step.
+template <int PB, int NT>
+__device__ __forceinline__ void mma_parts(float (&acc)[NT][4], const PartsA<2> &a,
+                                          const PartsB<PB> (&b)[NT]) {
+    float t[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) mma16_0(t[n], a.p[1], b[n].p[0].x, b[n].p[0].y);
+    if (PB == 2) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma16(t[n], a.p[0], b[n].p[PB - 1].x, b[n].p[PB - 1].y);
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) mma16(t[n], a.p[0], b[n].p[0].x, b[n].p[0].y);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[n][i] += t[n][i];
 }
 
 // Lane (g, t) holds columns 2t, 2t + 1 of row g of an 8 x 8 tile (bf16: in one
@@ -311,6 +365,26 @@ __device__ __forceinline__ void gemm(float (&acc)[NT][4], int s0, int s1, FA fa,
             for (int n = 0; n < G; ++n)
                 if (n0 + n < nt_end) b[0][n].set(fb(8 * (n0 + n) + g, k));
             mma_step<TA, TB, G, 1>(*reinterpret_cast<float(*)[G][4]>(&acc[n0]), a, b, nt_end - n0);
+        }
+    }
+}
+
+// The same with A in two bf16 parts, B in PB: fb gives a quad (PB = 2) or bf16 pairs (1).
+template <int PB, int NT, class FA, class FB>
+__device__ __forceinline__ void gemm_parts(float (&acc)[NT][4], int s0, int s1, FA fa, FB fb) {
+    const int g = (threadIdx.x & 31) >> 2, t2 = 2 * (threadIdx.x & 3);
+    constexpr int G = NT % 2 == 0 ? 2 : 1;
+#pragma unroll 1
+    for (int st = s0; st < s1; ++st) {
+        const int k = 16 * st + t2;
+        PartsA<2> a;
+        a.set(fa(g, k), fa(g + 8, k));
+#pragma unroll
+        for (int n0 = 0; n0 < NT; n0 += G) {
+            PartsB<PB> b[G];
+#pragma unroll
+            for (int n = 0; n < G; ++n) b[n].set(fb(8 * (n0 + n) + g, k));
+            mma_parts<PB, G>(*reinterpret_cast<float(*)[G][4]>(&acc[n0]), a, b);
         }
     }
 }

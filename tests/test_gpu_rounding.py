@@ -13,14 +13,29 @@ of the products' absolute sums; a row's 1 / den and delta as much again. So, wit
     dK: |n| <= sum_i (2^-15 |dS| + 2^-19 2 (|S| |dP - delta| + |s| (|dP| + |delta|)) / den) |q_i|
 and dQ likewise. An operand rounded to 8 bits is off by up to 2^-8: small elements that
 are sums of large ones fail.
+
+The delta rule's are held by a norm. A result differs from the rounded 64-bit value only
+where its error carries it over a border between two roundings, and then by one step. With
+steps u_i <= 2^-7 |x_i| and values that lie evenly between the borders, that is the case
+with probability |n_i| / u_i, so the expected square of the difference is sum |n_i| u_i <=
+2^-7 |n| |x|: relative to |x| it is sqrt(2^-7 |n| / |x|). Operands in two bf16 parts give
+|n| / |x| <= 2^-15 (twice their 2^-16, for sums that cancel a little), operands in two tf32
+parts less: sqrt(2^-22) = 2^-11. With 24 such elements or more expected, a sample's norm is
+at most 1.35 times the expected one (four standard deviations). Operands cut to 11 bits
+(2^-10) would give 2^-9.
 """
 import pytest
 import torch
 
 import kernelized_linear_attention_chunked_b200 as kata
-from _delta_ref import prefill_grads
+from _delta_ref import delta_forward, delta_inputs, prefill_grads, rel
 
 pytestmark = pytest.mark.gpu
+
+
+def check(got, want, name=""):
+    assert got.dtype == torch.bfloat16
+    assert rel(got, want.to(torch.bfloat16)) < 1.35 * 2**-11, name
 
 
 def prefill_errors(q, k, v, do, eps):
@@ -48,3 +63,22 @@ def test_prefill_gradients(B, H, T, d):
         assert a.dtype == torch.bfloat16
         over = (a.double() - b).abs() - (2**-8 * (b.abs() + e) + e)
         assert not (over > 0).any(), (name, int((over > 0).sum()), a.numel())
+
+
+@pytest.mark.parametrize("d", [16, 32, 64, 128])
+@pytest.mark.parametrize("B,H,T", [(2, 3, 63), (2, 3, 200), (1, 2, 1000)])
+def test_delta_prefill(B, H, T, d):
+    x = delta_inputs(B, H, T, d, torch.bfloat16, seed=T + d)
+    o, _ = kata.delta_prefill(x["q"], x["k"], x["v"], x["g"], x["beta"], S_in=x["S"])
+    kata.sync_status()
+    check(o, delta_forward(x["q"], x["k"], x["v"], x["g"], x["beta"], d**-0.5, x["S"])[0])
+
+
+@pytest.mark.parametrize("d", [16, 32, 64, 128])
+def test_delta_step(d):
+    x = delta_inputs(40, 7, 1, d, torch.bfloat16, seed=d)
+    S = x["S"].clone()
+    o = kata.delta_decode_step(*(x[n][:, :, 0].contiguous() for n in ("q", "k", "v", "g", "beta")), S)
+    kata.sync_status()
+    want = delta_forward(x["q"], x["k"], x["v"], x["g"], x["beta"], d**-0.5, x["S"])[0]
+    check(o, want[:, :, 0])
