@@ -26,7 +26,8 @@
 // product: every other 8 columns, so that the two halves of a triangular one
 // have equal work). Products that share an operand go together. What dbeta and dg
 // are made of is in two tf32 parts (mma_tf32.cuh); what only dQ and dK are made of
-// is in one for bf16 inputs, whose results are rounded to 8 bits next.
+// (PM, PN, E, dS) is in two bf16 parts, 16 bits, for bf16 inputs, whose results are rounded
+// to 8 bits next.
 //
 // Measured on B200 at B2 H16 T4096 d64 bf16: delta_prep 91 us, delta_walks 151,
 // delta_grad 185 (ncu: issue 52 %, tensor 38 %, shared memory 51 %, 16 warps per SM,
@@ -226,9 +227,12 @@ __global__ void __launch_bounds__(256, D <= 64 ? 2 : 1) delta_grad(Args p, Grads
                 mma_step<2, 2, 1, 1>(*reinterpret_cast<float(*)[1][4]>(&dr[nt]), az, b);
             }
         }
-        gemm<TI, TI, ND>(
-            dl, 0, SL / 16, [&](int m, int k) { return quad<true>(sE + m0 * SS, SS, m, k); },
-            [&](int n, int k) { return quad<true>(sDS + d0 * SS, SS, n, k); });
+        auto erows = [&](int m, int k) { return quad<true>(sE + m0 * SS, SS, m, k); };
+        auto srows = [&](int n, int k) { return quad<true>(sDS + d0 * SS, SS, n, k); };
+        if constexpr (TI == 1)
+            gemm_parts<2, ND>(dl, 0, SL / 16, erows, srows);
+        else
+            gemm<2, 2, ND>(dl, 0, SL / 16, erows, srows);
         Tin *dv = static_cast<Tin *>(gr_.dv);
         for (int i = tid; i < kC * SL / 2; i += 256) {
             const int r = i / (SL / 2), c = 2 * (i % (SL / 2));
@@ -307,23 +311,43 @@ __global__ void __launch_bounds__(256, D <= 64 ? 2 : 1) delta_grad(Args p, Grads
 #pragma unroll 1
     for (int ks = 0; ks < nt_end; ++ks) {  // PM and PN against K
         const int k = 16 * ks + t2;
-        FragA<TI> am[1], an[1];
-        am[0].set(quad<true>(sM + m0 * kTS, kTS, gr, k), quad<true>(sM + m0 * kTS, kTS, gr + 8, k));
-        an[0].set(quad<true>(sN + m0 * kTS, kTS, gr, k), quad<true>(sN + m0 * kTS, kTS, gr + 8, k));
+        const float4 mt = quad<true>(sM + m0 * kTS, kTS, gr, k), mb = quad<true>(sM + m0 * kTS, kTS, gr + 8, k);
+        const float4 nt_ = quad<true>(sN + m0 * kTS, kTS, gr, k), nb = quad<true>(sN + m0 * kTS, kTS, gr + 8, k);
+        if constexpr (TI == 1) {
+            PartsA<2> am, an;
+            am.set(mt, mb);
+            an.set(nt_, nb);
 #pragma unroll
-        for (int nt = 0; nt < ND; ++nt) {
-            FragB<TI> b[1][1];
-            b[0][0].set(quad<false>(sK + d0, KS, 8 * nt + gr, k));
-            mma_step<TI, TI, 1, 1>(*reinterpret_cast<float(*)[1][4]>(&dq[nt]), am, b);
-            mma_step<TI, TI, 1, 1>(*reinterpret_cast<float(*)[1][4]>(&dr[nt]), an, b);
+            for (int nt = 0; nt < ND; ++nt) {
+                PartsB<1> b[1];
+                b[0].set(pair<false>(sK + d0, KS, 8 * nt + gr, k));
+                mma_parts<1, 1>(*reinterpret_cast<float(*)[1][4]>(&dq[nt]), am, b);
+                mma_parts<1, 1>(*reinterpret_cast<float(*)[1][4]>(&dr[nt]), an, b);
+            }
+        } else {
+            FragA<2> am[1], an[1];
+            am[0].set(mt, mb);
+            an[0].set(nt_, nb);
+#pragma unroll
+            for (int nt = 0; nt < ND; ++nt) {
+                FragB<2> b[1][1];
+                b[0][0].set(quad<false>(sK + d0, KS, 8 * nt + gr, k));
+                mma_step<2, 2, 1, 1>(*reinterpret_cast<float(*)[1][4]>(&dq[nt]), am, b);
+                mma_step<2, 2, 1, 1>(*reinterpret_cast<float(*)[1][4]>(&dr[nt]), an, b);
+            }
         }
     }
-    gemm<TI, TI, ND>(
-        dr, rb, 4, [&](int m, int k) { return quad<false>(sM + m0, kTS, m, k); },
-        [&](int n, int k) { return quad<false>(sQ + d0, KS, n, k); });
-    gemm<TI, TI, ND>(
-        dr, rb, 4, [&](int m, int k) { return quad<false>(sN + m0, kTS, m, k); },
-        [&](int n, int k) { return quad<false>(sK + d0, KS, n, k); });
+    auto mcols = [&](int m, int k) { return quad<false>(sM + m0, kTS, m, k); };
+    auto ncols = [&](int m, int k) { return quad<false>(sN + m0, kTS, m, k); };
+    if constexpr (TI == 1) {
+        gemm_parts<1, ND>(dr, rb, 4, mcols,
+                          [&](int n, int k) { return pair<false>(sQ + d0, KS, n, k); });
+        gemm_parts<1, ND>(dr, rb, 4, ncols,
+                          [&](int n, int k) { return pair<false>(sK + d0, KS, n, k); });
+    } else {
+        gemm<2, 2, ND>(dr, rb, 4, mcols, [&](int n, int k) { return quad<false>(sQ + d0, KS, n, k); });
+        gemm<2, 2, ND>(dr, rb, 4, ncols, [&](int n, int k) { return quad<false>(sK + d0, KS, n, k); });
+    }
 #pragma unroll
     for (int nt = 0; nt < ND; ++nt)
 #pragma unroll

@@ -28,7 +28,7 @@ import pytest
 import torch
 
 import kernelized_linear_attention_chunked_b200 as kata
-from _delta_ref import delta_forward, delta_inputs, prefill_grads, rel
+from _delta_ref import delta_forward, delta_grads, delta_inputs, prefill_grads, rel
 
 pytestmark = pytest.mark.gpu
 
@@ -72,6 +72,18 @@ def test_delta_prefill(B, H, T, d):
     o, _ = kata.delta_prefill(x["q"], x["k"], x["v"], x["g"], x["beta"], S_in=x["S"])
     kata.sync_status()
     check(o, delta_forward(x["q"], x["k"], x["v"], x["g"], x["beta"], d**-0.5, x["S"])[0])
+
+
+@pytest.mark.parametrize("d", [16, 32, 64, 128])
+@pytest.mark.parametrize("B,H,T", [(2, 3, 63), (2, 3, 200), (1, 2, 500)])
+def test_delta_gradients(B, H, T, d):
+    x = delta_inputs(B, H, T, d, torch.bfloat16, seed=T + d)
+    got = kata.delta_backward(x["q"], x["k"], x["v"], x["g"], x["beta"], x["do"], S_in=x["S"],
+                              dS=x["dS"])
+    kata.sync_status()
+    want = delta_grads(x["q"], x["k"], x["v"], x["g"], x["beta"], d**-0.5, x["do"], x["S"], x["dS"])
+    for name, a, b in zip(("dq", "dk", "dv"), got, want):
+        check(a, b, name)
 
 
 @pytest.mark.parametrize("d", [16, 32, 64, 128])
