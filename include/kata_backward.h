@@ -22,7 +22,8 @@ KATA_API size_t kata_prefill_backward_workspace_bytes(int B, int H, int T, int d
  *   q, k, v      [B, H, T, d], dtype KATA_F32 or KATA_BF16; d 16, 32 or 64;
  *                T any positive number (no multiple is asked for).
  *   d_o          [B, H, T, d] gradient of o, in the dtype of q.
- *   dq, dk, dv   [B, H, T, d], dtype of q; must not overlap the inputs.
+ *   dq, dk, dv   [B, H, T, d], dtype of q. Outputs or a workspace that overlap
+ *                each other or an input are refused.
  *   workspace    device scratch of at least
  *                kata_prefill_backward_workspace_bytes(); calls that may run
  *                at the same time need one each.

@@ -42,13 +42,13 @@ KATA_API size_t kata_delta_prefill_workspace_bytes(int B, int H, int T, int d, i
  *   q, k, v   [B, H, T, d], dtype KATA_F32 or KATA_BF16.
  *   g, beta   [B, H, T] fp32.
  *   S_in      [B, H, d, d] first state; NULL = zero.
- *   o         [B, H, T, d], dtype of q; NULL: not computed. Must not
- *             overwrite q, k or v.
+ *   o         [B, H, T, d], dtype of q; NULL: not computed.
  *   S_out     [B, H, d, d] last state; NULL: not written; may be S_in. One of
  *             o and S_out at least.
  *   workspace device scratch of at least
  *             kata_delta_prefill_workspace_bytes(); calls that may run at the
  *             same time need one each.
+ * Buffers that overlap otherwise are refused.
  */
 KATA_API int kata_delta_prefill(const void *q, const void *k, const void *v, int dtype,
                                 const float *g, const float *beta, int B, int H, int T, int d,
@@ -58,7 +58,8 @@ KATA_API int kata_delta_prefill(const void *q, const void *k, const void *v, int
 /*
  * One token per (b, h): the state is updated IN PLACE, then read out.
  *   q, k, v  [B, H, d]; g, beta [B, H] fp32; S [B, H, d, d] fp32, read and
- *   written; o [B, H, d], dtype of q; must not overwrite q, k or v.
+ *   written; o [B, H, d], dtype of q. S and o that overlap each other or
+ *   another buffer are refused.
  */
 KATA_API int kata_delta_decode_step(const void *q, const void *k, const void *v, int dtype,
                                     const float *g, const float *beta, int B, int H, int d,
@@ -76,7 +77,7 @@ KATA_API size_t kata_delta_backward_workspace_bytes(int B, int H, int T, int d, 
  *   dq, dk, dv  [B, H, T, d], dtype of q; dg, dbeta [B, H, T] fp32.
  *   dS_in     [B, H, d, d] fp32 gradient of the first state; NULL: not
  *             written; may be dS_out.
- * The outputs must not overlap the inputs otherwise. Deterministic. The
+ * Buffers that overlap otherwise are refused. Deterministic. The
  * gradient of a g below -200 is that of -200 (0 to fp32 rounding of its
  * neighbours).
  */

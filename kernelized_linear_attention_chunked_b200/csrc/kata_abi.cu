@@ -102,6 +102,46 @@ int check_common(int dtype, int B, int H, int d) {
     return KATA_OK;
 }
 
+// A buffer of a call; NULL: not given. `over`: an input that an output may be.
+struct Buffer {
+    const char *name;
+    const void *p;
+    size_t bytes;
+    const void *over = nullptr;
+};
+
+int check_apart(const Buffer &out, const Buffer &b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(out.p), y = reinterpret_cast<uintptr_t>(b.p);
+    if (!x || !y || x >= y + b.bytes || y >= x + out.bytes || (x == y && out.over == b.p)) return KATA_OK;
+    return fail(KATA_ERR_INVALID_ARG, "%s must not overwrite %s", out.name, b.name);
+}
+
+// No output may overlap an input: one CTA would read what another has written.
+template <size_t NO, size_t NI>
+int check_outputs(const Buffer (&outs)[NO], const Buffer (&ins)[NI]) {
+    for (const Buffer &o : outs)
+        for (const Buffer &i : ins)
+            if (int st = check_apart(o, i)) return st;
+    return KATA_OK;
+}
+
+// Nor another output, and the workspace nothing at all.
+template <size_t NO, size_t NI>
+int check_scratch(const Buffer (&outs)[NO], const Buffer (&ins)[NI], const Buffer &workspace) {
+    for (size_t i = 0; i < NO; ++i) {
+        for (size_t j = 0; j < i; ++j)
+            if (int st = check_apart({outs[i].name, outs[i].p, outs[i].bytes}, outs[j])) return st;
+        if (int st = check_apart(workspace, outs[i])) return st;
+    }
+    for (const Buffer &i : ins)
+        if (int st = check_apart(workspace, i)) return st;
+    return KATA_OK;
+}
+
+size_t token_bytes(int dtype, int B, int H, int T, int d) {
+    return (size_t)B * H * T * d * (dtype == KATA_F32 ? 4 : 2);
+}
+
 #define KATA_REQUIRE_PTR(p)                                                        \
     do {                                                                           \
         if (!(p)) return fail(KATA_ERR_INVALID_ARG, "%s must not be NULL", #p);    \
@@ -854,14 +894,6 @@ static int check_delta_seq(int dtype, int B, int H, int T, int d, float scale) {
             return fail(KATA_ERR_INVALID_ARG, "%s is not 4-byte aligned", #p);     \
     } while (0)
 
-// An output that starts where an input does would be read by one CTA after
-// another has written it.
-#define KATA_NO_ALIAS(out, in)                                                     \
-    do {                                                                           \
-        if ((out) && (const void *)(out) == (const void *)(in))                    \
-            return fail(KATA_ERR_INVALID_ARG, "%s must not overwrite %s", #out, #in); \
-    } while (0)
-
 size_t kata_delta_prefill_workspace_bytes(int B, int H, int T, int d, int dtype) {
     if (check_delta_seq(dtype, B, H, T, d, 1.f)) return 0;
     return kata::delta_prefill_workspace_bytes((long)B * H, T, d);
@@ -883,13 +915,15 @@ int kata_delta_prefill(const void *q, const void *k, const void *v, int dtype, c
     KATA_OPTIONAL_PTR(o);
     KATA_OPTIONAL_PTR(S_out);
     if (!o && !S_out) return fail(KATA_ERR_INVALID_ARG, "o and S_out: at least one");
-    KATA_NO_ALIAS(o, q);
-    KATA_NO_ALIAS(o, k);
-    KATA_NO_ALIAS(o, v);
+    const size_t x = token_bytes(dtype, B, H, T, d), y = (size_t)B * H * T * 4, z = (size_t)B * H * d * d * 4;
+    const Buffer ins[] = {{"q", q, x}, {"k", k, x}, {"v", v, x}, {"g", g, y}, {"beta", beta, y}, {"S_in", S_in, z}};
+    const Buffer outs[] = {{"o", o, x}, {"S_out", S_out, z, S_in}};
+    if ((st = check_outputs(outs, ins))) return st;
     const size_t need = kata::delta_prefill_workspace_bytes((long)B * H, T, d);
     if (ws_bytes < need || !workspace)
         return fail(KATA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, need);
     KATA_REQUIRE_PTR(workspace);
+    if ((st = check_scratch(outs, ins, {"workspace", workspace, need}))) return st;
     kata::DeltaArgs a{q, k, v, dtype, g, beta, (long)B * H, T, d, scale, S_in, o, S_out, workspace};
     cudaError_t e = kata::delta_prefill(a, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "kata_delta_prefill launch");
@@ -909,9 +943,10 @@ int kata_delta_decode_step(const void *q, const void *k, const void *v, int dtyp
     KATA_REQUIRE_F32(beta);
     KATA_REQUIRE_PTR(S);
     KATA_REQUIRE_PTR(o);
-    KATA_NO_ALIAS(o, q);
-    KATA_NO_ALIAS(o, k);
-    KATA_NO_ALIAS(o, v);
+    const size_t x = token_bytes(dtype, B, H, 1, d), y = (size_t)B * H * 4, z = (size_t)B * H * d * d * 4;
+    const Buffer ins[] = {{"q", q, x}, {"k", k, x}, {"v", v, x}, {"g", g, y}, {"beta", beta, y}};
+    const Buffer outs[] = {{"S", S, z}, {"o", o, x}};
+    if ((st = check_outputs(outs, ins)) || (st = check_apart(outs[1], outs[0]))) return st;
     cudaError_t e = kata::delta_decode_step(q, k, v, dtype, g, beta, (long)B * H, d, scale, S, o,
                                             static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "kata_delta_decode_step launch");
@@ -945,10 +980,17 @@ int kata_delta_backward(const void *q, const void *k, const void *v, int dtype, 
     KATA_REQUIRE_F32(dg);
     KATA_REQUIRE_F32(dbeta);
     KATA_OPTIONAL_PTR(dS_in);
+    const size_t x = token_bytes(dtype, B, H, T, d), y = (size_t)B * H * T * 4, z = (size_t)B * H * d * d * 4;
+    const Buffer ins[] = {{"q", q, x},       {"k", k, x},       {"v", v, x},     {"g", g, y},
+                          {"beta", beta, y}, {"S_in", S_in, z}, {"d_o", d_o, x}, {"dS_out", dS_out, z}};
+    const Buffer outs[] = {{"dq", dq, x}, {"dk", dk, x},       {"dv", dv, x},
+                           {"dg", dg, y}, {"dbeta", dbeta, y}, {"dS_in", dS_in, z, dS_out}};
+    if ((st = check_outputs(outs, ins))) return st;
     const size_t need = kata::delta_backward_workspace_bytes((long)B * H, T, d);
     if (ws_bytes < need || !workspace)
         return fail(KATA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, need);
     KATA_REQUIRE_PTR(workspace);
+    if ((st = check_scratch(outs, ins, {"workspace", workspace, need}))) return st;
     kata::DeltaArgs a{q, k, v, dtype, g, beta, (long)B * H, T, d, scale, S_in, nullptr, nullptr,
                       workspace};
     kata::DeltaGrads gr{d_o, dS_out, dq, dk, dv, dg, dbeta, dS_in};
@@ -987,10 +1029,15 @@ int kata_prefill_backward(const void *q, const void *k, const void *v, int dtype
     KATA_REQUIRE_PTR(dq);
     KATA_REQUIRE_PTR(dk);
     KATA_REQUIRE_PTR(dv);
+    const size_t x = token_bytes(dtype, B, H, T, d);
+    const Buffer ins[] = {{"q", q, x}, {"k", k, x}, {"v", v, x}, {"d_o", d_o, x}};
+    const Buffer outs[] = {{"dq", dq, x}, {"dk", dk, x}, {"dv", dv, x}};
+    if ((st = check_outputs(outs, ins))) return st;
     const size_t need = kata::prefill_backward_workspace_bytes(dtype, (long)B * H, T);
     if (ws_bytes < need || !workspace)
         return fail(KATA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, need);
     KATA_REQUIRE_PTR(workspace);
+    if ((st = check_scratch(outs, ins, {"workspace", workspace, need}))) return st;
     unsigned int *err = error_word();
     if (!err) return fail(KATA_ERR_CUDA, "error word unavailable");
     kata::PrefillBackwardArgs a{q,   k,  v,  d_o, dtype,     (long)B * H, T,
