@@ -27,9 +27,11 @@ KATA_API size_t kata_prefill_backward_workspace_bytes(int B, int H, int T, int d
  *   workspace    device scratch of at least
  *                kata_prefill_backward_workspace_bytes(); calls that may run
  *                at the same time need one each.
- * Deterministic. Inputs are expected finite, up to the last token: a NaN or an
- * infinity reaches the whole 64- or 128-token tile it lies in. A row whose denominator is zero (eps = 0 and every score 0)
- * has no defined output; its gradients are taken as 0.
+ * Deterministic. Inputs are expected finite, up to the last token, and so are the
+ * scores' squares in fp32: a NaN or an infinity reaches the whole 64- or 128-token
+ * tile it lies in. A row whose denominator is below 2^-126, fp32's smallest normal
+ * number (eps = 0, and every score next to 0), has no defined output; its
+ * gradients are taken as 0.
  */
 KATA_API int kata_prefill_backward(const void *q, const void *k, const void *v, int dtype, int B,
                                    int H, int T, int d, float eps, const void *d_o, void *dq,

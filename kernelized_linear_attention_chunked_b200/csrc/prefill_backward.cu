@@ -31,6 +31,8 @@
 // five products per causal pair, of which nine are run in three tf32 parts (116 TFLOP/s of
 // 288 in tf32). Bound by issue (49 %), the tensor pipe (47 %) and the steps' dependent
 // parts (8 warps per SM).
+#include <float.h>
+
 #include "delta.cuh"
 
 namespace kata {
@@ -330,8 +332,9 @@ __global__ void __launch_bounds__(BwdCfg<D, ROWS>::THREADS) bwd_query(Args p) {
                 d += peer_f64(cl.at(sum + i, r));
                 n += peer_f64(cl.at(sum + ROWS + i, r));
             }
-            const double delta = d == 0.0 ? 0.0 : n / d;
-            inv2[h] = d == 0.0 ? 0.f : (float)(2.0 / d);
+            const bool none = d < (double)FLT_MIN;  // below it 2 / d may be infinite in fp32
+            const double delta = none ? 0.0 : n / d;
+            inv2[h] = none ? 0.f : (float)(2.0 / d);
             dhi[h] = (float)delta;
             dlo[h] = (float)(delta - (double)dhi[h]);
             if (cl.rank == 0 && quarter == 0 && (lane & 3) == 0 && q0 + i < p.T)

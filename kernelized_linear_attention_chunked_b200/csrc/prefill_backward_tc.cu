@@ -40,6 +40,8 @@
 // from shared memory (1700 of the 4000 cycles that a buffer is in use), and for the
 // queries the single threads that issue the products (66 cycles per MMA against 48
 // for the operands' shared-memory reads).
+#include <float.h>
+
 #include "kata_internal.h"
 #include "tc_tiles.cuh"
 
@@ -391,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 den += red[g * 256 + i];
                 num += red[g * 256 + 128 + i];
             }
-            if (den != 0.0) {
+            if (!(den < (double)FLT_MIN)) {  // below it 1 / den may be infinite in fp32
                 const double minus = -num / den;
                 inv = (float)(1.0 / den);
                 dhi = (float)minus;
