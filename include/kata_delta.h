@@ -18,7 +18,8 @@
  *   S_t = exp(g_t) S_{t-1} + beta_t k_t e_t^T
  *   o_t = scale S_t^T q_t
  * g_t is the log of the decay, <= 0 in use (values below -200 count as -200:
- * exp of either is 0 in fp32; minus infinity starts the state anew); beta_t is
+ * exp of either is 0 in fp32; minus infinity starts the state anew, from values
+ * that are finite themselves: 0 times an infinity or a NaN is a NaN); beta_t is
  * the writing strength. Keys are used as given: callers that want unit keys
  * normalise them. A token with beta = 0 and g = 0 leaves the state as it is,
  * so shorter sequences of a padded batch are padded with such tokens (with
@@ -34,7 +35,8 @@
 extern "C" {
 #endif
 
-/* Device workspace bytes kata_delta_prefill needs (0: invalid sizes). */
+/* Device workspace bytes kata_delta_prefill needs (0: invalid sizes): 4 (128 d +
+ * 4352) for each 64 tokens of a head, 50 KB at d = 64. */
 KATA_API size_t kata_delta_prefill_workspace_bytes(int B, int H, int T, int d, int dtype);
 
 /*
@@ -65,7 +67,9 @@ KATA_API int kata_delta_decode_step(const void *q, const void *k, const void *v,
                                     const float *g, const float *beta, int B, int H, int d,
                                     float scale, float *S, void *o, void *stream);
 
-/* Device workspace bytes kata_delta_backward needs (0: invalid sizes). */
+/* Device workspace bytes kata_delta_backward needs (0: invalid sizes): 8 (192 d +
+ * d d + 256) for each 64 tokens of a head, 133 KB at d = 64 and 330 KB at d = 128
+ * (1.1 GB for B = 2, H = 16, T = 16384, d = 64). */
 KATA_API size_t kata_delta_backward_workspace_bytes(int B, int H, int T, int d, int dtype);
 
 /*

@@ -2,7 +2,9 @@
 the LoLA self-recall-error sparse cache on NVIDIA B200 (sm_100a).
 
 Beside them the gated delta rule (delta_prefill, delta_decode_step,
-delta_backward) and the gradients of the prefill (prefill_backward).
+delta_backward) and the gradients of the prefill (prefill_backward). No call
+records an autograd graph: a training loop pairs each forward call with its
+gradients itself, in an autograd function of its own.
 
 The computation lives in libkata.so (C ABI: include/kata.h, kata_delta.h,
 kata_backward.h); this package is its thin Python binding plus the seeded

@@ -58,7 +58,8 @@ def _inputs(q, k, v, do):
 
 def prefill_backward(q, k, v, do, eps: float = 1e-6, workspace=None, stream=None):
     """Gradients (dq, dk, dv) of prefill's output from a zero state, for the
-    output's gradient ``do``. All [B, H, T, d] in q's dtype; any T."""
+    output's gradient ``do``. All [B, H, T, d] in q's dtype; any T. (prefill's own
+    output is fp32 for bf16 inputs as well: its gradient has to be cast.)"""
     dt, shape = _inputs(q, k, v, do)
     B, H, T, d = shape
     if workspace is not None:

@@ -27,6 +27,7 @@ SIGNATURES = {
                                  _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
 }
 
+
 def lib() -> C.CDLL:
     """libkata.so with this header's entry points; raises if it has not been built."""
     return bind(SIGNATURES)
@@ -74,8 +75,9 @@ def delta_prefill(q, k, v, g, beta, scale: float | None = None, S_in=None, state
     """The gated delta rule over q, k, v [B, H, T, d] with log decays g and
     writing strengths beta [B, H, T] (fp32), from the state S_in [B, H, d, d]
     (fp32, None: zero). ``scale`` defaults to d**-0.5. Returns (o, S): o in q's
-    dtype, None when ``output`` is False; the last state, None when ``state``
-    is False."""
+    dtype, None when ``output`` is False and no buffer ``o`` is given; the last
+    state, None when ``state`` is False and no ``S_out`` is given (it may be
+    S_in). No autograd graph is recorded: delta_backward gives the gradients."""
     dt, shape = _inputs(q, k, v, g, beta, 4)
     B, H, T, d = shape
     st = (B, H, d, d)
@@ -105,7 +107,7 @@ def delta_prefill(q, k, v, g, beta, scale: float | None = None, S_in=None, state
 def delta_decode_step(q, k, v, g, beta, S, scale: float | None = None, o=None, stream=None):
     """One token of the gated delta rule: q, k, v [B, H, d], g and beta [B, H]
     (fp32), the state S [B, H, d, d] (fp32) updated in place. Returns o in q's
-    dtype."""
+    dtype. No autograd graph is recorded."""
     dt, shape = _inputs(q, k, v, g, beta, 3)
     B, H, d = shape
     if S is None:

@@ -2,8 +2,8 @@
 
 Each .cu file under csrc/ is compiled to an object in _build/ (in parallel),
 then linked into kernelized_linear_attention_chunked_b200/libkata.so with the
-static CUDA runtime. Only the extern "C" entry points of include/kata.h are
-exported. build(debug=True) compiles the same sources with -DKATA_DEBUG (the
+static CUDA runtime. Only the extern "C" entry points of the headers under
+include/ are exported. build(debug=True) compiles the same sources with -DKATA_DEBUG (the
 device-side bounds checks) into _build_debug/ and libkata_debug.so.
 """
 from __future__ import annotations

@@ -35,12 +35,12 @@
 // which has the same shape: Z = Z0 + W' dS with W' = X^T diag(beta c) K and
 // Z0 = scale X^T diag(beta) M^T dO.
 //
-// Measured on B200 (bf16; both launches): B2 H16 T16384 d64 174 + 310 us, B4 H8 T2048
-// d32 19 + 31, B3 H5 T1531 d128 20 + 63. ncu at B2 H16 T4096 d64: delta_prep 59 % of
-// issue slots, tensor pipe 37 %, shared memory 63 %, its CTAs a sequence of short
-// dependent steps (32 warps per SM); delta_chain 128 CTAs of 148 SMs, 2200 cycles per
-// chunk, of which its critical products take 640: issue 35 %, tensor 38 %, shared
-// memory 68 %.
+// Measured on B200 (bf16; both launches, each by itself under ncu): B2 H16 T16384 d64
+// 186 + 325 us (485 a call), B4 H8 T2048 d32 21 + 30, B3 H5 T1531 d128 23 + 60. ncu at
+// B2 H16 T4096 d64: delta_prep 60 % of issue slots, tensor pipe 37 %, shared memory 62 %,
+// its CTAs a sequence of short dependent steps (32 warps per SM); delta_chain 128 CTAs of
+// 148 SMs, about 2200 cycles per chunk, of which its critical products take 640: issue
+// 41 %, tensor 40 %, shared memory 62 %.
 //
 // All products keep fp32 accuracy by split tf32 operands (mma_tf32.cuh): the
 // state, its gradient, dg and dbeta are fp32 results. Only Q S0 and M E of bf16 inputs,

@@ -29,8 +29,8 @@
 // (PM, PN, E, dS) is in two bf16 parts, 16 bits, for bf16 inputs, whose results are rounded
 // to 8 bits next.
 //
-// Measured on B200 at B2 H16 T4096 d64 bf16: delta_prep 91 us, delta_walks 151,
-// delta_grad 185 (ncu: issue 52 %, tensor 38 %, shared memory 51 %, 16 warps per SM,
+// Measured on B200 at B2 H16 T4096 d64 bf16, each by itself under ncu: delta_prep 93 us,
+// delta_walks 150, delta_grad 196 (issue 52 %, tensor 38 %, shared memory 49 %, 16 warps per SM,
 // their registers and 101 KB of shared memory per CTA in the way of more). Its two-way
 // bank conflicts (transposed reads of fp32 tiles, a third of its wavefronts) cost
 // nothing: without them it took as long.

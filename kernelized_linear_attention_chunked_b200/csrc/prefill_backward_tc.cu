@@ -15,9 +15,10 @@
 // Tensor memory (512 columns, one CTA per SM): three buffers of S (64 fp32
 // columns) and dP (64), then the accumulators. The workers overwrite S with P
 // and dP with dS as bf16 pairs, in place, sixteen columns with eight of upper parts and
-// eight of lower ones, and the output products take them from there as A operands. A streamed tile serves both products it is needed
-// in: [64 rows, d] in rows of 2 d bytes, swizzled by that width, is a K-major
-// operand for the scores and an MN-major one for the outputs.
+// eight of lower ones, and the output products take them from there as A operands. A
+// streamed tile serves both products it is needed in: [64 rows, d] in rows of 2 d bytes,
+// swizzled by that width, is a K-major operand for the scores and an MN-major one for the
+// outputs.
 //
 // Warp roles: two sets of workers on alternate steps, each two groups of four
 // warps with half the step's columns (thread = row), two issuers of the score products (alternate steps: one
@@ -28,18 +29,19 @@
 // parts each (16 bits), so that the gradients are off by little more than their last
 // rounding, 1.66e-3 of their norm. With one part dV was off by 2.3e-3, and dQ and dK, whose
 // terms cancel, by up to 3.1e-3 (the second part of P costs 6 % of the time, that of dS
-// 12 %). The
-// rows of the first 128 queries sum den and delta in 64 bits, and delta is two
+// 12 %). The rows of the first 128 queries sum den and delta in 64 bits, and delta is two
 // floats: with few keys dP - delta is a small difference. It stays exact because
 // S and dP come out of the same products with the same bits in both modes and
 // both walks.
 //
 // Measured on B200 at B2 H8 T8192 d64 (344 GFLOP as five products per causal
-// pair; twelve are run: six in either mode, P and dS counting twice): queries 482 us, keys 415 us, 383 TFLOP/s of the
-// five. What bounds it: the keys' workers, which read two statistics per column
-// from shared memory (1700 of the 4000 cycles that a buffer is in use), and for the
-// queries the single threads that issue the products (66 cycles per MMA against 48
-// for the operands' shared-memory reads).
+// pair; twelve are run: six in either mode, P and dS counting twice): 987 to 1029 us a call
+// (power), 334 to 348 TFLOP/s of the five; queries 534 us, keys 503 us by themselves under ncu. At T4096 ncu
+// shows the tensor pipe at 36 % (queries) and 38 % (keys) of its cycles, issue at 56 and
+// 63 %, shared memory at 42 and 53 %. What bounds it: the steps' hand-offs, the keys'
+// workers, which read two statistics per column from shared memory and cut P and dS
+// (without P's second part they took 451 us), and for the queries the single threads that
+// issue the products (66 cycles per MMA against 48 for the operands' shared-memory reads).
 #include <float.h>
 
 #include "kata_internal.h"
