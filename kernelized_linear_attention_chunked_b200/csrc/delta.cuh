@@ -469,6 +469,7 @@ struct ChainSmem {
     // the state in two parts; the chunk's errors whole, or in three bf16 parts
     static constexpr int S = 0, YC = S + D / 16 * 2 * FRAG, SIDE = YC + kC / 16 * 3 * FRAG / 2;
     // what passes between the chain and the side warps: E or (REV) Q^T diag(scale a) dO
+    // forward, bf16 inputs: the state in two bf16 parts, for the outputs
     static constexpr int SB = SIDE + (REV ? D / 16 * FRAG : kC / 16 * tf::Parts<Tin>::N * FRAG);
     static constexpr int STAGE = SB + (REV || sizeof(Tin) == 4 ? 0 : D / 16 * FRAG);
     // one stage: K, Q, coefficients, (REV) the dO slice
